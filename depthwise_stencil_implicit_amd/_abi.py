@@ -70,6 +70,30 @@ class ConvPlanOpts(ctypes.Structure):
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmiconv.so")
 
+# The sequence operators (include/miconv_lm.h).
+LM_I32, LM_U8 = 16, 17
+LM_CONV, LM_CONV_BWD, LM_CONV_STEP, LM_SCAN, LM_SCAN_BWD, LM_SCAN_STEP, LM_MV4 = range(7)
+LM_SLOTS = ("X", "W", "BIAS", "Y", "STATE_IN", "STATE_OUT", "OFFSETS", "GY", "GSTATE", "DX", "DW", "DBIAS", "DSTATE",
+            "DT", "A", "B", "C", "D", "Z", "DT_BIAS", "DDT", "DA", "DB", "DC", "DD", "DZ", "DDT_BIAS", "SAVED", "ROWS",
+            "SCALES", "ZEROS")
+LM_NSLOT = len(LM_SLOTS)
+LM_SILU, LM_SOFTPLUS = 1, 2
+
+
+class LmArgs(ctypes.Structure):
+    _fields_ = [("flags", _i32), ("reserved", _i32), ("max_len", _i64), ("chunk", _i64)]
+
+
+class LmPlan(ctypes.Structure):
+    _fields_ = [("op", _i32), ("dtype", _i32), ("args", LmArgs), ("t", ConvTensor * LM_NSLOT),
+                ("seqs", _i64), ("C", _i64), ("L", _i64), ("K", _i64), ("S", _i64), ("G", _i64),
+                ("chunk", _i64), ("chunks", _i64), ("saved_floats", _i64), ("workspace_bytes", _i64),
+                ("flops", _i64), ("bytes", _i64)]
+
+
+# Every symbol include/miconv_lm.h declares.
+LM_EXPORTS = ("lm_plan", "lm_run")
+
 # Every symbol include/miconv.h declares.
 EXPORTS = ("conv_bind", "conv_out_shape", "conv_plan", "conv_plan_ex", "conv_run", "conv_run_noalloc",
            "conv_backward_layout", "conv_plan_backward", "conv_run_backward",
@@ -124,5 +148,9 @@ def lib():
         L.conv_status_string.restype = ctypes.c_char_p
         L.conv_abi_version.argtypes = []
         L.conv_abi_version.restype = _i32
+        L.lm_plan.argtypes = [_i32, P(ConvTensor), P(LmArgs), P(LmPlan), ctypes.c_char_p, ctypes.c_size_t]
+        L.lm_plan.restype = ctypes.c_int
+        L.lm_run.argtypes = [P(LmPlan), P(ctypes.c_void_p), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.lm_run.restype = ctypes.c_int
         _lib = L
     return _lib

@@ -1,0 +1,480 @@
+// The short causal convolution of a sequence, its gradients and its step for
+// single tokens:
+//   p[c,t] = b[c] + sum_{k<K} w[c,k] xx[c, t-K+1+k],   y = act(p),
+// xx the rows of x behind the K-1 values of the incoming state.
+//
+// Bound by memory: 2 K + 4 operations for 2 elements moved.  A thread owns V
+// neighbouring channels and walks down a chunk of rows with the last K-1 rows,
+// the weights and the bias in registers, so x is read once but for the K-1
+// rows in front of each chunk.  Lanes lie along the channels: with channels
+// contiguous a wave reads and writes whole lines (V elements per lane, at any
+// element alignment); other strides take V = 1.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "lm_dev.h"
+#include "lm_internal.h"
+
+namespace miconv {
+namespace {
+
+constexpr int kRowsAhead = 4;   // rows whose loads are in flight while the previous ones are used
+
+struct ConvP {
+    const void *x, *w, *b, *s0, *gy, *gs;
+    void *y, *s1, *dx, *ds;
+    float *part;
+    const int32_t *off, *rows;
+    S3 xs, ys, s0s, s1s, gys, gss, dxs, dss;
+    int64_t ws_c, ws_k, bs;
+    int64_t seqs, C, L, chunk, chunks, cvs, state_rows;
+    int silu, w_dense;
+};
+
+// Thread -> (sequence, chunk, first channel).  Neighbouring threads take
+// neighbouring channels; the last group of V is moved back inside C and
+// repeats its neighbour's results.
+template <int V> __device__ __forceinline__ bool conv_item(const ConvP &p, int64_t &seq, int64_t &ch, int64_t &c)
+{
+    const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (item >= p.cvs * p.chunks * p.seqs) return false;
+    const int64_t r = item / p.cvs;
+    c = (item - r * p.cvs) * V;
+    if (c > p.C - V) c = p.C - V;
+    seq = r / p.chunks;
+    ch = r - seq * p.chunks;
+    return true;
+}
+
+template <typename T, int V> __device__ __forceinline__ void get(const T *p, int64_t cs, float (&o)[V])
+{
+    if constexpr (V == 1) o[0] = to_f32(*p);
+    else load_f32<T, V>(p, o);
+}
+template <typename T, int V> __device__ __forceinline__ void put(T *p, int64_t cs, const float (&v)[V])
+{
+    if constexpr (V == 1) *p = from_f32<T>(v[0]);
+    else store_f32<T, V>(p, v);
+}
+// V channels of one row at any channel stride (state rows, parameters).
+template <typename T, int V> __device__ __forceinline__ void get_strided(const T *p, int64_t cs, float (&o)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = to_f32(p[i * cs]);
+}
+template <typename T, int V> __device__ __forceinline__ void put_strided(T *p, int64_t cs, const float (&v)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i * cs] = from_f32<T>(v[i]);
+}
+
+template <typename T, int K, int V>
+__device__ __forceinline__ void get_weights(const ConvP &p, int64_t c, float (&w)[K][V], float (&b)[V])
+{
+    const T *wp = static_cast<const T *>(p.w) + c * p.ws_c;
+    if (p.w_dense) {   // [C, K] without gaps: V K neighbouring elements
+        float f[K * V];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            float v[V];
+            get<T, V>(wp + i * V, 1, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[i * V + j] = v[j];
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[k][i] = f[i * K + k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) get_strided<T, V>(wp + k * p.ws_k, p.ws_c, w[k]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = 0.f;
+    if (p.b) get_strided<T, V>(static_cast<const T *>(p.b) + c * p.bs, p.bs, b);
+}
+
+// Row t of the extended input (t >= -(K-1)): x, the incoming state, or zero.
+template <typename T, int K, int V>
+__device__ __forceinline__ void get_front(const ConvP &p, int64_t seq, const T *x, int64_t c, int64_t t, float (&o)[V])
+{
+    if (t >= 0) get<T, V>(x + t * p.xs.l, p.xs.c, o);
+    else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.f;
+        if (p.s0)
+            get_strided<T, V>(static_cast<const T *>(p.s0) + seq * p.s0s.n + c * p.s0s.c + (K - 1 + t) * p.s0s.l, p.s0s.c,
+                              o);
+    }
+}
+
+template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_fwd(const ConvP p)
+{
+    int64_t seq, ch, c;
+    if (!conv_item<V>(p, seq, ch, c)) return;
+    const SeqSpan sp = seq_span(p.off, seq, p.L);
+    const int64_t t0 = ch * p.chunk;
+    if (t0 >= sp.len && ch > 0) return;
+    const int64_t t1 = ch == p.chunks - 1 ? sp.len : (t0 + p.chunk < sp.len ? t0 + p.chunk : sp.len);
+    const T *x = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
+    T *y = static_cast<T *>(p.y) + sp.row0 * p.ys.n + c * p.ys.c + sp.start * p.ys.l;
+
+    float w[K][V], b[V];
+    get_weights<T, K, V>(p, c, w, b);
+    float h[K][V];   // h[0 .. K-2]: the rows in front, oldest first; h[K-1]: the current row
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) get_front<T, K, V>(p, seq, x, c, t0 - (K - 1) + k, h[k]);
+
+    Raw<T, V> next[kRowsAhead];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int r = 0; r < kRowsAhead; ++r)
+            if (t + r < t1) next[r] = load_raw<T, V>(x + (t + r) * p.xs.l);
+    };
+    fetch(t0);
+    for (int64_t t = t0; t < t1; t += kRowsAhead) {
+        Raw<T, V> cur[kRowsAhead];
+#pragma unroll
+        for (int r = 0; r < kRowsAhead; ++r) cur[r] = next[r];
+        fetch(t + kRowsAhead);
+#pragma unroll
+        for (int r = 0; r < kRowsAhead; ++r) {
+            if (t + r >= t1) break;
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                h[K - 1][i] = to_f32(cur[r].v[i]);
+                float a = b[i];
+#pragma unroll
+                for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[k][i], a);
+                o[i] = p.silu ? silu(a) : a;
+            }
+            put<T, V>(y + (t + r) * p.ys.l, p.ys.c, o);
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[k][i] = h[k + 1][i];
+        }
+    }
+    if (K > 1 && p.s1 && t1 == sp.len) {
+        T *s1 = static_cast<T *>(p.s1) + seq * p.s1s.n + c * p.s1s.c;
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) put_strided<T, V>(s1 + k * p.s1s.l, p.s1s.c, h[k]);
+    }
+}
+
+// One token for each batch row; the state row moves up by one in place.
+template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_step(const ConvP p)
+{
+    int64_t n, ch, c;
+    if (!conv_item<V>(p, n, ch, c)) return;
+    T *y = static_cast<T *>(p.y) + n * p.ys.n + c * p.ys.c;
+    int64_t row = n;
+    if (p.rows) {
+        row = p.rows[n];
+        if (row < 0 || row >= p.state_rows) {
+            const float zero[V] = {};
+            put_strided<T, V>(y, p.ys.c, zero);
+            return;
+        }
+    }
+    const T *x = static_cast<const T *>(p.x) + n * p.xs.n + c * p.xs.c;
+    T *st = static_cast<T *>(p.s1) + row * p.s1s.n + c * p.s1s.c;
+    float h[K][V], w[K][V], b[V], o[V];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+        if (p.s1s.c == 1) get<T, V>(st + k * p.s1s.l, 1, h[k]);
+        else get_strided<T, V>(st + k * p.s1s.l, p.s1s.c, h[k]);
+    }
+    if (p.xs.c == 1) get<T, V>(x, 1, h[K - 1]);
+    else get_strided<T, V>(x, p.xs.c, h[K - 1]);
+    get_weights<T, K, V>(p, c, w, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float a = b[i];
+#pragma unroll
+        for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[k][i], a);
+        o[i] = p.silu ? silu(a) : a;
+    }
+    if (p.ys.c == 1) put<T, V>(y, 1, o);
+    else put_strided<T, V>(y, p.ys.c, o);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+        if (p.s1s.c == 1) put<T, V>(st + k * p.s1s.l, 1, h[k + 1]);
+        else put_strided<T, V>(st + k * p.s1s.l, p.s1s.c, h[k + 1]);
+    }
+}
+
+// Gradients in one walk: at row r the pre-activation is recomputed from x,
+// g[r] = gy act'(p) joins a window of K rows, dx[r-K+1] leaves it, and dw, db
+// gather over the chunk's own rows.  The walk runs K-1 rows past the chunk for
+// dx's window (their dw belongs to the next chunk).  The sums of a chunk go to
+// part [seq * chunks + chunk][C][K+1]; conv_bwd_sums adds them in a fixed order.
+template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_bwd(const ConvP p)
+{
+    int64_t seq, ch, c;
+    if (!conv_item<V>(p, seq, ch, c)) return;
+    const SeqSpan sp = seq_span(p.off, seq, p.L);
+    const int64_t t0 = ch * p.chunk;
+    float dw[K][V] = {}, db[V] = {};
+    if (t0 < sp.len || ch == 0) {
+        const int64_t t1 = ch == p.chunks - 1 ? sp.len : (t0 + p.chunk < sp.len ? t0 + p.chunk : sp.len);
+        const T *x = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
+        const T *gy = static_cast<const T *>(p.gy) + sp.row0 * p.gys.n + c * p.gys.c + sp.start * p.gys.l;
+        T *dx = p.dx ? static_cast<T *>(p.dx) + sp.row0 * p.dxs.n + c * p.dxs.c + sp.start * p.dxs.l : nullptr;
+        float w[K][V], b[V];
+        get_weights<T, K, V>(p, c, w, b);
+        float h[K][V], g[K][V];   // g[k]: the gradient at row r - k
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) {
+            get_front<T, K, V>(p, seq, x, c, t0 - (K - 1) + k, h[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[k][i] = 0.f;
+        }
+        const int64_t end = t1 + (K - 1);                       // rows walked
+        const int64_t has = end < sp.len ? end : sp.len;        // rows that exist
+        Raw<T, V> nx[kRowsAhead], ng[kRowsAhead];
+        auto fetch = [&](int64_t t) {
+#pragma unroll
+            for (int r = 0; r < kRowsAhead; ++r)
+                if (t + r < has) {
+                    nx[r] = load_raw<T, V>(x + (t + r) * p.xs.l);
+                    ng[r] = load_raw<T, V>(gy + (t + r) * p.gys.l);
+                }
+        };
+        fetch(t0);
+        for (int64_t t = t0; t < end; t += kRowsAhead) {
+            Raw<T, V> cx[kRowsAhead], cg[kRowsAhead];
+#pragma unroll
+            for (int r = 0; r < kRowsAhead; ++r) cx[r] = nx[r], cg[r] = ng[r];
+            fetch(t + kRowsAhead);
+#pragma unroll
+            for (int r = 0; r < kRowsAhead; ++r) {
+                const int64_t row = t + r;
+                if (row >= end) break;
+#pragma unroll
+                for (int k = K - 1; k > 0; --k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) g[k][i] = g[k - 1][i];
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[0][i] = 0.f;
+                if (row < has) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        h[K - 1][i] = to_f32(cx[r].v[i]);
+                        float gi = to_f32(cg[r].v[i]);
+                        if (p.silu) {
+                            float a = b[i];
+#pragma unroll
+                            for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[k][i], a);
+                            gi *= silu_slope(a, sigmoid(a));
+                        }
+                        g[0][i] = gi;
+                    }
+                    if (row < t1) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            db[i] += g[0][i];
+#pragma unroll
+                            for (int k = 0; k < K; ++k) dw[k][i] = __builtin_fmaf(g[0][i], h[k][i], dw[k][i]);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) h[k][i] = h[k + 1][i];
+                }
+                const int64_t to = row - (K - 1);   // the row whose gradient is complete
+                if (to < t0 && !(ch == 0 && to < 0)) continue;
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    o[i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) o[i] = __builtin_fmaf(w[k][i], g[k][i], o[i]);
+                }
+                if (p.gs && to >= sp.len - (K - 1)) {
+                    float v[V];
+                    get_strided<T, V>(static_cast<const T *>(p.gs) + seq * p.gss.n + c * p.gss.c +
+                                          (to - (sp.len - (K - 1))) * p.gss.l,
+                                      p.gss.c, v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] += v[i];
+                }
+                if (to >= 0) {
+                    if (dx) put<T, V>(dx + to * p.dxs.l, p.dxs.c, o);
+                } else if (p.ds) {
+                    put_strided<T, V>(static_cast<T *>(p.ds) + seq * p.dss.n + c * p.dss.c + (K - 1 + to) * p.dss.l,
+                                      p.dss.c, o);
+                }
+            }
+        }
+    }
+    if (p.part) {
+        float *o = p.part + ((seq * p.chunks + ch) * p.C + c) * (K + 1);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) o[i * (K + 1) + k] = dw[k][i];
+            o[i * (K + 1) + K] = db[i];
+        }
+    }
+}
+
+// Sums of the chunks' parts: 64 outputs (of C (K+1)) per workgroup, four
+// quarters of the parts, joined in a fixed order.
+template <typename T>
+__global__ __launch_bounds__(256) void conv_bwd_sums(const float *part, int64_t parts, int64_t C, int K, T *dw,
+                                                     int64_t dws_c, int64_t dws_k, T *db, int64_t dbs)
+{
+    __shared__ float sh[4][64];
+    const int64_t out = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), n = C * (K + 1);
+    const int q = threadIdx.x >> 6;
+    float a[4] = {};
+    if (out < n) {
+        const int64_t lo = parts * q / 4, hi = parts * (q + 1) / 4;
+        int64_t i = lo;
+        for (; i + 4 <= hi; i += 4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] += part[(i + j) * n + out];
+        for (; i < hi; ++i) a[0] += part[i * n + out];
+    }
+    sh[q][threadIdx.x & 63] = (a[0] + a[1]) + (a[2] + a[3]);
+    __syncthreads();
+    if (q == 0 && out < n) {
+        const float v = (sh[0][threadIdx.x] + sh[1][threadIdx.x]) + (sh[2][threadIdx.x] + sh[3][threadIdx.x]);
+        const int64_t c = out / (K + 1);
+        const int k = (int)(out - c * (K + 1));
+        if (k < K) {
+            if (dw) dw[c * dws_c + k * dws_k] = from_f32<T>(v);
+        } else if (db) db[c * dbs] = from_f32<T>(v);
+    }
+}
+
+S3 s3(const conv_tensor &t) { return {t.strides[0], t.strides[1], t.rank > 2 ? t.strides[2] : 0}; }
+
+ConvP base(const lm_plan_t &p, lm_ptrs q)
+{
+    ConvP a = {};
+    a.x = q[LM_X], a.w = q[LM_W], a.b = q[LM_BIAS], a.s0 = q[LM_STATE_IN], a.gy = q[LM_GY], a.gs = q[LM_GSTATE];
+    a.y = q[LM_Y], a.s1 = q[LM_STATE_OUT], a.dx = q[LM_DX], a.ds = q[LM_DSTATE];
+    a.off = static_cast<const int32_t *>(q[LM_OFFSETS]);
+    a.rows = static_cast<const int32_t *>(q[LM_ROWS]);
+    a.xs = s3(p.t[LM_X]), a.ys = s3(p.t[LM_Y]), a.s0s = s3(p.t[LM_STATE_IN]), a.s1s = s3(p.t[LM_STATE_OUT]);
+    a.gys = s3(p.t[LM_GY]), a.gss = s3(p.t[LM_GSTATE]), a.dxs = s3(p.t[LM_DX]), a.dss = s3(p.t[LM_DSTATE]);
+    a.ws_c = p.t[LM_W].strides[0], a.ws_k = p.t[LM_W].strides[1], a.bs = p.t[LM_BIAS].strides[0];
+    a.seqs = p.seqs, a.C = p.C, a.L = p.L, a.chunk = p.chunk, a.chunks = p.chunks;
+    a.state_rows = p.t[LM_STATE_OUT].sizes[0];
+    a.silu = (p.args.flags & LM_SILU) != 0;
+    a.w_dense = a.ws_c == p.K && (a.ws_k == 1 || p.K == 1);
+    return a;
+}
+
+int blocks_of(ConvP &a, int V)
+{
+    a.cvs = lm_cdiv(a.C, V);
+    return (int)lm_cdiv(a.cvs * a.chunks * a.seqs, 256);
+}
+
+// f(k) for the tap count as a constant.
+template <typename F> void with_taps(int64_t K, F f)
+{
+    switch (K) {
+    case 1: f(std::integral_constant<int, 1>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 3: f(std::integral_constant<int, 3>()); break;
+    case 4: f(std::integral_constant<int, 4>()); break;
+    case 5: f(std::integral_constant<int, 5>()); break;
+    case 6: f(std::integral_constant<int, 6>()); break;
+    case 7: f(std::integral_constant<int, 7>()); break;
+    case 8: f(std::integral_constant<int, 8>()); break;
+    }
+}
+
+template <typename T> void fwd(const lm_plan_t &p, ConvP a, hipStream_t s)
+{
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = a.xs.c == 1 && a.ys.c == 1 && a.C >= V;
+    with_taps(p.K, [&](auto k) {
+        constexpr int K = decltype(k)::value;
+        if (vec) {
+            const int g = blocks_of(a, V);
+            if (g) conv_fwd<T, K, V><<<g, 256, 0, s>>>(a);
+        } else {
+            const int g = blocks_of(a, 1);
+            if (g) conv_fwd<T, K, 1><<<g, 256, 0, s>>>(a);
+        }
+    });
+}
+
+template <typename T> void step(const lm_plan_t &p, ConvP a, hipStream_t s)
+{
+    with_taps(p.K, [&](auto k) {
+        constexpr int K = decltype(k)::value;
+        // Two channels per thread: enough threads for small batches.  An odd C
+        // takes one: the state moves in place, so no two threads may share a
+        // channel.
+        if (a.C % 2 == 0) {
+            const int g = blocks_of(a, 2);
+            if (g) conv_step<T, K, 2><<<g, 256, 0, s>>>(a);
+        } else {
+            const int g = blocks_of(a, 1);
+            if (g) conv_step<T, K, 1><<<g, 256, 0, s>>>(a);
+        }
+    });
+}
+
+template <typename T> void bwd(const lm_plan_t &p, ConvP a, lm_ptrs q, hipStream_t s)
+{
+    constexpr int V = 4;
+    const bool vec = a.xs.c == 1 && a.gys.c == 1 && (!a.dx || a.dxs.c == 1) && a.C >= V;
+    with_taps(p.K, [&](auto k) {
+        constexpr int K = decltype(k)::value;
+        if (vec) {
+            const int g = blocks_of(a, V);
+            if (g) conv_bwd<T, K, V><<<g, 256, 0, s>>>(a);
+        } else {
+            const int g = blocks_of(a, 1);
+            if (g) conv_bwd<T, K, 1><<<g, 256, 0, s>>>(a);
+        }
+    });
+    if (q[LM_DW] || q[LM_DBIAS]) {
+        const conv_tensor &w = p.t[LM_DW], &b = p.t[LM_DBIAS];
+        conv_bwd_sums<T><<<(int)lm_cdiv(p.C * (p.K + 1), 64), 256, 0, s>>>(
+            a.part, p.seqs * p.chunks, p.C, (int)p.K, static_cast<T *>(q[LM_DW]), w.strides[0], w.strides[1],
+            static_cast<T *>(q[LM_DBIAS]), b.strides[0]);
+    }
+}
+
+}  // namespace
+
+int launch_lm_conv(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
+{
+    const ConvP a = base(p, q);
+    if (p.dtype == CONV_F32) fwd<float>(p, a, s);
+    else if (p.dtype == CONV_F16) fwd<f16_t>(p, a, s);
+    else fwd<bf16_t>(p, a, s);
+    return lm_launch_status();
+}
+
+int launch_lm_conv_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
+{
+    const ConvP a = base(p, q);
+    if (p.dtype == CONV_F32) step<float>(p, a, s);
+    else if (p.dtype == CONV_F16) step<f16_t>(p, a, s);
+    else step<bf16_t>(p, a, s);
+    return lm_launch_status();
+}
+
+int launch_lm_conv_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
+{
+    ConvP a = base(p, q);
+    a.part = q[LM_DW] || q[LM_DBIAS] ? static_cast<float *>(ws) : nullptr;
+    if (p.dtype == CONV_F32) bwd<float>(p, a, q, s);
+    else if (p.dtype == CONV_F16) bwd<f16_t>(p, a, q, s);
+    else bwd<bf16_t>(p, a, q, s);
+    return lm_launch_status();
+}
+
+}  // namespace miconv

@@ -1,0 +1,229 @@
+// What the scan's kernels share: parameters, the staged tile and cross-lane sums.
+//
+// A workgroup of four waves owns 64 channels of one group and walks along the
+// sequence in tiles of 32 steps.  Four neighbouring lanes share a channel and
+// hold NS states each (S <= 4 NS; states past S have A = B = C = 0).  Per tile
+// the threads stage d = softplus(dt + dt_bias) and d x, which need one
+// transcendental chain per (step, channel), once for the four lanes, next to
+// B and C in f32; thread (row, 8 channels) of the staging also applies D, the
+// gate and the stores afterwards, so x, dt and z cross from HBM once and stay
+// in its registers.
+#pragma once
+
+#include <type_traits>
+
+#include "lm_dev.h"
+#include "lm_internal.h"
+
+namespace miconv {
+
+struct S4 { int64_t n, g, s, l; };
+
+struct ScanP {
+    const void *x, *dt, *Bm, *Cm, *z, *gy;
+    const float *A, *D, *bias, *s0, *gs;
+    void *y, *dx, *ddt, *dz;
+    float *s1, *saved, *ds;
+    float *carry_h, *carry_d;        // per (sequence, chunk): state or gradient leaving it, sum of d
+    float *part_bc, *part_c;         // backward sums of a workgroup
+    const int32_t *off, *rows;
+    S3 xs, dts, zs, ys, gys, dxs, ddts, dzs;
+    S4 Bs, Cs;
+    S3 s0s, s1s, gss, dss;           // (sequence, channel, state)
+    int64_t A_c, A_s, D_s, bias_s;
+    int64_t seqs, C, L, S, chunk, chunks, Cg, blocks_g, blocks, rows_total, state_rows;
+    int softplus;
+};
+
+constexpr int kCH = LM_SCAN_CH, kTB = LM_SCAN_TB;
+constexpr int kRow = kCH + 16;       // padded f32 row: four rows x 16 channels on 64 banks
+
+// Eight channels of one row, as they are in memory; channels >= n are zero.
+template <typename T> __device__ __forceinline__ Raw<T, 8> get8(const T *p, int64_t cs, int n)
+{
+    if (cs == 1 && n >= 8) return load_raw<T, 8>(p);
+    Raw<T, 8> r;
+    __builtin_memset(&r, 0, sizeof(r));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) r.v[i] = p[i * cs];
+    return r;
+}
+template <typename T> __device__ __forceinline__ void put8(T *p, int64_t cs, int n, const float (&v)[8])
+{
+    if (cs == 1 && n >= 8) store_f32<T, 8>(p, v);
+    else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i * cs] = from_f32<T>(v[i]);
+    }
+}
+
+// Where a workgroup stands.
+struct ScanAt {
+    int64_t seq, ch, c0;     // sequence, chunk, first channel
+    int g, nc;               // group, channels of this workgroup
+    SeqSpan sp;
+    int64_t t0, t1;          // its steps of the sequence
+};
+__device__ __forceinline__ ScanAt scan_at(const ScanP &p, int64_t chunks)
+{
+    ScanAt a;
+    const int64_t b = blockIdx.x, r = b / p.blocks;
+    const int64_t cb = b - r * p.blocks;
+    a.seq = r / chunks;
+    a.ch = r - a.seq * chunks;
+    a.g = (int)(cb / p.blocks_g);
+    const int64_t in_g = (cb - a.g * p.blocks_g) * kCH;
+    a.c0 = a.g * p.Cg + in_g;
+    a.nc = (int)(p.Cg - in_g < kCH ? p.Cg - in_g : kCH);
+    a.sp = seq_span(p.off, a.seq, p.L);
+    a.t0 = a.ch * p.chunk;
+    a.t1 = a.ch == p.chunks - 1 || a.t0 + p.chunk > a.sp.len ? a.sp.len : a.t0 + p.chunk;
+    return a;
+}
+
+// First saved state of a sequence.  ceil(len / CK) states follow it; packed
+// sequences cannot meet since floor(start / CK) + s grows by at least that.
+template <int CK> __device__ __forceinline__ int64_t saved_at(const ScanP &p, const ScanAt &a)
+{
+    return p.off ? a.sp.start / CK + a.seq : a.seq * ((p.L + CK - 1) / CK);
+}
+
+// B and C of a tile on their way to LDS: element e of a thread is state
+// e % (4 NS) of row e / (4 NS) of B, then of C.
+template <typename T, int NS> struct BcRegs {
+    static constexpr int n = 2 * kTB * 4 * NS / 256;
+    T v[n];
+    __device__ __forceinline__ void fetch(const ScanP &p, const ScanAt &a, int64_t t, int64_t t1)
+    {
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const int e = (j * 256 + (int)threadIdx.x) % (kTB * 4 * NS);
+            const bool second = (j * 256 + (int)threadIdx.x) >= kTB * 4 * NS;
+            const int s = e % (4 * NS);
+            const int64_t l = t + e / (4 * NS);
+            T r;
+            __builtin_memset(&r, 0, sizeof(r));
+            if (s < p.S && l < t1) {
+                const S4 &st = second ? p.Cs : p.Bs;
+                r = static_cast<const T *>(second ? p.Cm : p.Bm)[a.sp.row0 * st.n + a.g * st.g + s * st.s +
+                                                               (a.sp.start + l) * st.l];
+            }
+            v[j] = r;
+        }
+    }
+    __device__ __forceinline__ void put(float *sh) const   // [kTB][2][4 NS]
+    {
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const int e = (j * 256 + (int)threadIdx.x) % (kTB * 4 * NS);
+            const int second = (j * 256 + (int)threadIdx.x) >= kTB * 4 * NS;
+            sh[(e / (4 * NS)) * (8 * NS) + second * (4 * NS) + e % (4 * NS)] = to_f32(v[j]);
+        }
+    }
+};
+
+template <int NS> __device__ __forceinline__ void lds_states(const float *p, float (&o)[NS])
+{
+    if constexpr (NS >= 4) {
+#pragma unroll
+        for (int i = 0; i < NS; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(p + i);
+            o[i] = v[0], o[i + 1] = v[1], o[i + 2] = v[2], o[i + 3] = v[3];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) o[i] = p[i];
+    }
+}
+
+// A lane's NS states of channel c in [row, channel, state] memory at any
+// strides; states past S are zero.
+template <int NS>
+__device__ __forceinline__ void get_states(const float *p, const S3 &st, int64_t row, int64_t c, int s0, int64_t S,
+                                           float (&h)[NS])
+{
+    const float *q = p + row * st.n + c * st.c + s0 * st.l;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) h[i] = s0 + i < S ? q[i * st.l] : 0.f;
+}
+template <int NS>
+__device__ __forceinline__ void put_states(float *p, const S3 &st, int64_t row, int64_t c, int s0, int64_t S,
+                                           const float (&h)[NS])
+{
+    float *q = p + row * st.n + c * st.c + s0 * st.l;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (s0 + i < S) q[i * st.l] = h[i];
+}
+
+// Lane exchange inside groups of four lanes.
+template <int CTRL> __device__ __forceinline__ float quad(float v)
+{
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += quad<0xB1>(v);        // lanes 1 0 3 2
+    return v + quad<0x4E>(v);  // lanes 2 3 0 1
+}
+// Sums over the four lanes of four values; lane q receives the sum of v[q].
+__device__ __forceinline__ float quad_sum4(const float (&v)[4], int q)
+{
+    const bool odd = q & 1, high = q & 2;
+    const float a0 = v[0] + quad<0xB1>(v[0]), a1 = v[1] + quad<0xB1>(v[1]);
+    const float a2 = v[2] + quad<0xB1>(v[2]), a3 = v[3] + quad<0xB1>(v[3]);
+    const float lo = odd ? a1 : a0, hi = odd ? a3 : a2;
+    const float b0 = lo + quad<0x4E>(lo), b1 = hi + quad<0x4E>(hi);
+    return high ? b1 : b0;
+}
+
+inline S3 lm_s3(const conv_tensor &t) { return {t.strides[0], t.strides[1], t.rank > 2 ? t.strides[2] : 0}; }
+inline S4 lm_s4(const conv_tensor &t) { return {t.strides[0], t.strides[1], t.strides[2], t.rank > 3 ? t.strides[3] : 0}; }
+
+inline ScanP scan_params(const lm_plan_t &p, lm_ptrs q)
+{
+    const auto f = [&](int s) { return static_cast<float *>(q[s]); };
+    ScanP a = {};
+    a.x = q[LM_X], a.dt = q[LM_DT], a.Bm = q[LM_B], a.Cm = q[LM_C], a.z = q[LM_Z], a.gy = q[LM_GY];
+    a.A = f(LM_A), a.D = f(LM_D), a.bias = f(LM_DT_BIAS), a.s0 = f(LM_STATE_IN), a.gs = f(LM_GSTATE);
+    a.y = q[LM_Y], a.dx = q[LM_DX], a.ddt = q[LM_DDT], a.dz = q[LM_DZ];
+    a.s1 = f(LM_STATE_OUT), a.saved = f(LM_SAVED), a.ds = f(LM_DSTATE);
+    a.off = static_cast<const int32_t *>(q[LM_OFFSETS]), a.rows = static_cast<const int32_t *>(q[LM_ROWS]);
+    a.xs = lm_s3(p.t[LM_X]), a.dts = lm_s3(p.t[LM_DT]), a.zs = lm_s3(p.t[LM_Z]), a.ys = lm_s3(p.t[LM_Y]);
+    a.gys = lm_s3(p.t[LM_GY]), a.dxs = lm_s3(p.t[LM_DX]), a.ddts = lm_s3(p.t[LM_DDT]), a.dzs = lm_s3(p.t[LM_DZ]);
+    a.Bs = lm_s4(p.t[LM_B]), a.Cs = lm_s4(p.t[LM_C]);
+    a.s0s = lm_s3(p.t[LM_STATE_IN]), a.s1s = lm_s3(p.t[LM_STATE_OUT]);
+    a.gss = lm_s3(p.t[LM_GSTATE]), a.dss = lm_s3(p.t[LM_DSTATE]);
+    a.A_c = p.t[LM_A].strides[0], a.A_s = p.t[LM_A].strides[1];
+    a.D_s = p.t[LM_D].strides[0], a.bias_s = p.t[LM_DT_BIAS].strides[0];
+    a.seqs = p.seqs, a.C = p.C, a.L = p.L, a.S = p.S, a.chunk = p.chunk, a.chunks = p.chunks;
+    a.Cg = p.C / p.G;
+    a.blocks_g = lm_cdiv(a.Cg, LM_SCAN_CH);
+    a.blocks = a.blocks_g * p.G;
+    a.rows_total = p.t[LM_X].sizes[0] * p.L;
+    a.state_rows = p.t[LM_STATE_OUT].sizes[0];
+    a.softplus = (p.args.flags & LM_SOFTPLUS) != 0;
+    return a;
+}
+
+// f(T) for the element type, f(NS) for the states per lane.
+template <typename F> void with_type(int32_t dtype, F f)
+{
+    if (dtype == CONV_F32) f(float());
+    else if (dtype == CONV_F16) f(f16_t());
+    else f(bf16_t());
+}
+template <typename F> void with_ns(int64_t S, F f)
+{
+    switch (scan_ns(S)) {
+    case 1: f(std::integral_constant<int, 1>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 4: f(std::integral_constant<int, 4>()); break;
+    case 8: f(std::integral_constant<int, 8>()); break;
+    case 16: f(std::integral_constant<int, 16>()); break;
+    }
+}
+
+}  // namespace miconv

@@ -1,0 +1,409 @@
+"""Sequence operators of language models on the GPU (binding of
+include/miconv_lm.h): the short causal convolution, the selective state space
+scan, and products with 4-bit weights.
+
+Activations are logical [N, C, L] with any strides, like the convolution's;
+channels-last storage (L rows of C channels) is the fast order.  A packed batch
+is [1, C, T] with ``offsets`` (int32 on the device, ascending from 0 to T):
+sequence s is the rows offsets[s] .. offsets[s+1]-1.  Give ``max_len`` with it,
+a length that few sequences pass: it decides how the work is split and nothing
+else.
+
+Each operator exists for prompts (``causal_conv``, ``selective_scan``), as its
+gradients (``*_backward``) and for single tokens (``*_step``, which update the
+state in place).  ``Prepared*`` objects keep the plan of fixed shapes, strides
+and types for loops where a call's latency counts; like ``Prepared`` of the
+convolution they take tensors of those descriptors and check no more.
+
+torch provides device memory and the current stream; all arithmetic is in the
+library's kernels.  Nothing here records autograd history.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _abi as A
+from .api import ConvError, _TORCH_DT
+
+_SLOT = {name: i for i, name in enumerate(A.LM_SLOTS)}
+(_X, _W, _BIAS, _Y, _S0, _S1, _OFF, _GY, _GS, _DX, _DW, _DBIAS, _DS, _DT, _A, _B, _C, _D, _Z, _DTB, _DDT, _DA, _DB, _DC,
+ _DD, _DZ, _DDTB, _SAVED, _ROWS, _SCALES, _ZEROS) = range(A.LM_NSLOT)
+_TYPES = {**_TORCH_DT, torch.int32: A.LM_I32, torch.uint8: A.LM_U8}
+_Ptrs = ctypes.c_void_p * A.LM_NSLOT
+
+
+class ConvOut(NamedTuple):
+    y: torch.Tensor
+    state: Optional[torch.Tensor]
+
+
+class ConvGrads(NamedTuple):
+    dx: Optional[torch.Tensor]
+    dw: Optional[torch.Tensor]
+    db: Optional[torch.Tensor]
+    dstate: Optional[torch.Tensor]
+
+
+class ScanOut(NamedTuple):
+    y: Optional[torch.Tensor]
+    state: Optional[torch.Tensor]
+    saved: Optional[torch.Tensor]
+
+
+class ScanGrads(NamedTuple):
+    dx: torch.Tensor
+    ddt: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dD: Optional[torch.Tensor]
+    dz: Optional[torch.Tensor]
+    ddt_bias: Optional[torch.Tensor]
+    dstate: Optional[torch.Tensor]
+
+
+# ------------------------------------------------------------------- plans --
+
+def _make_plan(op, tensors, flags=0, max_len=0, chunk=0) -> A.LmPlan:
+    """lm_plan for {place: tensor} (None: absent)."""
+    d = (A.ConvTensor * A.LM_NSLOT)()
+    for slot, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype not in _TYPES:
+            raise TypeError(f"{A.LM_SLOTS[slot].lower()}: unsupported dtype {t.dtype}")
+        if t.dim() > A.MAX_RANK or t.dim() == 0:
+            raise ValueError(f"{A.LM_SLOTS[slot].lower()}: 1 to {A.MAX_RANK} dims")
+        e = d[slot]
+        e.rank, e.dtype = t.dim(), _TYPES[t.dtype]
+        for i, (s, st) in enumerate(zip(t.shape, t.stride())):
+            e.sizes[i], e.strides[i] = s, st
+    args = A.LmArgs(flags, 0, int(max_len or 0), int(chunk or 0))
+    p = A.LmPlan()
+    err = ctypes.create_string_buffer(256)
+    st = A.lib().lm_plan(op, d, ctypes.byref(args), ctypes.byref(p), err, len(err))
+    if st != A.OK:
+        raise ConvError(st, err.value.decode())
+    return p
+
+
+# Plans by operator, arguments, shapes, strides and types (host structs only).
+_plans: dict = {}
+
+
+def _plan_for(op, inputs, outputs, flags=0, max_len=0, chunk=0, extra=None) -> A.LmPlan:
+    """The plan of a call.  ``outputs`` are allocated from the inputs'
+    descriptors and so need no place in the key; ``extra`` says which exist."""
+    key = (op, flags, max_len, chunk, extra,
+           tuple([(k, t.shape, t.stride(), t.dtype) for k, t in inputs.items() if t is not None]))
+    p = _plans.get(key)
+    if p is None:
+        p = _make_plan(op, {**inputs, **outputs}, flags, max_len, chunk)
+        if len(_plans) >= 512:
+            _plans.clear()
+        _plans[key] = p
+    return p
+
+
+def _check_device(inputs) -> torch.device:
+    dev = None
+    for slot, t in inputs.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+def _launch(p: A.LmPlan, tensors, dev: torch.device, stream: Optional[int] = None) -> None:
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(p, tensors, dev, stream)
+    q = _Ptrs()
+    for slot, t in tensors.items():
+        if t is not None:
+            q[slot] = t.data_ptr()
+    ws, n = None, p.workspace_bytes
+    if n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    st = A.lib().lm_run(ctypes.byref(p), q, ws.data_ptr() if n else None, n, stream)
+    if st != A.OK:
+        raise ConvError(st)
+
+
+def _rows_like(n, c, l, ref, dtype=None):
+    """[n, c, l] stored as l rows of c channels."""
+    return torch.empty((n, l, c), dtype=dtype or ref.dtype, device=ref.device).transpose(1, 2)
+
+
+def _act(activation) -> int:
+    if activation in (None, "none"):
+        return 0
+    if activation == "silu":
+        return A.LM_SILU
+    raise ValueError(f"activation {activation!r}: None or 'silu'")
+
+
+def _taps(w: torch.Tensor) -> torch.Tensor:
+    """[C, K] of a depthwise weight [C, 1, K] or [C, K]."""
+    return w.squeeze(1) if w.dim() == 3 and w.shape[1] == 1 else w
+
+
+def _seqs(x, offsets) -> int:
+    return x.shape[0] if offsets is None else offsets.shape[0] - 1
+
+
+# ------------------------------------------------------ causal convolution --
+
+def causal_conv(x, w, b=None, *, activation=None, state=None, offsets=None, max_len=None,
+                return_state: bool = False, chunk=None) -> ConvOut:
+    """act(bias + causal depthwise convolution of x with w [C, K] (or [C, 1, K])).
+
+    ``state`` [sequences, C, K-1] holds the K-1 values in front of each
+    sequence (zeros without it); ``return_state`` gives those in front of what
+    follows it.  ``chunk`` forces the rows one thread walks."""
+    w = _taps(w)
+    ins = {_X: x, _W: w, _BIAS: b, _S0: state, _OFF: offsets}
+    dev = _check_device(ins)
+    y = torch.empty_like(x)
+    last = _rows_like(_seqs(x, offsets), x.shape[1], w.shape[1] - 1, x) if return_state and w.dim() == 2 else None
+    outs = {_Y: y, _S1: last}
+    p = _plan_for(A.LM_CONV, ins, outs, _act(activation), max_len or 0, chunk or 0, return_state)
+    _launch(p, {**ins, **outs}, dev)
+    return ConvOut(y, last)
+
+
+def causal_conv_backward(gy, x, w, b=None, *, activation=None, state=None, offsets=None, max_len=None, gstate=None,
+                         need_dx: bool = True, need_dw: bool = True, chunk=None) -> ConvGrads:
+    """Gradients of ``causal_conv`` for gy, the gradient of y, and ``gstate``,
+    that of the returned state.  db comes with a bias, dstate with a state;
+    ``need_dw`` covers dw and db."""
+    shape, w = w.shape, _taps(w)
+    ins = {_GY: gy, _X: x, _W: w, _BIAS: b, _S0: state, _OFF: offsets, _GS: gstate}
+    dev = _check_device(ins)
+    dx = torch.empty_like(x) if need_dx else None
+    dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
+    db = torch.empty(b.shape, dtype=b.dtype, device=dev) if need_dw and b is not None else None
+    ds = torch.empty_like(state) if state is not None else None
+    outs = {_DX: dx, _DW: dw, _DBIAS: db, _DS: ds}
+    p = _plan_for(A.LM_CONV_BWD, ins, outs, _act(activation), max_len or 0, chunk or 0, (need_dx, need_dw))
+    _launch(p, {**ins, **outs}, dev)
+    return ConvGrads(dx, dw.view(shape) if dw is not None else None, db, ds)
+
+
+class _Step:
+    """A plan whose output is a new contiguous tensor of the plan's shape."""
+
+    def __init__(self, op, tensors, shape, ref, flags=0):
+        self.device = _check_device(tensors)
+        self.shape, self.dtype = shape, ref.dtype
+        self.plan = _make_plan(op, {**tensors, _Y: self.empty_output()}, flags)
+        self._plan_ref = ctypes.byref(self.plan)
+        self._run = A.lib().lm_run
+
+    def empty_output(self) -> torch.Tensor:
+        return torch.empty(self.shape, dtype=self.dtype, device=self.device)
+
+    def _launch(self, q, stream):
+        dev = self.device.index
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self._launch(q, stream)
+        st = self._run(self._plan_ref, q, None, 0, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+        if st != A.OK:
+            raise ConvError(st)
+
+
+class PreparedCausalConvStep(_Step):
+    """The step of ``causal_conv`` for fixed descriptors."""
+
+    def __init__(self, x, w, b, state, *, activation=None, rows=None):
+        super().__init__(A.LM_CONV_STEP, {_X: x, _W: _taps(w), _BIAS: b, _S1: state, _ROWS: rows}, tuple(x.shape), x,
+                         _act(activation))
+
+    def run(self, x, w, b, state, rows=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
+        if y is None:
+            y = self.empty_output()
+        q = _Ptrs()
+        q[_X], q[_W], q[_S1], q[_Y] = x.data_ptr(), w.data_ptr(), state.data_ptr(), y.data_ptr()
+        if b is not None:
+            q[_BIAS] = b.data_ptr()
+        if rows is not None:
+            q[_ROWS] = rows.data_ptr()
+        self._launch(q, stream)
+        return y
+
+
+def causal_conv_step(x, w, b, state, *, activation=None, rows=None) -> torch.Tensor:
+    """One token: x [N, C], state [N, C, K-1] updated in place.  With ``rows``
+    (int32 [N], distinct) batch row n uses state row rows[n]; a row outside
+    the state is left out and its y is zero."""
+    return PreparedCausalConvStep(x, w, b, state, activation=activation, rows=rows).run(x, _taps(w), b, state, rows)
+
+
+# --------------------------------------------------------- selective scan --
+
+def _grouped(v, dims):
+    """B or C with its group dim ([N, S, L] is one group)."""
+    return v.unsqueeze(1) if v is not None and v.dim() == dims - 1 else v
+
+
+def selective_scan(x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False, state=None, offsets=None,
+                   max_len=None, return_state: bool = False, save: bool = False, want_y: bool = True,
+                   chunk=None) -> ScanOut:
+    """h <- exp(d A) h + d x B,  y = (sum_s C h + D x) silu(z),
+    d = dt + dt_bias, or its softplus.
+
+    x, dt, z [N, C, L]; A [C, S], D, dt_bias [C] in f32; B, C [N, G, S, L] (or
+    [N, S, L]), channel c using group c // (C // G); ``state`` and the returned
+    state f32 [sequences, C, S].  ``save`` returns what ``selective_scan_backward``
+    takes as ``saved``.  ``chunk`` forces how many steps run in one piece."""
+    B, C = _grouped(B, 4), _grouped(C, 4)
+    ins = {_X: x, _DT: dt, _A: A_, _B: B, _C: C, _D: D, _Z: z, _DTB: dt_bias, _S0: state, _OFF: offsets}
+    dev = _check_device(ins)
+    n = _seqs(x, offsets)
+    outs = {_Y: torch.empty_like(x) if want_y else None,
+            _S1: torch.empty((n, x.shape[1], A_.shape[-1]), device=dev) if return_state else None,
+            _SAVED: _new_saved(x, A_, offsets) if save else None}
+    p = _plan_for(_abi_scan, ins, outs, A.LM_SOFTPLUS if dt_softplus else 0, max_len or 0, chunk or 0,
+                  (want_y, return_state, save))
+    _launch(p, {**ins, **outs}, dev)
+    return ScanOut(outs[_Y], outs[_S1], outs[_SAVED])
+
+
+_abi_scan = A.LM_SCAN
+
+
+def _new_saved(x, A_, offsets) -> torch.Tensor:
+    """Room for the states before every 16th step (fewer steps above 16 states)."""
+    s = A_.shape[-1]
+    ns = 1
+    while 4 * ns < s:
+        ns *= 2
+    ck = 16 if ns <= 4 else max(1, 64 // ns)
+    count = x.shape[0] * -(-x.shape[2] // ck) if offsets is None else x.shape[2] // ck + offsets.shape[0]
+    return torch.empty(count * x.shape[1] * 4 * ns, device=x.device)
+
+
+def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False, state=None,
+                            offsets=None, max_len=None, gstate=None, saved=None, chunk=None) -> ScanGrads:
+    """Gradients of ``selective_scan`` for gy, the gradient of y, and
+    ``gstate``, that of the returned state.  ``saved`` comes from the forward
+    call (``save=True``) on the same tensors; without it the states are computed
+    again.  dD, dz, ddt_bias and dstate come with D, z, dt_bias and state."""
+    if saved is None:
+        saved = selective_scan(x, dt, A_, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, state=state,
+                               offsets=offsets, max_len=max_len, save=True, want_y=False, chunk=chunk).saved
+    b_shape, c_shape, B, C = B.shape, C.shape, _grouped(B, 4), _grouped(C, 4)
+    ins = {_GY: gy, _X: x, _DT: dt, _A: A_, _B: B, _C: C, _D: D, _Z: z, _DTB: dt_bias, _OFF: offsets, _GS: gstate,
+           _SAVED: saved}
+    dev = _check_device(ins)
+    new = lambda t: torch.empty_like(t) if t is not None else None  # noqa: E731
+    outs = {_DX: new(x), _DDT: new(dt), _DA: new(A_), _DB: new(B), _DC: new(C), _DD: new(D), _DZ: new(z), _DDTB: new(dt_bias),
+            _DS: new(state)}
+    p = _plan_for(A.LM_SCAN_BWD, ins, outs, A.LM_SOFTPLUS if dt_softplus else 0, max_len or 0, chunk or 0,
+                  (state.shape, state.stride()) if state is not None else None)
+    _launch(p, {**ins, **outs}, dev)
+    return ScanGrads(outs[_DX], outs[_DDT], outs[_DA], outs[_DB].view(b_shape), outs[_DC].view(c_shape), outs[_DD], outs[_DZ],
+                     outs[_DDTB], outs[_DS])
+
+
+class PreparedSelectiveScanStep(_Step):
+    """The step of ``selective_scan`` for fixed descriptors."""
+
+    def __init__(self, x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False, rows=None):
+        super().__init__(A.LM_SCAN_STEP, {_X: x, _DT: dt, _A: A_, _B: _grouped(B, 3), _C: _grouped(C, 3), _S1: state, _D: D,
+                                          _Z: z, _DTB: dt_bias, _ROWS: rows}, tuple(x.shape), x,
+                         A.LM_SOFTPLUS if dt_softplus else 0)
+
+    def run(self, x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None, rows=None, y=None,
+            stream: Optional[int] = None) -> torch.Tensor:
+        if y is None:
+            y = self.empty_output()
+        q = _Ptrs()
+        q[_X], q[_DT], q[_A], q[_B], q[_C] = x.data_ptr(), dt.data_ptr(), A_.data_ptr(), B.data_ptr(), C.data_ptr()
+        q[_S1], q[_Y] = state.data_ptr(), y.data_ptr()
+        if D is not None:
+            q[_D] = D.data_ptr()
+        if z is not None:
+            q[_Z] = z.data_ptr()
+        if dt_bias is not None:
+            q[_DTB] = dt_bias.data_ptr()
+        if rows is not None:
+            q[_ROWS] = rows.data_ptr()
+        self._launch(q, stream)
+        return y
+
+
+def selective_scan_step(x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+                        rows=None) -> torch.Tensor:
+    """One token: x, dt, z [N, C], B and C [N, G, S] (or [N, S]), state f32
+    [N, C, S] updated in place; ``rows`` as in ``causal_conv_step``."""
+    p = PreparedSelectiveScanStep(x, dt, A_, B, C, state, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, rows=rows)
+    return p.run(x, dt, A_, B, C, state, D=D, z=z, dt_bias=dt_bias, rows=rows)
+
+
+# ---------------------------------------------------------- 4-bit products --
+
+class PreparedMatvec4(_Step):
+    """``matvec4`` for fixed descriptors (x [M, K])."""
+
+    def __init__(self, x, packed, scales, zeros=None, bias=None):
+        super().__init__(A.LM_MV4, {_X: x, _W: packed, _SCALES: scales, _ZEROS: zeros, _BIAS: bias},
+                         (x.shape[0], packed.shape[0]), x)
+
+    def run(self, x, packed, scales, zeros=None, bias=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
+        if y is None:
+            y = self.empty_output()
+        q = _Ptrs()
+        q[_X], q[_W], q[_SCALES], q[_Y] = x.data_ptr(), packed.data_ptr(), scales.data_ptr(), y.data_ptr()
+        if zeros is not None:
+            q[_ZEROS] = zeros.data_ptr()
+        if bias is not None:
+            q[_BIAS] = bias.data_ptr()
+        self._launch(q, stream)
+        return y
+
+
+def matvec4(x, packed, scales, zeros=None, bias=None) -> torch.Tensor:
+    """x [..., K] times 4-bit weights: sum_k x[k] scales[n, k // group]
+    (q[n, k] - zeros[n, k // group]) + bias[n], zeros 8 unless given.
+
+    ``packed`` uint8 [N, K/2] holds the even k in the low four bits; scales and
+    zeros [N, K/group] and x share a type; group is a multiple of 32.  Made for
+    few rows: 16 cost about what one does, more repeat the weights' pass.  A
+    row whose sums pass f32's range at 256 times x gives infinities or NaN."""
+    x2 = x.reshape(-1, x.shape[-1])
+    y = PreparedMatvec4(x2, packed, scales, zeros, bias).run(x2, packed, scales, zeros, bias)
+    return y.view(x.shape[:-1] + (packed.shape[0],))
+
+
+def quantize4(w: torch.Tensor, group: int = 128, symmetric: bool = True, dtype: torch.dtype = torch.bfloat16):
+    """(packed, scales, zeros) of a weight [N, K]: round to nearest with one
+    scale per group of columns, around 8 (zeros is None) or, not symmetric,
+    around the group's own zero point."""
+    n, k = w.shape
+    if k % group:
+        raise ValueError(f"{k} columns do not make groups of {group}")
+    g = w.float().view(n, k // group, group)
+    if symmetric:
+        scales = (g.abs().amax(2) / 7).to(dtype)
+        scales[scales == 0] = 1  # a group of zeros
+        zeros, z = None, 8.0
+    else:
+        lo, hi = g.amin(2).clamp(max=0), g.amax(2).clamp(min=0)
+        scales = ((hi - lo) / 15).to(dtype)
+        scales[scales == 0] = 1  # a group of zeros
+        zeros = torch.round(-lo / scales.float()).clamp(0, 15).to(dtype)
+        z = zeros.float()[..., None]
+    q = torch.clamp(torch.round(g / scales.float()[..., None]) + z, 0, 15).to(torch.uint8).view(n, k)
+    return (q[:, 0::2] | (q[:, 1::2] << 4)).contiguous(), scales, zeros
