@@ -19,7 +19,10 @@
 namespace miconv {
 namespace {
 
-constexpr int kRowsAhead = 4;   // rows whose loads are in flight while the previous ones are used
+// Loads past the end repeat the last row: behind a branch their registers
+// would be waited for where the paths meet.
+constexpr int kRowsAhead = 8;   // rows whose loads are in flight while the previous ones are used
+constexpr int kRowsAheadBwd = 4;
 
 struct ConvP {
     const void *x, *w, *b, *s0, *gy, *gs;
@@ -130,9 +133,9 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int r = 0; r < kRowsAhead; ++r)
-            if (t + r < t1) next[r] = load_raw<T, V>(x + (t + r) * p.xs.l);
+            next[r] = load_raw<T, V>(x + (t + r < t1 ? t + r : t1 - 1) * p.xs.l);
     };
-    fetch(t0);
+    if (t0 < t1) fetch(t0);
     for (int64_t t = t0; t < t1; t += kRowsAhead) {
         Raw<T, V> cur[kRowsAhead];
 #pragma unroll
@@ -144,7 +147,7 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
             float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                h[K - 1][i] = to_f32(cur[r].v[i]);
+                h[K - 1][i] = cur[r].f(i);
                 float a = b[i];
 #pragma unroll
                 for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[k][i], a);
@@ -234,23 +237,23 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
         }
         const int64_t end = t1 + (K - 1);                       // rows walked
         const int64_t has = end < sp.len ? end : sp.len;        // rows that exist
-        Raw<T, V> nx[kRowsAhead], ng[kRowsAhead];
+        Raw<T, V> nx[kRowsAheadBwd], ng[kRowsAheadBwd];
         auto fetch = [&](int64_t t) {
 #pragma unroll
-            for (int r = 0; r < kRowsAhead; ++r)
-                if (t + r < has) {
-                    nx[r] = load_raw<T, V>(x + (t + r) * p.xs.l);
-                    ng[r] = load_raw<T, V>(gy + (t + r) * p.gys.l);
-                }
+            for (int r = 0; r < kRowsAheadBwd; ++r) {
+                const int64_t l = t + r < has ? t + r : has - 1;
+                nx[r] = load_raw<T, V>(x + l * p.xs.l);
+                ng[r] = load_raw<T, V>(gy + l * p.gys.l);
+            }
         };
-        fetch(t0);
-        for (int64_t t = t0; t < end; t += kRowsAhead) {
-            Raw<T, V> cx[kRowsAhead], cg[kRowsAhead];
+        if (has > 0) fetch(t0);
+        for (int64_t t = t0; t < end; t += kRowsAheadBwd) {
+            Raw<T, V> cx[kRowsAheadBwd], cg[kRowsAheadBwd];
 #pragma unroll
-            for (int r = 0; r < kRowsAhead; ++r) cx[r] = nx[r], cg[r] = ng[r];
-            fetch(t + kRowsAhead);
+            for (int r = 0; r < kRowsAheadBwd; ++r) cx[r] = nx[r], cg[r] = ng[r];
+            if (has > 0) fetch(t + kRowsAheadBwd);
 #pragma unroll
-            for (int r = 0; r < kRowsAhead; ++r) {
+            for (int r = 0; r < kRowsAheadBwd; ++r) {
                 const int64_t row = t + r;
                 if (row >= end) break;
 #pragma unroll
@@ -262,8 +265,8 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
                 if (row < has) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        h[K - 1][i] = to_f32(cx[r].v[i]);
-                        float gi = to_f32(cg[r].v[i]);
+                        h[K - 1][i] = cx[r].f(i);
+                        float gi = cg[r].f(i);
                         if (p.silu) {
                             float a = b[i];
 #pragma unroll
@@ -322,18 +325,18 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
     }
 }
 
-// Sums of the chunks' parts: 64 outputs (of C (K+1)) per workgroup, four
-// quarters of the parts, joined in a fixed order.
+// Sums of the chunks' parts: 64 outputs (of C (K+1)) per workgroup, a
+// sixteenth of the parts per wave, joined in a fixed order.
 template <typename T>
-__global__ __launch_bounds__(256) void conv_bwd_sums(const float *part, int64_t parts, int64_t C, int K, T *dw,
-                                                     int64_t dws_c, int64_t dws_k, T *db, int64_t dbs)
+__global__ __launch_bounds__(1024) void conv_bwd_sums(const float *part, int64_t parts, int64_t C, int K, T *dw,
+                                                      int64_t dws_c, int64_t dws_k, T *db, int64_t dbs)
 {
-    __shared__ float sh[4][64];
+    __shared__ float sh[16][64];
     const int64_t out = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), n = C * (K + 1);
     const int q = threadIdx.x >> 6;
     float a[4] = {};
     if (out < n) {
-        const int64_t lo = parts * q / 4, hi = parts * (q + 1) / 4;
+        const int64_t lo = parts * q / 16, hi = parts * (q + 1) / 16;
         int64_t i = lo;
         for (; i + 4 <= hi; i += 4)
 #pragma unroll
@@ -343,7 +346,9 @@ __global__ __launch_bounds__(256) void conv_bwd_sums(const float *part, int64_t 
     sh[q][threadIdx.x & 63] = (a[0] + a[1]) + (a[2] + a[3]);
     __syncthreads();
     if (q == 0 && out < n) {
-        const float v = (sh[0][threadIdx.x] + sh[1][threadIdx.x]) + (sh[2][threadIdx.x] + sh[3][threadIdx.x]);
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += sh[i][threadIdx.x];
         const int64_t c = out / (K + 1);
         const int k = (int)(out - c * (K + 1));
         if (k < K) {
@@ -441,7 +446,7 @@ template <typename T> void bwd(const lm_plan_t &p, ConvP a, lm_ptrs q, hipStream
     });
     if (q[LM_DW] || q[LM_DBIAS]) {
         const conv_tensor &w = p.t[LM_DW], &b = p.t[LM_DBIAS];
-        conv_bwd_sums<T><<<(int)lm_cdiv(p.C * (p.K + 1), 64), 256, 0, s>>>(
+        conv_bwd_sums<T><<<(int)lm_cdiv(p.C * (p.K + 1), 64), 1024, 0, s>>>(
             a.part, p.seqs * p.chunks, p.C, (int)p.K, static_cast<T *>(q[LM_DW]), w.strides[0], w.strides[1],
             static_cast<T *>(q[LM_DBIAS]), b.strides[0]);
     }

@@ -89,7 +89,7 @@ __device__ __forceinline__ void mv_mma(const Raw<T, 8> &x, const uint4 &w, f32x4
     if constexpr (std::is_same<T, float>::value) {
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.v[i];
+        for (int i = 0; i < 8; ++i) v[i] = x.f(i);
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
             uint4 a;
@@ -125,55 +125,58 @@ __device__ __forceinline__ void transpose_words(uint32_t (&w)[4])
     s32(w[0], w[2]), s32(w[1], w[3]);
 }
 
-// WIDE: every block of 128 columns lies in one group.
-template <typename T, bool WIDE> __global__ __launch_bounds__(64 * kMvWaves) void mv4(const MvP p)
+// WIDE: every block of 128 columns lies in one group.  DENSE: x's columns are
+// contiguous.
+template <typename T, bool WIDE, bool DENSE> __global__ __launch_bounds__(64 * kMvWaves) void mv4(const MvP p)
 {
-    typedef typename MvOp<T>::in I;
+    constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;   // blocks of a wave in flight
     __shared__ float s_acc[kMvWaves][16][17];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kb = lane >> 4, col = lane & 15;
     const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16;
     const int64_t n = n0 + col < p.N ? n0 + col : p.N - 1;
-    const bool has_m = m0 + col < p.M;
-    const uint8_t *w = p.w + n * p.w_n + kb * 16;
-    const T *x = static_cast<const T *>(p.x) + (m0 + (has_m ? col : 0)) * p.xs_m;
+    const uint8_t *w = p.w + n * p.w_n;
+    const T *x = static_cast<const T *>(p.x) + (m0 + col < p.M ? m0 + col : p.M - 1) * p.xs_m;
     const T *sc = static_cast<const T *>(p.scales) + n * p.sc_n;
-    const T *ze = p.zeros ? static_cast<const T *>(p.zeros) + n * p.z_n : nullptr;
-    const bool want_sx = std::is_same<T, bf16_t>::value || ze;
+    const bool has_z = p.zeros;
+    const T *ze = has_z ? static_cast<const T *>(p.zeros) + n * p.z_n : sc;
+    const int64_t ze_g = has_z ? p.z_g : p.sc_g;
+    const bool want_sx = std::is_same<T, bf16_t>::value || has_z;
 
     struct Block {
         uint4 w;
         Raw<T, 8> x[4];
         T s[WIDE ? 1 : 4], z[WIDE ? 1 : 4];
     };
-    const auto fetch = [&](int64_t b, Block &o) {
-        const int64_t k0 = b * 128;
-        const bool in = WIDE || k0 + 32 * kb < p.K;
-        o.w = in ? *reinterpret_cast<const uint4 *>(w + b * 64) : uint4{0, 0, 0, 0};
+    // Lanes past the last row, output or column repeat one that exists: rows
+    // and outputs past the end are not stored, columns are cleared in x below.
+    const int K = (int)p.K, group = (int)p.group;
+    const auto fetch = [&](int b, Block &o) {
+        const int k0 = b * 128;
+        o.w = *reinterpret_cast<const uint4 *>(w + (WIDE || k0 + 32 * kb < K ? k0 + 32 * kb : 0) / 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t k = k0 + (WIDE ? 32 * kb + 8 * j : 32 * j + 8 * kb);
-            __builtin_memset(&o.x[j], 0, sizeof(o.x[j]));
-            if (has_m && (WIDE || k < p.K)) {
-                if (p.xs_k == 1) o.x[j] = load_raw<T, 8>(x + k);
-                else {
+            int k = k0 + (WIDE ? 32 * kb + 8 * j : 32 * j + 8 * kb);
+            if (!WIDE && k >= K) k = 0;
+            if constexpr (DENSE) o.x[j] = load_raw<T, 8>(x + k);
+            else {
+                o.x[j].zero();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o.x[j].v[i] = x[(k + i) * p.xs_k];
-                }
+                for (int i = 0; i < 8; ++i) o.x[j].set(i, x[(k + i) * p.xs_k]);
             }
         }
 #pragma unroll
         for (int j = 0; j < (WIDE ? 1 : 4); ++j) {
-            const int64_t k = k0 + 32 * j;
-            const int64_t g = (WIDE || k < p.K ? k : k0) / p.group;
+            const int k = k0 + 32 * j;
+            const int64_t g = (WIDE || k < K ? k : k0) / group;
             o.s[j] = sc[g * p.sc_g];
-            if (ze) o.z[j] = ze[g * p.z_g];
+            o.z[j] = ze[g * ze_g];
         }
     };
     f32x4 y = {0, 0, 0, 0};
     const auto flush = [&](const f32x4 &acc, const f32x4 &sx, T s, T z) {
         const float sf = to_f32(s);
         if (want_sx) {
-            const float off = excess<T>() + (ze ? to_f32(z) : 8.f);
+            const float off = excess<T>() + (has_z ? to_f32(z) : 8.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(sf, __builtin_fmaf(-off, sx[i], acc[i]), y[i]);
         } else {
@@ -181,24 +184,36 @@ template <typename T, bool WIDE> __global__ __launch_bounds__(64 * kMvWaves) voi
             for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(sf, acc[i], y[i]);
         }
     };
-    const int64_t blocks = (p.K + 127) / 128;
-    Block next;
-    if (wave < blocks) fetch(wave, next);
-    for (int64_t b = wave; b < blocks; b += kMvWaves) {
-        const Block cur = next;
-        if (b + kMvWaves < blocks) fetch(b + kMvWaves, next);
-        uint32_t word[4] = {cur.w.x, cur.w.y, cur.w.z, cur.w.w};
-        f32x4 acc = {0, 0, 0, 0}, sx = {0, 0, 0, 0};
-        if (!WIDE) transpose_words(word);
+    const int blocks = (int)((p.K + 127) / 128);
+    Block ring[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            mv_mma<T>(cur.x[j], widen(word[j], T()), acc, sx, want_sx);
-            if (!WIDE) {
-                flush(acc, sx, cur.s[j], cur.z[j]);
-                acc = f32x4{0, 0, 0, 0}, sx = f32x4{0, 0, 0, 0};
+    for (int r = 0; r < kAhead; ++r)
+        if (wave + r * kMvWaves < blocks) fetch(wave + r * kMvWaves, ring[r]);
+    for (int b0 = wave; b0 < blocks; b0 += kMvWaves * kAhead) {
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            const int b = b0 + r * kMvWaves;
+            if (b >= blocks) break;
+            Block cur = ring[r];
+            if (b + kMvWaves * kAhead < blocks) fetch(b + kMvWaves * kAhead, ring[r]);
+            if (!WIDE && b == blocks - 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (b * 128 + 32 * j + 8 * kb >= K) cur.x[j].zero();
             }
+            uint32_t word[4] = {cur.w.x, cur.w.y, cur.w.z, cur.w.w};
+            f32x4 acc = {0, 0, 0, 0}, sx = {0, 0, 0, 0};
+            if (!WIDE) transpose_words(word);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mv_mma<T>(cur.x[j], widen(word[j], T()), acc, sx, want_sx);
+                if (!WIDE) {
+                    flush(acc, sx, cur.s[j], cur.z[j]);
+                    acc = f32x4{0, 0, 0, 0}, sx = f32x4{0, 0, 0, 0};
+                }
+            }
+            if (WIDE) flush(acc, sx, cur.s[0], cur.z[0]);
         }
-        if (WIDE) flush(acc, sx, cur.s[0], cur.z[0]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) s_acc[wave][kb * 4 + i][col] = y[i];
@@ -232,8 +247,13 @@ int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
     const bool wide = a.group % 128 == 0;
     const auto go = [&](auto t) {
         typedef decltype(t) T;
-        if (wide) mv4<T, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
-        else mv4<T, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
+        if (a.xs_k == 1 || a.K == 1) {
+            if (wide) mv4<T, true, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
+            else mv4<T, false, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
+        } else {
+            if (wide) mv4<T, true, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
+            else mv4<T, false, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
+        }
     };
     if (p.dtype == CONV_F32) go(float());
     else if (p.dtype == CONV_F16) go(f16_t());

@@ -13,38 +13,106 @@
 namespace miconv {
 namespace {
 
+constexpr int kTB = LM_SCAN_TB;      // steps of a tile: 8 channels of one row per staging thread
+
+template <int NS> struct FwdLds {
+    float2 in[2][kTB][kCH];                                          // d, d x
+    __attribute__((aligned(16))) float bc[2][kTB * 8 * NS];
+    __attribute__((aligned(16))) float y[2][kTB][kRow];
+};
+
+// The staging waves of one workgroup.
+template <typename T, int NS, bool PRE, bool DENSE>
+__device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdLds<NS> &sh, int tid)
+{
+    const int tr = tid >> 3, tc = (tid & 7) * 8;
+    const int tn = at.nc - tc;
+    const int64_t sc = at.c0 + tc;
+    const int shift = DENSE && sc > p.C - 8 ? (int)(sc - (p.C - 8)) : 0;
+    const bool any_shift = at.c0 + kCH > p.C;
+    const auto row_of = [&](const void *base, const S3 &st) {
+        return static_cast<const T *>(base) + at.sp.row0 * st.n + at.sp.start * st.l;
+    };
+    const T *px = row_of(p.x, p.xs), *pdt = row_of(p.dt, p.dts);
+    const bool has_z = !PRE && p.z;
+    const T *pz = has_z ? row_of(p.z, p.zs) : px;
+    const S3 zs = has_z ? p.zs : p.xs;
+    T *py = p.y ? const_cast<T *>(row_of(p.y, p.ys)) + sc * p.ys.c : nullptr;
+    float bias[8], D[8];
+    get_param<8>(p.bias, p.bias_s, sc, tn, bias);
+    get_param<8>(p.D, p.D_s, sc, tn, D);
+    Raw<T, 8> nx, ndt, nz, cx, cz, ox, oz;   // tile being loaded; in the core; leaving
+    BcRegs<T, NS, kTB, DENSE> bc(p, at, tid);
+    const auto fetch = [&](int64_t t) {
+        const int64_t l = t + tr < at.t1 ? t + tr : at.t1 - 1;
+        nx = get_row<T, 8, DENSE>(px + l * p.xs.l, p.xs.c, sc, p.C);
+        ndt = get_row<T, 8, DENSE>(pdt + l * p.dts.l, p.dts.c, sc, p.C);
+        if (!PRE) nz = get_row<T, 8, DENSE>(pz + l * zs.l, zs.c, sc, p.C);
+        bc.fetch(p, t, at.t1);
+    };
+    const auto stage = [&](int64_t t, int buf) {
+        if (any_shift) {
+            shift_row(nx, shift), shift_row(ndt, shift);
+            if (!PRE) shift_row(nz, shift);
+        }
+        const bool row_in = t + tr < at.t1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float d = ndt.f(i) + bias[i];
+            if (p.softplus) d = softplus(d);
+            const bool in = row_in && i < tn;
+            sh.in[buf][tr][tc + i] = make_float2(in ? d : 0.f, in ? d * nx.f(i) : 0.f);
+        }
+        bc.put(p, sh.bc[buf], t, at.t1);
+    };
+    const auto leave = [&](int64_t t, int buf) {
+        if (PRE || !py || t + tr >= at.t1) return;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[i] = __builtin_fmaf(D[i], ox.f(i), sh.y[buf][tr][tc + i]);
+            if (has_z) o[i] *= silu(oz.f(i));
+        }
+        put_row<T, 8>(py + (t + tr) * p.ys.l, p.ys.c, tn, o);
+    };
+    if (at.t0 < at.t1) {
+        fetch(at.t0);
+        stage(at.t0, 0);
+        cx = nx, cz = nz;
+        fetch(at.t0 + kTB);
+    }
+    lds_sync();
+    int buf = 0;
+    for (int64_t t = at.t0; t < at.t1; t += kTB, buf ^= 1) {
+        // The core is at tile t in buf.
+        stage(t + kTB, buf ^ 1);
+        const Raw<T, 8> sx = nx, sz = nz;
+        fetch(t + 2 * kTB);
+        if (t > at.t0) leave(t - kTB, buf ^ 1);
+        ox = cx, oz = cz, cx = sx, cz = sz;
+        lds_sync();
+    }
+    if (at.t0 < at.t1) leave(at.t0 + (at.t1 - 1 - at.t0) / kTB * kTB, buf ^ 1);
+}
+
 // PRE: only the state that leaves a chunk entered with zero, and the chunk's
 // sum of d (its decay is exp(A sum d)); the main pass folds them into the
 // state its chunk starts from.
-template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void scan_fwd(const ScanP p)
+template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) void scan_fwd(const ScanP p)
 {
     constexpr int CK = NS <= 4 ? 16 : 64 / NS;
-    __shared__ float2 s_in[kTB][kCH];
-    __shared__ __attribute__((aligned(16))) float s_bc[kTB * 8 * NS];
-    __shared__ __attribute__((aligned(16))) float s_y[PRE ? 1 : kTB][kRow];
-
+    __shared__ FwdLds<NS> sh;
     const ScanAt at = scan_at(p, PRE ? p.chunks - 1 : p.chunks);
     if (PRE ? at.t0 + p.chunk >= at.sp.len : (at.t0 >= at.sp.len && at.ch > 0)) return;
-
-    // Staging place: one row, eight channels.
-    const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
-    const int tn = at.nc - tc;
-    const int64_t sc = at.c0 + tc;
-    const auto row_of = [&](const void *base, const S3 &st) {
-        return static_cast<const T *>(base) + at.sp.row0 * st.n + sc * st.c + (at.sp.start + tr) * st.l;
-    };
-    const T *px = row_of(p.x, p.xs), *pdt = row_of(p.dt, p.dts);
-    const T *pz = p.z ? row_of(p.z, p.zs) : nullptr;
-    T *py = p.y ? const_cast<T *>(row_of(p.y, p.ys)) : nullptr;
-    float bias[8], D[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = p.bias && i < tn ? p.bias[(sc + i) * p.bias_s] : 0.f;
-        D[i] = p.D && i < tn ? p.D[(sc + i) * p.D_s] : 0.f;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= 4) {
+        if (p.dense) fwd_stage<T, NS, PRE, true>(p, at, sh, (int)threadIdx.x - 256);
+        else fwd_stage<T, NS, PRE, false>(p, at, sh, (int)threadIdx.x - 256);
+        return;
     }
 
-    // Core place: a quarter of one channel's states.
-    const int lane = threadIdx.x & 63, q = lane & 3, c = (threadIdx.x >> 6) * 16 + (lane >> 2);
+    // A quarter of one channel's states.
+    const int lane = threadIdx.x & 63, q = lane & 3, c = wave * 16 + (lane >> 2);
     const bool real = c < at.nc;
     const int64_t cc = at.c0 + c;
     float A2[NS], h[NS];
@@ -61,74 +129,45 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void s
                 h[i] = __builtin_fmaf(hw_exp2(d * A2[i]), h[i], p.carry_h[(k * 4 + q) * NS + i]);
         }
     }
-    float *saved = !PRE && p.saved && real ? p.saved + (saved_at<CK>(p, at) * p.C + cc) * 4 * NS + q * NS : nullptr;
+    float *saved = !PRE && p.saved && real
+                       ? p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * 4 * NS + q * NS : nullptr;
     float sum_d = 0.f;
-
-    Raw<T, 8> nx, ndt, nz;
-    BcRegs<T, NS> bc;
-    const auto fetch = [&](int64_t t) {
-        if (t + tr < at.t1) {
-            nx = get8(px + t * p.xs.l, p.xs.c, tn);
-            ndt = get8(pdt + t * p.dts.l, p.dts.c, tn);
-            if (!PRE && pz) nz = get8(pz + t * p.zs.l, p.zs.c, tn);
-        } else {
-            __builtin_memset(&nx, 0, sizeof(nx));
-        }
-        bc.fetch(p, at, t, at.t1);
-    };
-    fetch(at.t0);
-    for (int64_t t = at.t0; t < at.t1; t += kTB) {
-        const Raw<T, 8> x = nx, dt = ndt, z = nz;
-        const bool row_in = t + tr < at.t1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float d = 0.f;
-            if (row_in && i < tn) {
-                d = to_f32(dt.v[i]) + bias[i];
-                if (p.softplus) d = softplus(d);
-            }
-            s_in[tr][tc + i] = make_float2(d, d * to_f32(x.v[i]));
-        }
-        bc.put(s_bc);
-        if (t + kTB < at.t1) fetch(t + kTB);
-        __syncthreads();
+    lds_sync();
+    int buf = 0;
+    for (int64_t t = at.t0; t < at.t1; t += kTB, buf ^= 1) {
         const int steps = at.t1 - t < kTB ? (int)(at.t1 - t) : kTB;
-        for (int k = 0; k < steps; k += 4) {
-            if (!PRE && saved && k % CK == 0) {
-                float *o = saved + ((t + k) / CK) * p.C * 4 * NS;
+        // Four steps at a time, their LDS reads one group ahead; steps past
+        // the end have d = 0 and leave the state as it is.
+        Steps4<NS, !PRE> g[2];
+        g[0].load(sh.in[buf], sh.bc[buf], 0, c, q);
+        for (int k0 = 0; k0 < steps; k0 += 16) {
 #pragma unroll
-                for (int i = 0; i < NS; ++i) o[i] = h[i];
-            }
-            float y4[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = s_in[k + j][c];
-                const float *row = s_bc + (k + j) * 8 * NS + q * NS;
-                float b[NS], cv[NS];
-                lds_states<NS>(row, b);
-                if (!PRE) lds_states<NS>(row + 4 * NS, cv);
-                float y = 0.f;
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const float a = hw_exp2(v.x * A2[i]);
-                    h[i] = __builtin_fmaf(a, h[i], v.y * b[i]);
-                    if (!PRE) y = __builtin_fmaf(cv[i], h[i], y);
+            for (int kk = 0; kk < 16; kk += 4) {
+                const int k = k0 + kk;
+                const Steps4<NS, !PRE> &cur = g[kk / 4 & 1];
+                g[kk / 4 & 1 ^ 1].load(sh.in[buf], sh.bc[buf], (k + 4) % kTB, c, q);
+                if (!PRE && kk % CK == 0 && saved && k < steps) {
+                    store_f32<float, NS>(saved, h);
+                    saved += p.C * 4 * NS;
                 }
-                y4[j] = y;
-                if (PRE) sum_d += v.x;
-            }
-            if (!PRE) s_y[k + q][c] = quad_sum4(y4, q);
-        }
-        __syncthreads();
-        if (!PRE && py && row_in) {
-            float o[8];
+                float a[4][NS], y4[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                o[i] = __builtin_fmaf(D[i], to_f32(x.v[i]), s_y[tr][tc + i]);
-                if (pz) o[i] *= silu(to_f32(z.v[i]));
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) a[j][i] = hw_exp2(cur.v[j].x * A2[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        h[i] = __builtin_fmaf(a[j][i], h[i], cur.v[j].y * cur.b[j][i]);
+                        if (!PRE) y4[j] = i ? __builtin_fmaf(cur.c[j][i], h[i], y4[j]) : cur.c[j][0] * h[0];
+                    }
+                    if (PRE) sum_d += cur.v[j].x;
+                }
+                if (!PRE) sh.y[buf][k + q][c] = quad_sum4(y4, q);
             }
-            put8(py + t * p.ys.l, p.ys.c, tn, o);
         }
+        lds_sync();
     }
     if (!real) return;
     if (PRE) {
@@ -159,16 +198,25 @@ template <typename T, int NS> __global__ __launch_bounds__(256) void scan_step(c
         }
     }
     float h[NS], A[NS], b[NS], cv[NS];
-    get_states<NS>(p.s1, p.s1s, row, c, q * NS, p.S, h);
     const int64_t g = c / p.Cg;
     const T *pb = static_cast<const T *>(p.Bm) + n * p.Bs.n + g * p.Bs.g + q * NS * p.Bs.s;
     const T *pc = static_cast<const T *>(p.Cm) + n * p.Cs.n + g * p.Cs.g + q * NS * p.Cs.s;
+    float *ph = p.s1 + row * p.s1s.n + c * p.s1s.c + q * NS * p.s1s.l;
+    const float *pA = p.A + c * p.A_c + q * NS * p.A_s;
+    if (p.dense) {   // whole quarters of contiguous states: one access each
+        load_f32<float, NS>(ph, h);
+        load_f32<float, NS>(pA, A);
+        load_f32<T, NS>(pb, b);
+        load_f32<T, NS>(pc, cv);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const bool in = q * NS + i < p.S;
-        A[i] = in ? p.A[c * p.A_c + (q * NS + i) * p.A_s] : 0.f;
-        b[i] = in ? to_f32(pb[i * p.Bs.s]) : 0.f;
-        cv[i] = in ? to_f32(pc[i * p.Cs.s]) : 0.f;
+        for (int i = 0; i < NS; ++i) {
+            const bool in = q * NS + i < p.S;
+            h[i] = in ? ph[i * p.s1s.l] : 0.f;
+            A[i] = in ? pA[i * p.A_s] : 0.f;
+            b[i] = in ? to_f32(pb[i * p.Bs.s]) : 0.f;
+            cv[i] = in ? to_f32(pc[i * p.Cs.s]) : 0.f;
+        }
     }
     const float x = to_f32(static_cast<const T *>(p.x)[n * p.xs.n + c * p.xs.c]);
     float d = to_f32(static_cast<const T *>(p.dt)[n * p.dts.n + c * p.dts.c]);
@@ -181,7 +229,8 @@ template <typename T, int NS> __global__ __launch_bounds__(256) void scan_step(c
         h[i] = __builtin_fmaf(hw_exp2(d2 * A[i]), h[i], dx * b[i]);
         o = __builtin_fmaf(cv[i], h[i], o);
     }
-    put_states<NS>(p.s1, p.s1s, row, c, q * NS, p.S, h);
+    if (p.dense) store_f32<float, NS>(ph, h);
+    else put_states<NS>(p.s1, p.s1s, row, c, q * NS, p.S, h);
     o = quad_sum(o);
     if (q) return;
     if (p.D) o = __builtin_fmaf(p.D[c * p.D_s], x, o);
@@ -195,14 +244,15 @@ int launch_lm_scan(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
 {
     ScanP a = scan_params(p, q);
     if (a.seqs == 0) return CONV_OK;
+    a.dense = scan_dense(p, a, scan_ns(p.S));
     a.carry_d = static_cast<float *>(ws);
     a.carry_h = a.carry_d + lm_cdiv(a.seqs * (a.chunks - 1) * a.C, 4) * 4;
     with_type(p.dtype, [&](auto t) {
         with_ns(p.S, [&](auto n) {
             typedef decltype(t) T;
             constexpr int NS = decltype(n)::value;
-            if (a.chunks > 1) scan_fwd<T, NS, true><<<(int)(a.seqs * (a.chunks - 1) * a.blocks), 256, 0, s>>>(a);
-            scan_fwd<T, NS, false><<<(int)(a.seqs * a.chunks * a.blocks), 256, 0, s>>>(a);
+            if (a.chunks > 1) scan_fwd<T, NS, true><<<(int)(a.seqs * (a.chunks - 1) * a.blocks), kThreads, 0, s>>>(a);
+            scan_fwd<T, NS, false><<<(int)(a.seqs * a.chunks * a.blocks), kThreads, 0, s>>>(a);
         });
     });
     return lm_launch_status();
@@ -210,8 +260,9 @@ int launch_lm_scan(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
 
 int launch_lm_scan_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
 {
-    const ScanP a = scan_params(p, q);
+    ScanP a = scan_params(p, q);
     if (a.seqs == 0) return CONV_OK;
+    a.dense = p.S == 4 * scan_ns(p.S) && a.s1s.l == 1 && a.A_s == 1 && a.Bs.s == 1 && a.Cs.s == 1;
     with_type(p.dtype, [&](auto t) {
         with_ns(p.S, [&](auto n) {
             scan_step<decltype(t), decltype(n)::value><<<(int)lm_cdiv(a.seqs * a.C * 4, 256), 256, 0, s>>>(a);

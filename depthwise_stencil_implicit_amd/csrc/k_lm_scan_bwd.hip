@@ -21,29 +21,31 @@
 namespace miconv {
 namespace {
 
-// Sum of two values over lane pairs 8 (4) apart inside a row of 16: lanes with
-// bit 3 (2) clear receive the sum of a, the others that of b.  One asm block
-// for two pairs, with the two wait states that a cross-lane read of a register
-// needs after its last write by the vector unit.
-__device__ __forceinline__ void halve8(float a0, float b0, float a1, float b1, float &r0, float &r1)
+// Sums of eight values over the four channels of a row of 16 lanes, halving
+// the values with the lanes: over lanes 8 apart, where lanes with bit 3 clear
+// keep the even values' sums, then 4 apart likewise by bit 2.  The lane
+// receives z0 = sum of v[2 bit2 + bit3], z1 = sum of v[4 + 2 bit2 + bit3].
+// One asm block: a cross-lane read of a register needs two wait states after
+// its last write by the vector unit; the s_nop gives them to the inputs, two
+// instructions in between give them to each intermediate.
+__device__ __forceinline__ void halve_row(const float (&v)[8], float &z0, float &z1)
 {
+    float r0, r1, r2, r3;
     asm("s_nop 1\n\t"
-        "v_add_f32_dpp %0, %2, %2 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
-        "v_add_f32_dpp %0, %3, %3 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
-        "v_add_f32_dpp %1, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
-        "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc"
-        : "=&v"(r0), "=&v"(r1)
-        : "v"(a0), "v"(b0), "v"(a1), "v"(b1));
-}
-__device__ __forceinline__ void halve4(float a0, float b0, float a1, float b1, float &r0, float &r1)
-{
-    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %3, %8, %8 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %4, %10, %10 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %5, %12, %12 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %2, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %3, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %4, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
         "v_add_f32_dpp %0, %2, %2 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
         "v_add_f32_dpp %0, %3, %3 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
         "v_add_f32_dpp %1, %4, %4 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
         "v_add_f32_dpp %1, %5, %5 row_shr:4 row_mask:0xf bank_mask:0xa"
-        : "=&v"(r0), "=&v"(r1)
-        : "v"(a0), "v"(b0), "v"(a1), "v"(b1));
+        : "=&v"(z0), "=&v"(z1), "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3)
+        : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
 }
 // The same across rows: lanes of even (lower) rows receive the sum of a.
 __device__ __forceinline__ float halve16(float a, float b)
@@ -60,44 +62,163 @@ __device__ __forceinline__ float halve32(float a, float b)
 // receives that of v[4 bit4 + 2 bit2 + bit3] -- still to be added over bit 5.
 __device__ __forceinline__ float halve_channels(const float (&v)[8])
 {
-    float r0, r1, r2, r3, z0, z1;
-    halve8(v[0], v[1], v[2], v[3], r0, r1);
-    halve8(v[4], v[5], v[6], v[7], r2, r3);
-    halve4(r0, r1, r2, r3, z0, z1);
+    float z0, z1;
+    halve_row(v, z0, z1);
     return halve16(z0, z1);
+}
+
+// Steps of a tile: what LDS holds twice.
+template <int NS> constexpr int bwd_tile() { return NS <= 4 ? 32 : 128 / NS; }
+
+template <int NS, bool PRE> struct BwdLds {
+    static constexpr int TB = bwd_tile<NS>();
+    float2 in[2][TB][kCH];                                         // d, d x
+    float s[2][TB][kCH];                                           // gy silu(z)
+    __attribute__((aligned(16))) float bc[2][TB * 8 * NS];
+    __attribute__((aligned(16))) float o[PRE ? 1 : 2][3][PRE ? 1 : TB][kRow];   // sums over s of r B, r A a h, C h
+    float red[PRE ? 1 : 2][4][PRE ? 1 : TB][8 * NS];               // a wave's dB, dC
+};
+
+// The staging waves: tiles in descending order.
+template <typename T, int NS, bool PRE, bool DENSE>
+__device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdLds<NS, PRE> &sh, int tid)
+{
+    constexpr int TB = bwd_tile<NS>(), V = TB / 4;
+    const int tr = tid / (256 / TB), tc = tid % (256 / TB) * V;
+    const int tn = at.nc - tc;
+    const int64_t sc = at.c0 + tc;
+    const int shift = DENSE && sc > p.C - V ? (int)(sc - (p.C - V)) : 0;
+    const bool any_shift = at.c0 + kCH > p.C, has_z = p.z != nullptr;
+    const auto row_of = [&](const void *base, const S3 &st) {
+        return static_cast<const T *>(base) + at.sp.row0 * st.n + at.sp.start * st.l;
+    };
+    const T *px = row_of(p.x, p.xs), *pdt = row_of(p.dt, p.dts), *pgy = row_of(p.gy, p.gys);
+    const T *pz = has_z ? row_of(p.z, p.zs) : px;
+    const S3 zs = has_z ? p.zs : p.xs;
+    float bias[V], D[V], sum_D[V] = {}, sum_b[V] = {};
+    get_param<V>(p.bias, p.bias_s, sc, tn, bias);
+    get_param<V>(p.D, p.D_s, sc, tn, D);
+    struct Tile { Raw<T, V> x, dt, z, gy; } nt, ct, ot;   // being loaded; in the core; leaving
+    BcRegs<T, NS, TB, DENSE> bc(p, at, tid);
+    const auto fetch = [&](int64_t t) {
+        int64_t l = t + tr < at.t1 ? t + tr : at.t1 - 1;
+        if (l < at.t0) l = at.t0;   // before the chunk: loaded for nothing
+        nt.x = get_row<T, V, DENSE>(px + l * p.xs.l, p.xs.c, sc, p.C);
+        nt.dt = get_row<T, V, DENSE>(pdt + l * p.dts.l, p.dts.c, sc, p.C);
+        nt.gy = get_row<T, V, DENSE>(pgy + l * p.gys.l, p.gys.c, sc, p.C);
+        nt.z = get_row<T, V, DENSE>(pz + l * zs.l, zs.c, sc, p.C);
+        bc.fetch(p, t < at.t0 ? at.t0 : t, at.t1);
+    };
+    const auto stage = [&](int64_t t, int buf) {
+        if (any_shift) shift_row(nt.x, shift), shift_row(nt.dt, shift), shift_row(nt.gy, shift), shift_row(nt.z, shift);
+        const bool row_in = t + tr < at.t1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float d = nt.dt.f(i) + bias[i];
+            if (p.softplus) d = softplus(d);
+            const bool in = row_in && i < tn;
+            sh.in[buf][tr][tc + i] = make_float2(in ? d : 0.f, in ? d * nt.x.f(i) : 0.f);
+            float s = nt.gy.f(i);
+            if (has_z) s *= silu(nt.z.f(i));
+            sh.s[buf][tr][tc + i] = in ? s : 0.f;
+        }
+        bc.put(p, sh.bc[buf], t, at.t1);
+    };
+    const auto leave = [&](int64_t t, int buf) {
+        if constexpr (!PRE) {
+            const int rows = at.t1 - t < TB ? (int)(at.t1 - t) : TB;
+            float *part = p.part_bc + (((at.c0 - at.g * p.Cg) / kCH + at.g * p.blocks_g) * p.rows_total +
+                                       at.sp.row0 * p.L + at.sp.start + t) * 8 * NS;
+            const float *red = &sh.red[buf][0][0][0];
+            constexpr int n = TB * 8 * NS;
+            for (int e = tid; e < rows * 8 * NS; e += 256)
+                part[e] = (red[e] + red[n + e]) + (red[2 * n + e] + red[3 * n + e]);
+            if (t + tr >= at.t1) return;
+            float ox[V], od[V], oz[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xv = ot.x.f(i), g = ot.gy.f(i), raw = ot.dt.f(i) + bias[i];
+                const float d = p.softplus ? softplus(raw) : raw;
+                float s = g;
+                if (has_z) {
+                    const float zv = ot.z.f(i), qz = sigmoid(zv);
+                    s *= zv * qz;
+                    oz[i] = g * __builtin_fmaf(D[i], xv, sh.o[buf][2][tr][tc + i]) * silu_slope(zv, qz);
+                }
+                const float rb = sh.o[buf][0][tr][tc + i];
+                ox[i] = __builtin_fmaf(D[i], s, d * rb);
+                float dd = __builtin_fmaf(xv, rb, sh.o[buf][1][tr][tc + i]);
+                if (p.softplus) dd *= sigmoid(raw);
+                od[i] = dd;
+                sum_b[i] += i < tn ? dd : 0.f;
+                sum_D[i] += i < tn ? s * xv : 0.f;
+            }
+            const auto put = [&](void *base, const S3 &st, const float (&v)[V]) {
+                put_row<T, V>(static_cast<T *>(base) + at.sp.row0 * st.n + sc * st.c + (at.sp.start + t + tr) * st.l, st.c, tn,
+                              v);
+            };
+            put(p.dx, p.dxs, ox);
+            put(p.ddt, p.ddts, od);
+            if (has_z) put(p.dz, p.dzs, oz);
+        }
+    };
+    const int tiles = (int)((at.t1 - at.t0 + TB - 1) / TB);
+    const auto at_tile = [&](int k) { return at.t0 + (int64_t)k * TB; };
+    if (tiles > 0) {
+        fetch(at_tile(tiles - 1));
+        stage(at_tile(tiles - 1), 0);
+        ct = nt;
+        fetch(at_tile(tiles - 2));
+    }
+    lds_sync();
+    int buf = 0;
+    for (int k = tiles - 1; k >= 0; --k, buf ^= 1) {
+        // The core is at tile k in buf.
+        if (k > 0) stage(at_tile(k - 1), buf ^ 1);
+        const Tile st = nt;
+        fetch(at_tile(k - 2));
+        if (k < tiles - 1) leave(at_tile(k + 1), buf ^ 1);
+        ot = ct, ct = st;
+        lds_sync();
+    }
+    if (tiles > 0) leave(at_tile(0), buf ^ 1);
+    if constexpr (!PRE) {
+        // Sums of D's and the bias's gradients over the rows of the staging waves.
+        float(*sum)[kRow] = sh.o[0][0];
+        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (4 * NS + 2);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            lds_sync();
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[tr][tc + i] = which ? sum_b[i] : sum_D[i];
+            lds_sync();
+            if (tid < at.nc) {
+                float v = 0.f;
+                for (int k = 0; k < TB; ++k) v += sum[k][tid];
+                pc[tid * (4 * NS + 2) + 4 * NS + which] = v;
+            }
+        }
+    }
 }
 
 // PRE: only the gradient that leaves a chunk at its front when none enters at
 // its end, and the chunk's sum of d.
-template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void scan_bwd(const ScanP p)
+template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) void scan_bwd(const ScanP p)
 {
-    constexpr int CK = NS <= 4 ? 16 : 64 / NS;
+    constexpr int CK = NS <= 4 ? 16 : 64 / NS, TB = bwd_tile<NS>();
     constexpr int NB = NS < 4 ? 4 : NS;      // states per lane in the exchanges
-    __shared__ float2 s_in[kTB][kCH];        // d, d x
-    __shared__ float s_s[kTB][kCH];          // s = gy silu(z)
-    __shared__ __attribute__((aligned(16))) float s_bc[kTB * 8 * NS];
-    __shared__ __attribute__((aligned(16))) float s_o[PRE ? 1 : 3][PRE ? 1 : kTB][kRow];   // sums over s of r B, r A a h, C h
-    __shared__ float s_red[PRE ? 1 : 4][PRE ? 1 : kTB][8 * NS];
-
+    __shared__ BwdLds<NS, PRE> sh;
     const ScanAt at = scan_at(p, p.chunks);
     if (at.t0 >= at.sp.len && at.ch > 0) return;
     if (PRE && at.ch == 0) return;
-
-    const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
-    const int tn = at.nc - tc;
-    const int64_t sc = at.c0 + tc;
-    const auto row_of = [&](const void *base, const S3 &st) {
-        return base ? static_cast<const T *>(base) + at.sp.row0 * st.n + sc * st.c + (at.sp.start + tr) * st.l : nullptr;
-    };
-    const T *px = row_of(p.x, p.xs), *pdt = row_of(p.dt, p.dts), *pz = row_of(p.z, p.zs), *pgy = row_of(p.gy, p.gys);
-    float bias[8], D[8], sum_D[8] = {}, sum_b[8] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = p.bias && i < tn ? p.bias[(sc + i) * p.bias_s] : 0.f;
-        D[i] = p.D && i < tn ? p.D[(sc + i) * p.D_s] : 0.f;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= 4) {
+        if (p.dense) bwd_stage<T, NS, PRE, true>(p, at, sh, (int)threadIdx.x - 256);
+        else bwd_stage<T, NS, PRE, false>(p, at, sh, (int)threadIdx.x - 256);
+        return;
     }
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 3, c = wave * 16 + (lane >> 2);
+    const int lane = threadIdx.x & 63, q = lane & 3, c = wave * 16 + (lane >> 2);
     const bool real = c < at.nc;
     const int64_t cc = at.c0 + c;
     float A[NS], dA[NS] = {}, r[NS] = {};    // r: the gradient that enters from the step behind
@@ -115,81 +236,56 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void s
                 r[i] = __builtin_fmaf(hw_exp2(d * A[i]), r[i], p.carry_h[(k * 4 + q) * NS + i]);
         }
     }
-    const float *saved = p.saved + (saved_at<CK>(p, at) * p.C + cc) * 4 * NS + q * NS;
+    const float *saved = p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * 4 * NS + q * NS;
     float sum_d = 0.f;
-
-    Raw<T, 8> nx, ndt, nz, ng;
-    BcRegs<T, NS> bc;
-    float nh[kTB / CK][NS];
-    const auto fetch = [&](int64_t t) {
-        __builtin_memset(&nx, 0, sizeof(nx));
-        __builtin_memset(&ndt, 0, sizeof(ndt));
-        __builtin_memset(&nz, 0, sizeof(nz));
-        __builtin_memset(&ng, 0, sizeof(ng));
-        if (t + tr < at.t1) {
-            nx = get8(px + t * p.xs.l, p.xs.c, tn);
-            ndt = get8(pdt + t * p.dts.l, p.dts.c, tn);
-            ng = get8(pgy + t * p.gys.l, p.gys.c, tn);
-            if (pz) nz = get8(pz + t * p.zs.l, p.zs.c, tn);
-        }
-        bc.fetch(p, at, t, at.t1);
-        if (!PRE) {
+    const int tiles = (int)((at.t1 - at.t0 + TB - 1) / TB);
+    float nh[2][NS] = {};                    // states saved in a tile, loaded a tile ahead
+    const auto fetch = [&](int k) {
+        if (PRE || k < 0) return;
 #pragma unroll
-            for (int k = 0; k < kTB / CK; ++k)
-#pragma unroll
-                for (int i = 0; i < NS; ++i)
-                    nh[k][i] = real && t + k * CK < at.t1 ? saved[(t / CK + k) * p.C * 4 * NS + i] : 0.f;
+        for (int j = 0; j < 2; ++j) {
+            if (real && at.t0 + (int64_t)k * TB + j * CK < at.t1)
+                load_f32<float, NS>(saved + ((int64_t)k * 2 + j) * p.C * 4 * NS, nh[j]);
         }
     };
-    const int64_t tiles = (at.t1 - at.t0 + kTB - 1) / kTB;
-    if (tiles > 0) fetch(at.t0 + (tiles - 1) * kTB);
-    for (int64_t tile = tiles - 1; tile >= 0; --tile) {
-        const int64_t t = at.t0 + tile * kTB;
-        const Raw<T, 8> x = nx, dt = ndt, z = nz, gy = ng;
-        float h0[kTB / CK][NS];
-#pragma unroll
-        for (int k = 0; k < kTB / CK; ++k)
-#pragma unroll
-            for (int i = 0; i < NS; ++i) h0[k][i] = nh[k][i];
-        const bool row_in = t + tr < at.t1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float d = 0.f;
-            if (row_in && i < tn) {
-                d = to_f32(dt.v[i]) + bias[i];
-                if (p.softplus) d = softplus(d);
-            }
-            s_in[tr][tc + i] = make_float2(d, d * to_f32(x.v[i]));
-            float s = to_f32(gy.v[i]);
-            if (pz) s *= silu(to_f32(z.v[i]));
-            s_s[tr][tc + i] = s;
-        }
-        bc.put(s_bc);
-        if (tile > 0) fetch(t - kTB);
-        __syncthreads();
-        if (PRE) {
-            for (int k = kTB - 1; k >= 0; --k) {
-                const float2 v = s_in[k][c];
-                const float s = s_s[k][c], d2 = v.x * kLog2e;
+    fetch(tiles - 1);
+    lds_sync();
+    int buf = 0;
+    for (int tile = tiles - 1; tile >= 0; --tile, buf ^= 1) {
+        const int64_t t = at.t0 + (int64_t)tile * TB;
+        const float2(*in)[kCH] = sh.in[buf];
+        const float(*ss)[kCH] = sh.s[buf];
+        const float *bc = sh.bc[buf];
+        if constexpr (PRE) {
+            for (int k = TB - 1; k >= 0; --k) {
+                const float2 v = in[k][c];
+                const float s = ss[k][c], d2 = v.x * kLog2e;
                 float cv[NS];
-                lds_states<NS>(s_bc + k * 8 * NS + 4 * NS + q * NS, cv);
+                lds_states<NS>(bc + k * 8 * NS + 4 * NS + q * NS, cv);
 #pragma unroll
                 for (int i = 0; i < NS; ++i) r[i] = hw_exp2(d2 * A[i]) * __builtin_fmaf(cv[i], s, r[i]);
                 sum_d += v.x;
             }
         } else {
+            float h0[2][NS];
 #pragma unroll
-            for (int part = kTB / CK - 1; part >= 0; --part) {
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) h0[j][i] = nh[j][i];
+            fetch(tile - 1);
+#pragma unroll 1
+            for (int part = 1; part >= 0; --part) {
                 if (t + part * CK >= at.t1) continue;
+                const int row0 = part * CK;
                 float a[CK][NS], u[CK][NS], h[NS];
 #pragma unroll
-                for (int i = 0; i < NS; ++i) h[i] = h0[part][i];
+                for (int i = 0; i < NS; ++i) h[i] = part ? h0[1][i] : h0[0][i];
 #pragma unroll
                 for (int k = 0; k < CK; ++k) {
-                    const float2 v = s_in[part * CK + k][c];
+                    const float2 v = in[row0 + k][c];
                     const float d2 = v.x * kLog2e;
                     float b[NS];
-                    lds_states<NS>(s_bc + (part * CK + k) * 8 * NS + q * NS, b);
+                    lds_states<NS>(bc + (row0 + k) * 8 * NS + q * NS, b);
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
                         a[k][i] = hw_exp2(d2 * A[i]);
@@ -200,12 +296,12 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void s
                 float o4[3][4], pair[NB / 4];
 #pragma unroll
                 for (int k = CK - 1; k >= 0; --k) {
-                    const int row = part * CK + k;
-                    const float2 v = s_in[row][c];
-                    const float s = s_s[row][c];
+                    const int row = row0 + k;
+                    const float2 v = in[row][c];
+                    const float s = ss[row][c];
                     float b[NS], cv[NS], vb[NB], vc[NB];
-                    lds_states<NS>(s_bc + row * 8 * NS + q * NS, b);
-                    lds_states<NS>(s_bc + row * 8 * NS + 4 * NS + q * NS, cv);
+                    lds_states<NS>(bc + row * 8 * NS + q * NS, b);
+                    lds_states<NS>(bc + row * 8 * NS + 4 * NS + q * NS, cv);
                     float rb = 0.f, ra = 0.f, ch = 0.f;
 #pragma unroll
                     for (int i = 0; i < NB; ++i) vb[i] = vc[i] = 0.f;
@@ -225,7 +321,7 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void s
                     o4[0][k & 3] = rb, o4[1][k & 3] = ra, o4[2][k & 3] = ch;
                     if ((k & 3) == 0) {
 #pragma unroll
-                        for (int j = 0; j < 3; ++j) s_o[j][row + q][c] = quad_sum4(o4[j], q);
+                        for (int j = 0; j < 3; ++j) sh.o[buf][j][row + q][c] = quad_sum4(o4[j], q);
                     }
                     // dB and dC of two steps meet in the last exchange.
 #pragma unroll
@@ -238,74 +334,29 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(256) void s
                             const float both = halve32(got, pair[m]);
                             const int i = 4 * m + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1);
                             if (i < NS)
-                                s_red[wave][row + (lane >> 5)][((lane >> 4) & 1) * 4 * NS + q * NS + i] = both;
+                                sh.red[buf][wave][row + (lane >> 5)][((lane >> 4) & 1) * 4 * NS + q * NS + i] = both;
                         }
                     }
                 }
             }
         }
-        __syncthreads();
-        if (PRE) continue;
-        // The workgroup's parts of dB and dC.
-        const int rows = at.t1 - t < kTB ? (int)(at.t1 - t) : kTB;
-        float *part = p.part_bc + (((at.c0 - at.g * p.Cg) / kCH + at.g * p.blocks_g) * p.rows_total +
-                                   at.sp.row0 * p.L + at.sp.start + t) * 8 * NS;
-        for (int e = threadIdx.x; e < rows * 8 * NS; e += 256) {
-            const int k = e / (8 * NS), j = e % (8 * NS);
-            part[e] = (s_red[0][k][j] + s_red[1][k][j]) + (s_red[2][k][j] + s_red[3][k][j]);
-        }
-        if (row_in) {
-            float ox[8], od[8], oz[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = s_in[tr][tc + i].x, s = s_s[tr][tc + i], xv = to_f32(x.v[i]);
-                const float rb = s_o[0][tr][tc + i];
-                ox[i] = __builtin_fmaf(D[i], s, d * rb);
-                float dd = __builtin_fmaf(xv, rb, s_o[1][tr][tc + i]);
-                if (p.softplus) dd *= sigmoid(to_f32(dt.v[i]) + bias[i]);
-                od[i] = dd;
-                sum_b[i] += dd;
-                sum_D[i] = __builtin_fmaf(s, xv, sum_D[i]);
-                const float zv = to_f32(z.v[i]);
-                oz[i] = to_f32(gy.v[i]) * __builtin_fmaf(D[i], xv, s_o[2][tr][tc + i]) * silu_slope(zv, sigmoid(zv));
-            }
-            const auto put = [&](void *base, const S3 &st, const float (&v)[8]) {
-                put8(static_cast<T *>(base) + at.sp.row0 * st.n + sc * st.c + (at.sp.start + t + tr) * st.l, st.c, tn, v);
-            };
-            put(p.dx, p.dxs, ox);
-            put(p.ddt, p.ddts, od);
-            if (pz) put(p.dz, p.dzs, oz);
-        }
-        // The next tile's staging overwrites s_in, s_s and s_bc only.
-        __syncthreads();
+        lds_sync();
     }
-    if (PRE) {
+    if constexpr (PRE) {
         if (!real) return;
         const int64_t k = (at.seq * p.chunks + at.ch) * p.C + cc;
 #pragma unroll
         for (int i = 0; i < NS; ++i) p.carry_h[(k * 4 + q) * NS + i] = r[i];
         if (q == 0) p.carry_d[k] = sum_d;
-        return;
-    }
-    if (real && p.ds && at.ch == 0) put_states<NS>(p.ds, p.dss, at.seq, cc, q * NS, p.S, r);
-    // Parts of dA (4 NS per channel), dD and the bias, laid out [part][channel][4 NS + 2].
-    float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (4 * NS + 2);
-    if (real) {
+    } else {
+        // The staging waves' four barriers of the last sums.
+        for (int k = 0; k < 4; ++k) lds_sync();
+        if (!real) return;
+        if (p.ds && at.ch == 0) put_states<NS>(p.ds, p.dss, at.seq, cc, q * NS, p.S, r);
+        // Parts of dA (4 NS per channel), dD and the bias, laid out [part][channel][4 NS + 2].
+        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (4 * NS + 2);
 #pragma unroll
         for (int i = 0; i < NS; ++i) pc[c * (4 * NS + 2) + q * NS + i] = dA[i];
-    }
-    float (&sum)[kTB][kRow] = reinterpret_cast<float (&)[kTB][kRow]>(s_o[0]);
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[tr][tc + i] = which ? sum_b[i] : sum_D[i];
-        __syncthreads();
-        if ((int)threadIdx.x < at.nc) {
-            float v = 0.f;
-            for (int k = 0; k < kTB; ++k) v += sum[k][threadIdx.x];
-            pc[threadIdx.x * (4 * NS + 2) + 4 * NS + which] = v;
-        }
     }
 }
 
@@ -363,14 +414,15 @@ int launch_lm_scan_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     a.part_c = f, f += lm_cdiv(a.seqs * a.chunks * a.C * (W + 2), 4) * 4;
     a.carry_d = f, f += lm_cdiv(a.seqs * a.chunks * a.C, 4) * 4;
     a.carry_h = f;
+    a.dense = scan_dense(p, a, W <= 16 ? W / 4 : 4);
     const int grid = (int)(a.seqs * a.chunks * a.blocks);
     with_type(p.dtype, [&](auto t) {
         typedef decltype(t) T;
         with_ns(p.S, [&](auto n) {
             constexpr int NS = decltype(n)::value;
             if (grid == 0) return;
-            if (a.chunks > 1) scan_bwd<T, NS, true><<<grid, 256, 0, s>>>(a);
-            scan_bwd<T, NS, false><<<grid, 256, 0, s>>>(a);
+            if (a.chunks > 1) scan_bwd<T, NS, true><<<grid, kThreads, 0, s>>>(a);
+            scan_bwd<T, NS, false><<<grid, kThreads, 0, s>>>(a);
         });
         if (a.rows_total > 0) scan_bwd_bc<T><<<(int)lm_cdiv(a.rows_total * 2 * W * p.G, 256), 256, 0, s>>>(
             a.part_bc, a.rows_total, p.L, a.blocks_g, (int)p.G, (int)p.S, W, static_cast<T *>(q[LM_DB]),

@@ -46,29 +46,63 @@ __device__ __forceinline__ float softplus(float v)
     return fmaxf(v, 0.f) + __builtin_fmaf(kLn2, hw_log2(u), lost);
 }
 
+// V elements as they are in memory, held as 32-bit words (held as elements, a
+// 16-bit one would take a register of its own).
+template <typename T, int V> struct Raw {
+    static constexpr int n = (V * (int)sizeof(T) + 3) / 4;
+    uint32_t w[n];
+    __device__ __forceinline__ float f(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return i & 1 ? hi_f32(w[i / 2], T()) : lo_f32(w[i / 2], T());
+    }
+    __device__ __forceinline__ void set(int i, T v)   // on words that are zero there
+    {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v);
+        else w[i / 2] |= (uint32_t)v.u << (i & 1 ? 16 : 0);
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < n; ++i) w[i] = 0;
+    }
+};
 // V consecutive elements from any element-aligned address (one wide load: the
 // hardware takes unaligned global accesses).
 template <typename T, int V> struct __attribute__((packed, aligned(sizeof(T)))) Pack { T v[V]; };
-template <typename T, int V> struct Raw { T v[V]; };
 template <typename T, int V> __device__ __forceinline__ Raw<T, V> load_raw(const T *p)
 {
     Raw<T, V> r;
-    __builtin_memcpy(&r, reinterpret_cast<const Pack<T, V> *>(p), sizeof(r));
+    if constexpr (V * sizeof(T) < 4) r.w[0] = p->u;
+    else __builtin_memcpy(r.w, reinterpret_cast<const Pack<T, V> *>(p), sizeof(r));
     return r;
 }
 template <typename T, int V> __device__ __forceinline__ void load_f32(const T *p, float (&o)[V])
 {
     const Raw<T, V> r = load_raw<T, V>(p);
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = to_f32(r.v[i]);
+    for (int i = 0; i < V; ++i) o[i] = r.f(i);
 }
 template <typename T, int V> __device__ __forceinline__ void store_f32(T *p, const float (&v)[V])
 {
-    Raw<T, V> r;
+    if constexpr (V == 1) *p = from_f32<T>(v[0]);
+    else {
+        Raw<T, V> r;
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = from_f32<T>(v[i]);
-    __builtin_memcpy(reinterpret_cast<Pack<T, V> *>(p), &r, sizeof(r));
+            for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) r.w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+        }
+        __builtin_memcpy(reinterpret_cast<Pack<T, V> *>(p), r.w, sizeof(r));
+    }
 }
+
+// A workgroup barrier that waits for this wave's LDS accesses only.
+// __syncthreads() would also drain the loads of the next tile, which are meant
+// to stay in flight across it.
+__device__ __forceinline__ void lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Element strides of a [rows, channels, positions] tensor.
 struct S3 { int64_t n, c, l; };

@@ -202,7 +202,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
             k.fail(CONV_EUNSUPPORTED, "w needs contiguous rows a multiple of 16 bytes apart");
             return k.status;
         }
-        if (lm_cdiv(p.seqs, 16) > 65535 || lm_cdiv(p.C, 16) > 0x7fffffff) {
+        if (p.K > 0x7fffff00 || lm_cdiv(p.seqs, 16) > 65535 || lm_cdiv(p.C, 16) > 0x7fffffff) {
             k.fail(CONV_EUNSUPPORTED, "too many rows");
             return k.status;
         }
@@ -283,7 +283,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
 
     const int64_t rows = packed ? p.L : N * p.L, cells = rows * p.C;
     if (conv) {
-        if (!step) conv_chunks(p, max_len, bwd ? 4 : 16 / e, bwd ? 32 : 16);
+        if (!step) conv_chunks(p, max_len, bwd ? 4 : 16 / e, bwd ? 32 : 8);
         else p.chunk = p.chunks = 1;
         if (bwd && (k.has(LM_DW) || k.has(LM_DBIAS))) p.workspace_bytes = p.seqs * p.chunks * p.C * (p.K + 1) * 4;
         const int64_t st = p.seqs * p.C * (p.K - 1) * e * ((k.has(LM_STATE_IN) || step) + k.has(LM_STATE_OUT) + k.has(LM_GSTATE) + k.has(LM_DSTATE));

@@ -1,13 +1,15 @@
 // What the scan's kernels share: parameters, the staged tile and cross-lane sums.
 //
-// A workgroup of four waves owns 64 channels of one group and walks along the
-// sequence in tiles of 32 steps.  Four neighbouring lanes share a channel and
-// hold NS states each (S <= 4 NS; states past S have A = B = C = 0).  Per tile
-// the threads stage d = softplus(dt + dt_bias) and d x, which need one
-// transcendental chain per (step, channel), once for the four lanes, next to
-// B and C in f32; thread (row, 8 channels) of the staging also applies D, the
-// gate and the stores afterwards, so x, dt and z cross from HBM once and stay
-// in its registers.
+// A workgroup owns 64 channels of one group and walks along the sequence in
+// tiles.  Four core waves run the recurrence: four neighbouring lanes share a
+// channel and hold NS states each (S <= 4 NS; states past S have A = B = C = 0).
+// Four staging waves work a tile ahead of them and one behind: they load a
+// tile, put d = softplus(dt + dt_bias) and d x -- one transcendental chain per
+// (step, channel), not four -- and B and C in f32 into LDS, and take the core's
+// sums out again through D, the gate and the stores.  x, dt and z cross from
+// HBM once and stay in the staging waves' registers between the two.  With one
+// kind of wave that did both in turn, a SIMD stood idle at every barrier and
+// behind every store: 200 us for 8 x 1024 x 2048 channels of 16 states.
 #pragma once
 
 #include <type_traits>
@@ -32,31 +34,62 @@ struct ScanP {
     S3 s0s, s1s, gss, dss;           // (sequence, channel, state)
     int64_t A_c, A_s, D_s, bias_s;
     int64_t seqs, C, L, S, chunk, chunks, Cg, blocks_g, blocks, rows_total, state_rows;
-    int softplus;
+    int softplus, dense;
 };
 
-constexpr int kCH = LM_SCAN_CH, kTB = LM_SCAN_TB;
+constexpr int kCH = LM_SCAN_CH;
+constexpr int kThreads = 512;        // four core waves, four staging waves
 constexpr int kRow = kCH + 16;       // padded f32 row: four rows x 16 channels on 64 banks
 
-// Eight channels of one row, as they are in memory; channels >= n are zero.
-template <typename T> __device__ __forceinline__ Raw<T, 8> get8(const T *p, int64_t cs, int n)
+// Loads of a staging thread never stand behind a branch: a register that two
+// paths may have written is settled, and so waited for, where they meet, and
+// the loads of a tile would go out one by one (they did: 2 us each).  Rows and
+// channels past the end are clamped to the last ones instead, and masked when
+// the values are used.
+//
+// V channels of one row from c0 on.  DENSE: channels are contiguous and the
+// tensor has at least V of them; a group that would pass the end starts at
+// C - V, and shift_row moves its channels into place.
+template <typename T, int V, bool DENSE>
+__device__ __forceinline__ Raw<T, V> get_row(const T *row, int64_t cs, int64_t c0, int64_t C)
 {
-    if (cs == 1 && n >= 8) return load_raw<T, 8>(p);
-    Raw<T, 8> r;
-    __builtin_memset(&r, 0, sizeof(r));
+    if constexpr (DENSE) return load_raw<T, V>(row + (c0 < C - V ? c0 : C - V));
+    else {
+        Raw<T, V> r;
+        r.zero();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) r.v[i] = p[i * cs];
-    return r;
+        for (int i = 0; i < V; ++i) r.set(i, row[(c0 + i < C ? c0 + i : C - 1) * cs]);
+        return r;
+    }
 }
-template <typename T> __device__ __forceinline__ void put8(T *p, int64_t cs, int n, const float (&v)[8])
+template <typename T, int V> __device__ __forceinline__ void shift_row(Raw<T, V> &r, int by)
 {
-    if (cs == 1 && n >= 8) store_f32<T, 8>(p, v);
+    constexpr int n = Raw<T, V>::n, per = 4 / sizeof(T);   // words, elements of a word
+    if (per == 2 && (by & 1)) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) r.w[i] = r.w[i] >> 16 | (i + 1 < n ? r.w[i + 1] << 16 : 0);
+    }
+#pragma unroll
+    for (int s = 1; s < n; s *= 2)
+        if (by & s * per) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) r.w[i] = i + s < n ? r.w[i + s] : 0;
+        }
+}
+template <typename T, int V> __device__ __forceinline__ void put_row(T *p, int64_t cs, int n, const float (&v)[V])
+{
+    if (cs == 1 && n >= V) store_f32<T, V>(p, v);
     else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < V; ++i)
             if (i < n) p[i * cs] = from_f32<T>(v[i]);
     }
+}
+// V values per channel of an f32 parameter, zero without it or past the end.
+template <int V> __device__ __forceinline__ void get_param(const float *p, int64_t st, int64_t c0, int n, float (&o)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = p && i < n ? p[(c0 + i) * st] : 0.f;
 }
 
 // Where a workgroup stands.
@@ -90,37 +123,40 @@ template <int CK> __device__ __forceinline__ int64_t saved_at(const ScanP &p, co
     return p.off ? a.sp.start / CK + a.seq : a.seq * ((p.L + CK - 1) / CK);
 }
 
-// B and C of a tile on their way to LDS: element e of a thread is state
-// e % (4 NS) of row e / (4 NS) of B, then of C.
-template <typename T, int NS> struct BcRegs {
-    static constexpr int n = 2 * kTB * 4 * NS / 256;
-    T v[n];
-    __device__ __forceinline__ void fetch(const ScanP &p, const ScanAt &a, int64_t t, int64_t t1)
+// B and C of a tile on their way to LDS: threads 0 .. 127 hold n neighbouring
+// states of one row of B, threads 128 .. 255 of C.  DENSE: states are
+// contiguous and S a multiple of n.
+template <typename T, int NS, int TB, bool DENSE> struct BcRegs {
+    static constexpr int n = TB * 4 * NS / 128;
+    Raw<T, n> v;
+    const T *base;
+    int64_t sl;
+    int row, s0, to;
+    __device__ __forceinline__ BcRegs(const ScanP &p, const ScanAt &a, int tid)
     {
+        const int e = tid % 128 * n;
+        const S4 &st = tid < 128 ? p.Bs : p.Cs;
+        row = e / (4 * NS), s0 = e % (4 * NS);
+        to = row * (8 * NS) + (tid < 128 ? 0 : 4 * NS) + s0;
+        base = static_cast<const T *>(tid < 128 ? p.Bm : p.Cm) + a.sp.row0 * st.n + a.g * st.g + a.sp.start * st.l;
+        if (DENSE) base += s0 < p.S ? s0 : 0;
+        sl = st.l;
+    }
+    __device__ __forceinline__ void fetch(const ScanP &p, int64_t t, int64_t t1)
+    {
+        const T *q = base + (t + row < t1 ? t + row : t1 - 1) * sl;
+        if constexpr (DENSE) v = load_raw<T, n>(q);
+        else {
+            v.zero();
+            const int64_t ss = threadIdx.x % 256 < 128 ? p.Bs.s : p.Cs.s;
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
-            const int e = (j * 256 + (int)threadIdx.x) % (kTB * 4 * NS);
-            const bool second = (j * 256 + (int)threadIdx.x) >= kTB * 4 * NS;
-            const int s = e % (4 * NS);
-            const int64_t l = t + e / (4 * NS);
-            T r;
-            __builtin_memset(&r, 0, sizeof(r));
-            if (s < p.S && l < t1) {
-                const S4 &st = second ? p.Cs : p.Bs;
-                r = static_cast<const T *>(second ? p.Cm : p.Bm)[a.sp.row0 * st.n + a.g * st.g + s * st.s +
-                                                               (a.sp.start + l) * st.l];
-            }
-            v[j] = r;
+            for (int i = 0; i < n; ++i) v.set(i, q[(s0 + i < p.S ? s0 + i : p.S - 1) * ss]);
         }
     }
-    __device__ __forceinline__ void put(float *sh) const   // [kTB][2][4 NS]
+    __device__ __forceinline__ void put(const ScanP &p, float *sh, int64_t t, int64_t t1) const   // [TB][2][4 NS]
     {
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
-            const int e = (j * 256 + (int)threadIdx.x) % (kTB * 4 * NS);
-            const int second = (j * 256 + (int)threadIdx.x) >= kTB * 4 * NS;
-            sh[(e / (4 * NS)) * (8 * NS) + second * (4 * NS) + e % (4 * NS)] = to_f32(v[j]);
-        }
+        for (int i = 0; i < n; ++i) sh[to + i] = t + row < t1 && s0 + i < p.S ? v.f(i) : 0.f;
     }
 };
 
@@ -137,6 +173,23 @@ template <int NS> __device__ __forceinline__ void lds_states(const float *p, flo
         for (int i = 0; i < NS; ++i) o[i] = p[i];
     }
 }
+
+// What a lane reads from LDS for four steps: d and d x of its channel, B and
+// (WITH_C) C of its states.  Filled a group ahead of its use, so that one wave
+// per SIMD does not wait for LDS.
+template <int NS, bool WITH_C> struct Steps4 {
+    float2 v[4];
+    float b[4][NS], c[4][WITH_C ? NS : 1];
+    __device__ __forceinline__ void load(const float2 (*in)[kCH], const float *bc, int k, int ch, int q)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = in[k + j][ch];
+            lds_states<NS>(bc + (k + j) * 8 * NS + q * NS, b[j]);
+            if constexpr (WITH_C) lds_states<NS>(bc + (k + j) * 8 * NS + 4 * NS + q * NS, c[j]);
+        }
+    }
+};
 
 // A lane's NS states of channel c in [row, channel, state] memory at any
 // strides; states past S are zero.
@@ -206,6 +259,15 @@ inline ScanP scan_params(const lm_plan_t &p, lm_ptrs q)
     a.state_rows = p.t[LM_STATE_OUT].sizes[0];
     a.softplus = (p.args.flags & LM_SOFTPLUS) != 0;
     return a;
+}
+
+// Whether the staging waves may load V = 8 (backward: fewer above 16 states)
+// channels and n states at once.
+inline bool scan_dense(const lm_plan_t &p, const ScanP &a, int n)
+{
+    for (int s : {LM_X, LM_DT, LM_Z, LM_GY})
+        if (p.t[s].rank && p.t[s].strides[1] != 1 && p.C > 1) return false;
+    return p.C >= 8 && p.S % n == 0 && (a.Bs.s == 1 || p.S == 1) && (a.Cs.s == 1 || p.S == 1);
 }
 
 // f(T) for the element type, f(NS) for the states per lane.
