@@ -112,7 +112,7 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
     }
 
     // A quarter of one channel's states.
-    const int lane = threadIdx.x & 63, q = lane & 3, c = wave * 16 + (lane >> 2);
+    const int lane = threadIdx.x & 63, q = lane >> 4, c = wave * 16 + (lane & 15);
     const bool real = c < at.nc;
     const int64_t cc = at.c0 + c;
     float A2[NS], h[NS];
@@ -139,33 +139,38 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         // Four steps at a time, their LDS reads one group ahead; steps past
         // the end have d = 0 and leave the state as it is.
         Steps4<NS, !PRE> g[2];
-        g[0].load(sh.in[buf], sh.bc[buf], 0, c, q);
+        g[0].load(sh.in[buf], sh.bc[buf], 0, c, q, lane);
         for (int k0 = 0; k0 < steps; k0 += 16) {
-#pragma unroll
-            for (int kk = 0; kk < 16; kk += 4) {
-                const int k = k0 + kk;
-                const Steps4<NS, !PRE> &cur = g[kk / 4 & 1];
-                g[kk / 4 & 1 ^ 1].load(sh.in[buf], sh.bc[buf], (k + 4) % kTB, c, q);
-                if (!PRE && kk % CK == 0 && saved && k < steps) {
+            each<4>([&](auto group) {
+                constexpr int G = decltype(group)::value;
+                const int k = k0 + 4 * G;
+                const Steps4<NS, !PRE> &cur = g[G & 1];
+                g[(G & 1) ^ 1].load(sh.in[buf], sh.bc[buf], (k + 4) % kTB, c, q, lane);
+                // Without the barrier the reads sink to their uses.
+                __builtin_amdgcn_sched_barrier(0);
+                if (!PRE && 4 * G % CK == 0 && saved && k < steps) {
                     store_f32<float, NS>(saved, h);
                     saved += p.C * 4 * NS;
                 }
-                float a[4][NS], y4[4];
+                float a[4][NS], hs[4][NS], y4[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < NS; ++i) a[j][i] = hw_exp2(cur.v[j].x * A2[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        h[i] = __builtin_fmaf(a[j][i], h[i], cur.v[j].y * cur.b[j][i]);
-                        if (!PRE) y4[j] = i ? __builtin_fmaf(cur.c[j][i], h[i], y4[j]) : cur.c[j][0] * h[0];
-                    }
+                each<4>([&](auto step) {
+                    constexpr int j = decltype(step)::value;
+                    y4[j] = 0.f;
+                    each<NS>([&](auto state) {
+                        constexpr int i = decltype(state)::value;
+                        h[i] = __builtin_fmaf(a[j][i], h[i], cur.v[j].y * cur.b.template at<j, i>());
+                        hs[j][i] = h[i];
+                        if constexpr (!PRE && NS != 4) y4[j] = __builtin_fmaf(cur.c.template at<j, i>(), h[i], y4[j]);
+                    });
                     if (PRE) sum_d += cur.v[j].x;
-                }
-                if (!PRE) sh.y[buf][k + q][c] = quad_sum4(y4, q);
-            }
+                });
+                if constexpr (!PRE && NS == 4) dot4x4(cur.c.v[0], hs, y4);
+                if (!PRE) sh.y[buf][k + q][c] = quarters4(y4);
+            });
         }
         lds_sync();
     }
@@ -178,6 +183,17 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
     } else if (p.s1 && at.t1 == at.sp.len) {
         put_states<NS>(p.s1, p.s1s, at.seq, cc, q * NS, p.S, h);
     }
+}
+
+template <int CTRL> __device__ __forceinline__ float quad(float v)
+{
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+// Sum over four neighbouring lanes.
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += quad<0xB1>(v);        // lanes 1 0 3 2
+    return v + quad<0x4E>(v);  // lanes 2 3 0 1
 }
 
 // One token for each batch row; four lanes per (row, channel), the state is

@@ -6,14 +6,14 @@
 // and dz = gy (sum_s C h + D x) silu'(z), ddt = dd softplus'.
 //
 // States come from the saved ones: CK steps are run forward again from a saved
-// state, a and a h[t-1] stay in registers (2 CK NS = 128 values per lane), then
+// state, a and h[t-1] stay in registers (2 CK NS = 128 values per lane), then
 // the same steps are run in reverse.  Running the recurrence backwards instead
 // (h[t-1] = (h[t] - d x B) / a) would divide by factors near zero.
 //
-// Sums over states cross four lanes; sums over channels (dB, dC) cross the
-// sixteen channels of a wave by halving exchanges, then the four waves through
-// LDS, and leave the workgroup as f32 parts that scan_bwd_bc adds in a fixed
-// order, as scan_bwd_c does for dA, dD and the bias over the sequences.
+// Sums over states cross the four rows of a wave; sums over channels (dB, dC)
+// cross a row's sixteen channels by halving exchanges, then the four waves
+// through LDS, and leave the workgroup as f32 parts that scan_bwd_bc adds in a
+// fixed order, as scan_bwd_c does for dA, dD and the bias over the sequences.
 #include <hip/hip_runtime.h>
 
 #include "lm_scan.h"
@@ -47,24 +47,16 @@ __device__ __forceinline__ void halve_row(const float (&v)[8], float &z0, float 
         : "=&v"(z0), "=&v"(z1), "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3)
         : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
 }
-// The same across rows: lanes of even (lower) rows receive the sum of a.
-__device__ __forceinline__ float halve16(float a, float b)
+// The same over lanes 2 and 1 apart, by selection.
+__device__ __forceinline__ float halve_quad(float a, float b, bool second, bool pairs)
 {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float halve32(float a, float b)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-// Sums over the sixteen channels of a wave of eight values per lane: the lane
-// receives that of v[4 bit4 + 2 bit2 + bit3] -- still to be added over bit 5.
-__device__ __forceinline__ float halve_channels(const float (&v)[8])
-{
-    float z0, z1;
-    halve_row(v, z0, z1);
-    return halve16(z0, z1);
+    const auto across = [&](float v) {
+        const uint32_t u = __float_as_uint(v);
+        return __uint_as_float(pairs ? __builtin_amdgcn_mov_dpp(u, 0x4E, 0xf, 0xf, true)     // lanes 2 3 0 1
+                                     : __builtin_amdgcn_mov_dpp(u, 0xB1, 0xf, 0xf, true));   // lanes 1 0 3 2
+    };
+    const float sa = a + across(a), sb = b + across(b);
+    return second ? sb : sa;
 }
 
 // Steps of a tile: what LDS holds twice.
@@ -147,7 +139,7 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
                 }
                 const float rb = sh.o[buf][0][tr][tc + i];
                 ox[i] = __builtin_fmaf(D[i], s, d * rb);
-                float dd = __builtin_fmaf(xv, rb, sh.o[buf][1][tr][tc + i]);
+                float dd = __builtin_fmaf(kLn2, sh.o[buf][1][tr][tc + i], xv * rb);   // summed with A log2(e)
                 if (p.softplus) dd *= sigmoid(raw);
                 od[i] = dd;
                 sum_b[i] += i < tn ? dd : 0.f;
@@ -218,22 +210,23 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         return;
     }
 
-    const int lane = threadIdx.x & 63, q = lane & 3, c = wave * 16 + (lane >> 2);
+    const int lane = threadIdx.x & 63, q = lane >> 4, c = wave * 16 + (lane & 15);
     const bool real = c < at.nc;
     const int64_t cc = at.c0 + c;
-    float A[NS], dA[NS] = {}, r[NS] = {};    // r: the gradient that enters from the step behind
+    float A2[NS], dA[NS] = {}, r[NS] = {};   // A log2(e); r: the gradient that enters from the step behind
 #pragma unroll
-    for (int i = 0; i < NS; ++i) A[i] = real && q * NS + i < p.S ? p.A[cc * p.A_c + (q * NS + i) * p.A_s] : 0.f;
+    for (int i = 0; i < NS; ++i)
+        A2[i] = real && q * NS + i < p.S ? kLog2e * p.A[cc * p.A_c + (q * NS + i) * p.A_s] : 0.f;
     if (!PRE && real) {
         if (p.gs) get_states<NS>(p.gs, p.gss, at.seq, cc, q * NS, p.S, r);
         int64_t last = (at.sp.len - 1) / p.chunk;
         if (last > p.chunks - 1) last = p.chunks - 1;
         for (int64_t j = last; j > at.ch; --j) {
             const int64_t k = (at.seq * p.chunks + j) * p.C + cc;
-            const float d = p.carry_d[k] * kLog2e;
+            const float d = p.carry_d[k];
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                r[i] = __builtin_fmaf(hw_exp2(d * A[i]), r[i], p.carry_h[(k * 4 + q) * NS + i]);
+                r[i] = __builtin_fmaf(hw_exp2(d * A2[i]), r[i], p.carry_h[(k * 4 + q) * NS + i]);
         }
     }
     const float *saved = p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * 4 * NS + q * NS;
@@ -257,14 +250,18 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         const float(*ss)[kCH] = sh.s[buf];
         const float *bc = sh.bc[buf];
         if constexpr (PRE) {
-            for (int k = TB - 1; k >= 0; --k) {
-                const float2 v = in[k][c];
-                const float s = ss[k][c], d2 = v.x * kLog2e;
-                float cv[NS];
-                lds_states<NS>(bc + k * 8 * NS + 4 * NS + q * NS, cv);
-#pragma unroll
-                for (int i = 0; i < NS; ++i) r[i] = hw_exp2(d2 * A[i]) * __builtin_fmaf(cv[i], s, r[i]);
-                sum_d += v.x;
+            for (int k0 = TB - 4; k0 >= 0; k0 -= 4) {
+                States4<NS> cs;
+                cs.load(bc + k0 * 8 * NS + 4 * NS + q * NS, lane);
+                each<4>([&](auto step) {
+                    constexpr int j = 3 - decltype(step)::value;
+                    const float d = in[k0 + j][c].x, s = ss[k0 + j][c];
+                    each<NS>([&](auto state) {
+                        constexpr int i = decltype(state)::value;
+                        r[i] = hw_exp2(d * A2[i]) * __builtin_fmaf(cs.template at<j, i>(), s, r[i]);
+                    });
+                    sum_d += d;
+                });
             }
         } else {
             float h0[2][NS];
@@ -277,67 +274,77 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
             for (int part = 1; part >= 0; --part) {
                 if (t + part * CK >= at.t1) continue;
                 const int row0 = part * CK;
-                float a[CK][NS], u[CK][NS], h[NS];
+                float a[CK][NS], h[CK + 1][NS];   // h[k]: the state before step k
 #pragma unroll
-                for (int i = 0; i < NS; ++i) h[i] = part ? h0[1][i] : h0[0][i];
+                for (int i = 0; i < NS; ++i) h[0][i] = part ? h0[1][i] : h0[0][i];
+                each<CK / 4>([&](auto group) {
+                    constexpr int k0 = 4 * decltype(group)::value;
+                    Steps4<NS, false> g;
+                    g.load(in, bc, row0 + k0, c, q, lane);
+                    each<4>([&](auto step) {
+                        constexpr int j = decltype(step)::value, k = k0 + j;
+                        each<NS>([&](auto state) {
+                            constexpr int i = decltype(state)::value;
+                            a[k][i] = hw_exp2(g.v[j].x * A2[i]);
+                            h[k + 1][i] = __builtin_fmaf(a[k][i], h[k][i], g.v[j].y * g.b.template at<j, i>());
+                        });
+                    });
+                });
+                each<CK / 4>([&](auto group) {
+                    constexpr int k0 = CK - 4 - 4 * decltype(group)::value;
+                    const int row = row0 + k0;
+                    Steps4<NS, true> g;
+                    g.load(in, bc, row, c, q, lane);
+                    float s[4], o4[3][4];
+                    float zb[NB / 4][4], zc[NB / 4][4];   // sums over a row, spread over its lanes
 #pragma unroll
-                for (int k = 0; k < CK; ++k) {
-                    const float2 v = in[row0 + k][c];
-                    const float d2 = v.x * kLog2e;
-                    float b[NS];
-                    lds_states<NS>(bc + (row0 + k) * 8 * NS + q * NS, b);
+                    for (int j = 0; j < 4; ++j) s[j] = ss[row + j][c];
+                    each<4>([&](auto step) {
+                        constexpr int j = 3 - decltype(step)::value, k = k0 + j;
+                        float vb[NB], vc[NB], ra = 0.f, rb = 0.f, ch = 0.f;
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        a[k][i] = hw_exp2(d2 * A[i]);
-                        u[k][i] = a[k][i] * h[i];
-                        h[i] = __builtin_fmaf(v.y, b[i], u[k][i]);
-                    }
-                }
-                float o4[3][4], pair[NB / 4];
+                        for (int i = 0; i < NB; ++i) vb[i] = vc[i] = 0.f;
+                        if constexpr (NS == 4) back4<j>(g.c.v[0], g.b.v[0], s[j], h[k + 1], r, ch, rb);
+                        else
+                            each<NS>([&](auto state) {
+                                constexpr int i = decltype(state)::value;
+                                const float cv = g.c.template at<j, i>();
+                                r[i] = __builtin_fmaf(cv, s[j], r[i]);
+                                ch = __builtin_fmaf(cv, h[k + 1][i], ch);
+                                rb = __builtin_fmaf(g.b.template at<j, i>(), r[i], rb);
+                            });
 #pragma unroll
-                for (int k = CK - 1; k >= 0; --k) {
-                    const int row = row0 + k;
-                    const float2 v = in[row][c];
-                    const float s = ss[row][c];
-                    float b[NS], cv[NS], vb[NB], vc[NB];
-                    lds_states<NS>(bc + row * 8 * NS + q * NS, b);
-                    lds_states<NS>(bc + row * 8 * NS + 4 * NS + q * NS, cv);
-                    float rb = 0.f, ra = 0.f, ch = 0.f;
+                        for (int i = 0; i < NS; ++i) {
+                            vb[i] = r[i] * g.v[j].y;
+                            vc[i] = s[j] * h[k + 1][i];
+                            r[i] *= a[k][i];
+                            const float w = r[i] * h[k][i];
+                            ra = __builtin_fmaf(w, A2[i], ra);
+                            dA[i] = __builtin_fmaf(w, g.v[j].x, dA[i]);
+                        }
+                        o4[0][j] = rb, o4[1][j] = ra, o4[2][j] = ch;
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) vb[i] = vc[i] = 0.f;
+                        for (int m = 0; m < NB / 4; ++m) {
+                            const float v8[8] = {vb[4 * m], vb[4 * m + 1], vb[4 * m + 2], vb[4 * m + 3],
+                                                 vc[4 * m], vc[4 * m + 1], vc[4 * m + 2], vc[4 * m + 3]};
+                            halve_row(v8, zb[m][j], zc[m][j]);
+                        }
+                    });
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        const float rr = __builtin_fmaf(cv[i], s, r[i]);
-                        const float hh = __builtin_fmaf(v.y, b[i], u[k][i]);
-                        vb[i] = rr * v.y;
-                        vc[i] = s * hh;
-                        rb = __builtin_fmaf(rr, b[i], rb);
-                        ch = __builtin_fmaf(cv[i], hh, ch);
-                        const float w = rr * u[k][i];
-                        ra = __builtin_fmaf(w, A[i], ra);
-                        dA[i] = __builtin_fmaf(w, v.x, dA[i]);
-                        r[i] = a[k][i] * rr;
-                    }
-                    o4[0][k & 3] = rb, o4[1][k & 3] = ra, o4[2][k & 3] = ch;
-                    if ((k & 3) == 0) {
-#pragma unroll
-                        for (int j = 0; j < 3; ++j) sh.o[buf][j][row + q][c] = quad_sum4(o4[j], q);
-                    }
-                    // dB and dC of two steps meet in the last exchange.
+                    for (int j = 0; j < 3; ++j) sh.o[buf][j][row + q][c] = quarters4(o4[j]);
+                    // A lane keeps B or C by bit 1, the earlier or later of two steps by bit 0.
+                    const bool kind = lane & 2, odd = lane & 1;
 #pragma unroll
                     for (int m = 0; m < NB / 4; ++m) {
-                        const float v8[8] = {vb[4 * m], vb[4 * m + 1], vb[4 * m + 2], vb[4 * m + 3],
-                                             vc[4 * m], vc[4 * m + 1], vc[4 * m + 2], vc[4 * m + 3]};
-                        const float got = halve_channels(v8);
-                        if (k & 1) pair[m] = got;
-                        else {
-                            const float both = halve32(got, pair[m]);
-                            const int i = 4 * m + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1);
-                            if (i < NS)
-                                sh.red[buf][wave][row + (lane >> 5)][((lane >> 4) & 1) * 4 * NS + q * NS + i] = both;
-                        }
+                        float z[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) z[j] = halve_quad(zb[m][j], zc[m][j], kind, true);
+                        const int i = 4 * m + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1);
+                        float *to = &sh.red[buf][wave][row + odd][kind * 4 * NS + q * NS + i];
+                        const float e = halve_quad(z[0], z[1], odd, false), l = halve_quad(z[2], z[3], odd, false);
+                        if (i < NS) to[0] = e, to[2 * 8 * NS] = l;
                     }
-                }
+                });
             }
         }
         lds_sync();

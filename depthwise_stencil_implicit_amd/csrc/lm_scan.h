@@ -1,8 +1,12 @@
 // What the scan's kernels share: parameters, the staged tile and cross-lane sums.
 //
 // A workgroup owns 64 channels of one group and walks along the sequence in
-// tiles.  Four core waves run the recurrence: four neighbouring lanes share a
-// channel and hold NS states each (S <= 4 NS; states past S have A = B = C = 0).
+// tiles.  Four core waves run the recurrence, 16 channels each: lane 16 q + c
+// holds NS states of channel c, a quarter (S <= 4 NS; states past S have A = B =
+// C = 0).  B and C are the same for all channels, so a row of 16 lanes loads 16
+// different values of its quarter -- four steps of four states -- with one LDS
+// read and takes each by a row broadcast in the instruction that uses it;
+// reading them to every lane kept LDS busy 100 of the 195 clocks of a step.
 // Four staging waves work a tile ahead of them and one behind: they load a
 // tile, put d = softplus(dt + dt_bias) and d x -- one transcendental chain per
 // (step, channel), not four -- and B and C in f32 into LDS, and take the core's
@@ -13,6 +17,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "lm_dev.h"
 #include "lm_internal.h"
@@ -160,34 +165,101 @@ template <typename T, int NS, int TB, bool DENSE> struct BcRegs {
     }
 };
 
-template <int NS> __device__ __forceinline__ void lds_states(const float *p, float (&o)[NS])
+// f(0) .. f(N-1) with constant arguments.
+template <typename F, int... I> __device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>)
 {
-    if constexpr (NS >= 4) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F> __device__ __forceinline__ void each(F f) { each(f, std::make_integer_sequence<int, N>()); }
+
+// Lane N of every row of 16 lanes, to all of them.
+template <int N> __device__ __forceinline__ float row_bcast(float v)
+{
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), 0x150 + N, 0xf, 0xf, true));
+}
+
+// A quarter's states of B or C for four steps: value j NS + i (step j, state
+// i) in register / 16, lane % 16 of the quarter's row.
+template <int NS> struct States4 {
+    static constexpr int n = NS < 4 ? 1 : NS / 4;
+    float v[n];
+    __device__ __forceinline__ void load(const float *bc, int lane)   // bc: the quarter's states of the first step
+    {
 #pragma unroll
-        for (int i = 0; i < NS; i += 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(p + i);
-            o[i] = v[0], o[i + 1] = v[1], o[i + 2] = v[2], o[i + 3] = v[3];
+        for (int m = 0; m < n; ++m) {
+            const int f = (m * 16 + (lane & 15)) % (4 * NS);
+            v[m] = bc[f / NS * (8 * NS) + f % NS];
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) o[i] = p[i];
     }
+    template <int J, int I> __device__ __forceinline__ float at() const
+    {
+        return row_bcast<(J * NS + I) % 16>(v[(J * NS + I) / 16]);
+    }
+};
+
+// y[j] = sum_i C[j][i] h[j][i] of four steps and four states.  The compiler
+// folds a row broadcast into a multiplication but not into a multiply-add.
+// The s_nop gives c the two wait states that a cross-lane read needs, should
+// it have been moved by the vector unit just before.
+__device__ __forceinline__ void dot4x4(float c, const float (&h)[4][4], float (&y)[4])
+{
+    asm("s_nop 1\n\t"
+        "v_mul_f32_dpp %0, %4, %5 row_newbcast:0 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %4, %9 row_newbcast:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %4, %13 row_newbcast:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %4, %17 row_newbcast:12 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %4, %6 row_newbcast:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %10 row_newbcast:5 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %14 row_newbcast:9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %18 row_newbcast:13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %4, %7 row_newbcast:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %11 row_newbcast:6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %15 row_newbcast:10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %19 row_newbcast:14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %4, %8 row_newbcast:3 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %12 row_newbcast:7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %16 row_newbcast:11 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %20 row_newbcast:15 row_mask:0xf bank_mask:0xf"
+        : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+        : "v"(c), "v"(h[0][0]), "v"(h[0][1]), "v"(h[0][2]), "v"(h[0][3]), 
+          "v"(h[1][0]), "v"(h[1][1]), "v"(h[1][2]), "v"(h[1][3]), "v"(h[2][0]), "v"(h[2][1]), "v"(h[2][2]), "v"(h[2][3]), 
+          "v"(h[3][0]), "v"(h[3][1]), "v"(h[3][2]), "v"(h[3][3]));
+}
+
+// One step of the backward recurrence for four states: r[i] += C[J][i] s,
+// ch = sum_i C[J][i] h[i], rb = sum_i B[J][i] r[i] (the new r).
+template <int J>
+__device__ __forceinline__ void back4(float c, float b, float s, const float (&h)[4], float (&r)[4], float &ch, float &rb)
+{
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %6, %8 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %6, %8 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %6, %8 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %4, %6, %9 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %5, %7, %0 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %6, %10 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %5, %7, %1 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %6, %11 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %5, %7, %2 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %6, %12 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %5, %7, %3 row_newbcast:%16 row_mask:0xf bank_mask:0xf"
+        : "+&v"(r[0]), "+&v"(r[1]), "+&v"(r[2]), "+&v"(r[3]), "=&v"(ch), "=&v"(rb)
+        : "v"(c), "v"(b), "v"(s), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]), "n"(4 * J), "n"(4 * J + 1),
+          "n"(4 * J + 2), "n"(4 * J + 3));
 }
 
 // What a lane reads from LDS for four steps: d and d x of its channel, B and
-// (WITH_C) C of its states.  Filled a group ahead of its use, so that one wave
-// per SIMD does not wait for LDS.
+// (WITH_C) C of its row.
 template <int NS, bool WITH_C> struct Steps4 {
     float2 v[4];
-    float b[4][NS], c[4][WITH_C ? NS : 1];
-    __device__ __forceinline__ void load(const float2 (*in)[kCH], const float *bc, int k, int ch, int q)
+    States4<NS> b, c;
+    __device__ __forceinline__ void load(const float2 (*in)[kCH], const float *bc, int k, int ch, int q, int lane)
     {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = in[k + j][ch];
-            lds_states<NS>(bc + (k + j) * 8 * NS + q * NS, b[j]);
-            if constexpr (WITH_C) lds_states<NS>(bc + (k + j) * 8 * NS + 4 * NS + q * NS, c[j]);
-        }
+        for (int j = 0; j < 4; ++j) v[j] = in[k + j][ch];
+        b.load(bc + k * 8 * NS + q * NS, lane);
+        if constexpr (WITH_C) c.load(bc + k * 8 * NS + 4 * NS + q * NS, lane);
     }
 };
 
@@ -211,25 +283,22 @@ __device__ __forceinline__ void put_states(float *p, const S3 &st, int64_t row, 
         if (s0 + i < S) q[i * st.l] = h[i];
 }
 
-// Lane exchange inside groups of four lanes.
-template <int CTRL> __device__ __forceinline__ float quad(float v)
+// Sums of lane pairs 16 (32) apart: lanes of even rows (of the lower half)
+// receive that of a, the others that of b.
+__device__ __forceinline__ float halve16(float a, float b)
 {
-    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xf, 0xf, true));
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-__device__ __forceinline__ float quad_sum(float v)
+__device__ __forceinline__ float halve32(float a, float b)
 {
-    v += quad<0xB1>(v);        // lanes 1 0 3 2
-    return v + quad<0x4E>(v);  // lanes 2 3 0 1
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// Sums over the four lanes of four values; lane q receives the sum of v[q].
-__device__ __forceinline__ float quad_sum4(const float (&v)[4], int q)
+// Sums over the four quarters of four values; quarter q receives that of v[q].
+__device__ __forceinline__ float quarters4(const float (&v)[4])
 {
-    const bool odd = q & 1, high = q & 2;
-    const float a0 = v[0] + quad<0xB1>(v[0]), a1 = v[1] + quad<0xB1>(v[1]);
-    const float a2 = v[2] + quad<0xB1>(v[2]), a3 = v[3] + quad<0xB1>(v[3]);
-    const float lo = odd ? a1 : a0, hi = odd ? a3 : a2;
-    const float b0 = lo + quad<0x4E>(lo), b1 = hi + quad<0x4E>(hi);
-    return high ? b1 : b0;
+    return halve32(halve16(v[0], v[1]), halve16(v[2], v[3]));
 }
 
 inline S3 lm_s3(const conv_tensor &t) { return {t.strides[0], t.strides[1], t.rank > 2 ? t.strides[2] : 0}; }
