@@ -13,8 +13,11 @@
 // pair of weights, exactly.  f32 rows are split into three bf16 terms, which
 // hold all 24 bits, against exact weights.
 //
-// A workgroup owns 16 outputs; its waves take blocks of 128 columns in turn
-// (each lane 16 bytes = 32 weights of one output), and join through LDS.
+// A workgroup works on tiles of 16 outputs; its waves take blocks of 128
+// columns in turn (each lane 16 bytes = 32 weights of one output) and join
+// through LDS.  mv4_tiles keeps the rows of x in registers over many tiles, so
+// its loop only streams weights; mv4_stream, for rows that do not fit, loads x
+// with each block.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -81,32 +84,34 @@ __device__ __forceinline__ uint4 pair_up(const uint4 &u)
                  __builtin_amdgcn_perm(u.w, u.y, 0x05040100u), __builtin_amdgcn_perm(u.w, u.y, 0x07060302u)};
 }
 
-// acc += x w, sx += x 1 for one block of 32 columns.
-template <typename T>
-__device__ __forceinline__ void mv_mma(const Raw<T, 8> &x, const uint4 &w, f32x4 &acc, f32x4 &sx, bool want_sx)
-{
-    typedef typename MvOp<T>::in I;
-    if constexpr (std::is_same<T, float>::value) {
-        float v[8];
+// Eight values of a row as matrix operands: themselves, or three bf16 terms of
+// f32 ones.
+template <typename T> struct XOp {
+    static constexpr int n = sizeof(T) == 4 ? 3 : 1;
+    uint4 v[n];
+    __device__ __forceinline__ void set(const Raw<T, 8> &x)
+    {
+        if constexpr (n == 3) {
+            float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.f(i);
+            for (int i = 0; i < 8; ++i) f[i] = x.f(i);
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-            uint4 a;
-            a.x = pack2<bf16_t>(v[0], v[4]), a.y = pack2<bf16_t>(v[1], v[5]);
-            a.z = pack2<bf16_t>(v[2], v[6]), a.w = pack2<bf16_t>(v[3], v[7]);
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+            for (int part = 0; part < 3; ++part) {
+                const uint32_t u[4] = {pack2<bf16_t>(f[0], f[4]), pack2<bf16_t>(f[1], f[5]), pack2<bf16_t>(f[2], f[6]),
+                                       pack2<bf16_t>(f[3], f[7])};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] -= lo_f32(u[i], bf16_t()), v[i + 4] -= hi_f32(u[i], bf16_t());
-            mma_16x16x32(a, w, acc, bf16_t());
-            if (want_sx) mma_16x16x32(a, ones<bf16_t>(), sx, bf16_t());
-        }
-    } else {
-        const uint4 a = pair_up(__builtin_bit_cast(uint4, x));
-        mma_16x16x32(a, w, acc, I());
-        if (want_sx) mma_16x16x32(a, ones<I>(), sx, I());
+                for (int i = 0; i < 4; ++i) f[i] -= lo_f32(u[i], bf16_t()), f[i + 4] -= hi_f32(u[i], bf16_t());
+                v[part] = uint4{u[0], u[1], u[2], u[3]};
+            }
+        } else v[0] = pair_up(__builtin_bit_cast(uint4, x));
     }
-}
+    // acc += x w
+    __device__ __forceinline__ void times(const uint4 &w, f32x4 &acc) const
+    {
+#pragma unroll
+        for (int part = 0; part < n; ++part) mma_16x16x32(v[part], w, acc, typename MvOp<T>::in());
+    }
+};
 
 // The words of a block as loaded (lane group g holds the 32 columns 32 g ..
 // of its output) -> word j of lane group g holds columns 32 j + 8 g ..: a 4x4
@@ -125,9 +130,9 @@ __device__ __forceinline__ void transpose_words(uint32_t (&w)[4])
     s32(w[0], w[2]), s32(w[1], w[3]);
 }
 
-// WIDE: every block of 128 columns lies in one group.  DENSE: x's columns are
-// contiguous.
-template <typename T, bool WIDE, bool DENSE> __global__ __launch_bounds__(64 * kMvWaves) void mv4(const MvP p)
+// Any group that is a multiple of 32 columns and any row length.  WIDE: every
+// block of 128 columns lies in one group.
+template <typename T, bool WIDE> __global__ __launch_bounds__(64 * kMvWaves) void mv4_stream(const MvP p)
 {
     constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;   // blocks of a wave in flight
     __shared__ float s_acc[kMvWaves][16][17];
@@ -157,12 +162,7 @@ template <typename T, bool WIDE, bool DENSE> __global__ __launch_bounds__(64 * k
         for (int j = 0; j < 4; ++j) {
             int k = k0 + (WIDE ? 32 * kb + 8 * j : 32 * j + 8 * kb);
             if (!WIDE && k >= K) k = 0;
-            if constexpr (DENSE) o.x[j] = load_raw<T, 8>(x + k);
-            else {
-                o.x[j].zero();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o.x[j].set(i, x[(k + i) * p.xs_k]);
-            }
+            o.x[j] = load_raw<T, 8>(x + k);
         }
 #pragma unroll
         for (int j = 0; j < (WIDE ? 1 : 4); ++j) {
@@ -206,7 +206,10 @@ template <typename T, bool WIDE, bool DENSE> __global__ __launch_bounds__(64 * k
             if (!WIDE) transpose_words(word);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                mv_mma<T>(cur.x[j], widen(word[j], T()), acc, sx, want_sx);
+                XOp<T> x8;
+                x8.set(cur.x[j]);
+                x8.times(widen(word[j], T()), acc);
+                if (want_sx) x8.times(ones<typename MvOp<T>::in>(), sx);
                 if (!WIDE) {
                     flush(acc, sx, cur.s[j], cur.z[j]);
                     acc = f32x4{0, 0, 0, 0}, sx = f32x4{0, 0, 0, 0};
@@ -230,9 +233,160 @@ template <typename T, bool WIDE, bool DENSE> __global__ __launch_bounds__(64 * k
     }
 }
 
+// At most eight NB blocks of columns, GR columns per group (128: one group
+// holds a block or more), NB blocks of every wave with their x in registers.  Each
+// block's weights of the next tile are requested as soon as the present ones
+// are used, so NB KiB per wave stay in flight across the barrier of a tile.
+template <typename T, int GR, int NB, bool Z>
+__global__ __launch_bounds__(64 * kMvWaves, NB * XOp<T>::n <= 4 ? 4 : 2) void mv4_tiles(const MvP p, int tiles)
+{
+    constexpr int NG = 128 / GR;
+    extern __shared__ __attribute__((aligned(16))) float sh[];   // sums of x [block][group][16], then [2][wave][16][17]
+    const int waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kb = lane >> 4,
+              col = lane & 15;
+    const int m0 = blockIdx.y * 16, blocks = (int)p.K / 128, rows = p.M - m0 < 16 ? (int)p.M - m0 : 16;
+    constexpr bool want_sx = std::is_same<T, bf16_t>::value || Z;
+    const T *x = static_cast<const T *>(p.x) + (m0 + (col < rows ? col : rows - 1)) * p.xs_m;
+    const T *sc = static_cast<const T *>(p.scales), *ze = static_cast<const T *>(p.zeros);
+    float *s_sx = sh + wave * NB * NG * 16;
+    float *s_acc = sh + waves * NB * NG * 16;
+
+    struct Block {
+        uint4 w;
+        Raw<T, NG> s;
+        Raw<T, Z ? NG : 1> z;
+    } ring[NB];
+    // Offsets from uniform bases fit 32 bits (tile_blocks sees to it).
+    const auto fetch = [&](int tile, int r) {
+        const int b = wave + r * waves < blocks ? wave + r * waves : 0;
+        const uint32_t n = tile * 16 + col < (int)p.N ? tile * 16 + col : (int)p.N - 1;
+        ring[r].w = *reinterpret_cast<const uint4 *>(p.w + b * 64 + (n * (uint32_t)p.w_n + kb * 16));
+        const int g = GR == 128 ? b * 128 / (int)p.group : b * NG;
+        ring[r].s = load_raw<T, NG>(sc + g + n * (uint32_t)p.sc_n);
+        if constexpr (Z) ring[r].z = load_raw<T, NG>(ze + g + n * (uint32_t)p.z_n);
+    };
+#pragma unroll
+    for (int r = 0; r < NB; ++r) fetch(blockIdx.x, r);
+
+    // All loads of x before the first use of one.
+    Raw<T, 8> raw[NB][4];
+    const auto x_at = [&](int r, int j) {
+        const int b = wave + r * waves;
+        return (b < blocks ? b : 0) * 128 + (GR == 128 ? 32 * kb + 8 * j : 32 * j + 8 * kb);
+    };
+#pragma unroll
+    for (int r = 0; r < NB; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw[r][j] = load_raw<T, 8>(x + x_at(r, j));
+    XOp<T> xa[NB][4];
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+        f32x4 sx = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (wave + r * waves >= blocks) raw[r][j].zero();
+            xa[r][j].set(raw[r][j]);
+            xa[r][j].times(ones<typename MvOp<T>::in>(), sx);
+            if ((j + 1) * 32 % GR == 0) {   // the same in every column: the first lane of each four rows keeps it
+                if (col == 0) *reinterpret_cast<f32x4 *>(s_sx + (r * NG + (j + 1) * 32 / GR - 1) * 16 + kb * 4) = sx;
+                sx = f32x4{0, 0, 0, 0};
+            }
+        }
+    }
+    int buf = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+        f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < NB; ++r) {
+            uint32_t word[4] = {ring[r].w.x, ring[r].w.y, ring[r].w.z, ring[r].w.w};
+            const Raw<T, NG> s = ring[r].s;
+            const auto z = ring[r].z;
+            fetch(tile + (int)gridDim.x < tiles ? tile + (int)gridDim.x : tile, r);
+            if (GR < 128) transpose_words(word);
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                xa[r][j].times(widen(word[j], T()), acc);
+                if ((j + 1) * 32 % GR) continue;
+                const int g = (j + 1) * 32 / GR - 1;
+                if constexpr (want_sx) {
+                    const f32x4 sx = *reinterpret_cast<const f32x4 *>(s_sx + (r * NG + g) * 16 + kb * 4);
+                    const float off = excess<T>() + (Z ? z.f(g) : 8.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(-off, sx[i], acc[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(s.f(g), acc[i], y[i]), acc[i] = 0.f;
+            }
+            // Blocks mixed by the scheduler would not fit the registers.
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        float *mine = s_acc + (buf * waves + wave) * (16 * 17);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine[(kb * 4 + i) * 17 + col] = y[i];   // all rows: a condition would move the sums behind it
+        lds_sync();
+        const int m = threadIdx.x >> 4;
+        const int64_t n = (int64_t)tile * 16 + col;
+        if (m < rows && n < p.N) {
+            const float *all = s_acc + buf * waves * (16 * 17) + m * 17 + col;
+            float v = 0.f;
+            for (int i = 0; i < waves; ++i) v += all[i * 16 * 17];
+            if (p.bias) v += to_f32(static_cast<const T *>(p.bias)[n * p.bs]);
+            static_cast<T *>(p.y)[(m0 + m) * p.ys_m + n * p.ys_n] = from_f32<T>(v);
+        }
+    }
+}
+
+// x with its columns apart -> contiguous rows in the workspace.
+template <typename T> __global__ __launch_bounds__(256) void mv4_rows(const MvP p, T *out)
+{
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (k >= p.K) return;
+    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) out[m * p.K + k] = static_cast<const T *>(p.x)[m * p.xs_m + k * p.xs_k];
+}
+
+// Blocks per wave of mv4_tiles, 0 where it does not apply: the registers hold
+// eight blocks of 16-bit rows or two of f32's terms beside eight waves.
+int tile_blocks(const lm_plan_t &p)
+{
+    const int64_t group = p.K / p.G, blocks = p.K / 128;
+    const bool dense = (p.G == 1 || p.t[LM_SCALES].strides[1] == 1) &&
+                       (!p.t[LM_ZEROS].rank || p.G == 1 || p.t[LM_ZEROS].strides[1] == 1);
+    for (int s : {LM_W, LM_SCALES, LM_ZEROS})
+        if (p.t[s].rank && p.t[s].strides[0] > 0x7fffffff / (p.C + 1)) return 0;
+    if (!dense || p.C > 0x7fffff00 || p.K % 128 || (group % 128 && group != 64 && group != 32)) return 0;
+    const int most = p.dtype == CONV_F32 ? 2 : 8;
+    for (int nb = 1; nb <= most; nb *= 2)
+        if (blocks <= kMvWaves * nb) return nb;
+    return 0;
+}
+
+template <typename T, int GR> void run_tiles(const MvP &a, int nb, hipStream_t s)
+{
+    const int blocks = (int)(a.K / 128), waves = (int)lm_cdiv(blocks, nb), tiles = (int)lm_cdiv(a.N, 16);
+    // At least four waves finish a tile of 16 rows.
+    const int threads = 64 * (waves < 4 ? 4 : waves);
+    // As many workgroups as are resident at once on 256 compute units.
+    const int per_cu = nb * XOp<T>::n <= 4 ? 1024 / threads : 1;
+    const dim3 grid((unsigned)(tiles < 256 * per_cu ? tiles : 256 * per_cu), (unsigned)lm_cdiv(a.M, 16));
+    const size_t lds = (size_t)(threads / 64) * (nb * (128 / GR) * 16 + 2 * 16 * 17) * sizeof(float);
+    const auto go = [&](auto n) {
+        constexpr int NB = decltype(n)::value;
+        if (a.zeros) mv4_tiles<T, GR, NB, true><<<grid, threads, lds, s>>>(a, tiles);
+        else mv4_tiles<T, GR, NB, false><<<grid, threads, lds, s>>>(a, tiles);
+    };
+    if (nb == 1) go(std::integral_constant<int, 1>());
+    else if (nb == 2) go(std::integral_constant<int, 2>());
+    else if constexpr (sizeof(T) == 2) {
+        if (nb == 4) go(std::integral_constant<int, 4>());
+        else go(std::integral_constant<int, 8>());
+    }
+}
+
 }  // namespace
 
-int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
+int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
 {
     MvP a = {};
     a.x = q[LM_X], a.scales = q[LM_SCALES], a.zeros = q[LM_ZEROS], a.bias = q[LM_BIAS];
@@ -247,13 +401,17 @@ int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
     const bool wide = a.group % 128 == 0;
     const auto go = [&](auto t) {
         typedef decltype(t) T;
-        if (a.xs_k == 1 || a.K == 1) {
-            if (wide) mv4<T, true, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
-            else mv4<T, false, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
-        } else {
-            if (wide) mv4<T, true, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
-            else mv4<T, false, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
+        if (a.xs_k != 1 && a.K > 1) {
+            mv4_rows<T><<<dim3((unsigned)lm_cdiv(a.K, 256), (unsigned)(a.M < 65535 ? a.M : 65535)), 256, 0, s>>>(
+                a, static_cast<T *>(ws));
+            a.x = ws, a.xs_m = a.K, a.xs_k = 1;
         }
+        if (const int nb = tile_blocks(p)) {
+            if (wide) run_tiles<T, 128>(a, nb, s);
+            else if (a.group == 64) run_tiles<T, 64>(a, nb, s);
+            else run_tiles<T, 32>(a, nb, s);
+        } else if (wide) mv4_stream<T, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
+        else mv4_stream<T, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
     };
     if (p.dtype == CONV_F32) go(float());
     else if (p.dtype == CONV_F16) go(f16_t());

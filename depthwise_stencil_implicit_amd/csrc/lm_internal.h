@@ -36,7 +36,7 @@ int launch_lm_conv_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
 int launch_lm_scan(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 int launch_lm_scan_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 int launch_lm_scan_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
-int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
+int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 
 inline int lm_launch_status() { return hipGetLastError() == hipSuccess ? CONV_OK : CONV_EDEVICE; }
 

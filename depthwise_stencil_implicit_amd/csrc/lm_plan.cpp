@@ -206,6 +206,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
             k.fail(CONV_EUNSUPPORTED, "too many rows");
             return k.status;
         }
+        if (x.strides[1] != 1 && p.K > 1) p.workspace_bytes = p.seqs * p.K * e;
         p.flops = 2 * p.seqs * p.K * p.C;
         p.bytes = p.C * p.K / 2 + p.C * p.G * e * (k.has(LM_ZEROS) ? 2 : 1) + (p.seqs * (p.K + p.C) + (k.has(LM_BIAS) ? p.C : 0)) * e;
         *out = p;
@@ -346,7 +347,7 @@ extern "C" int lm_run(const lm_plan_t *p, void *const *q, void *workspace, size_
     case LM_SCAN: return launch_lm_scan(*p, q, workspace, s);
     case LM_SCAN_BWD: return launch_lm_scan_bwd(*p, q, workspace, s);
     case LM_SCAN_STEP: return launch_lm_scan_step(*p, q, s);
-    case LM_MV4: return launch_lm_mv4(*p, q, s);
+    case LM_MV4: return launch_lm_mv4(*p, q, workspace, s);
     default: return CONV_EINVAL;
     }
 }

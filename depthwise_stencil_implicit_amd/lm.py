@@ -208,6 +208,7 @@ class _Step:
         self.shape, self.dtype = shape, ref.dtype
         self.plan = _make_plan(op, {**tensors, _Y: self.empty_output()}, flags)
         self._plan_ref = ctypes.byref(self.plan)
+        self.workspace_bytes = int(self.plan.workspace_bytes)
         self._run = A.lib().lm_run
 
     def empty_output(self) -> torch.Tensor:
@@ -218,7 +219,10 @@ class _Step:
         if dev != torch.cuda.current_device():
             with torch.cuda.device(dev):
                 return self._launch(q, stream)
-        st = self._run(self._plan_ref, q, None, 0, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+        n = self.workspace_bytes
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        st = self._run(self._plan_ref, q, ws.data_ptr() if n else None, n,
+                       torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
         if st != A.OK:
             raise ConvError(st)
 
