@@ -28,13 +28,15 @@
 namespace miconv {
 namespace {
 
-constexpr int kMvWaves = 8;
+constexpr int kMvWaves = 8;      // of mv4_stream
+constexpr int kTileWaves = 16;   // of mv4_tiles, at most
 
 struct MvP {
     const void *x, *scales, *zeros, *bias;
     const uint8_t *w;
     void *y;
     int64_t M, N, K, group, groups;
+    uint32_t block_group;   // 2^20 group 128ths of a block, rounded up: block -> group
     int64_t xs_m, xs_k, w_n, sc_n, sc_g, z_n, z_g, bs, ys_m, ys_n;
 };
 
@@ -238,14 +240,17 @@ template <typename T, bool WIDE> __global__ __launch_bounds__(64 * kMvWaves) voi
 // block's weights of the next tile are requested as soon as the present ones
 // are used, so NB KiB per wave stay in flight across the barrier of a tile.
 template <typename T, int GR, int NB, bool Z>
-__global__ __launch_bounds__(64 * kMvWaves, NB * XOp<T>::n <= 4 ? 4 : 2) void mv4_tiles(const MvP p, int tiles)
+__global__ __launch_bounds__(64 * kTileWaves) void mv4_tiles(const MvP p, int tiles, float *partial)
 {
     constexpr int NG = 128 / GR;
     extern __shared__ __attribute__((aligned(16))) float sh[];   // sums of x [block][group][16], then [2][wave][16][17]
     const int waves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kb = lane >> 4,
               col = lane & 15;
-    const int m0 = blockIdx.y * 16, blocks = (int)p.K / 128, rows = p.M - m0 < 16 ? (int)p.M - m0 : 16;
+    // Blocks of this part of the columns: first .. first + blocks - 1.
+    const int all = (int)p.K / 128, first = (int)(blockIdx.z * (int64_t)all / gridDim.z),
+              blocks = (int)((blockIdx.z + 1) * (int64_t)all / gridDim.z) - first;
+    const int m0 = blockIdx.y * 16, rows = p.M - m0 < 16 ? (int)p.M - m0 : 16;
     constexpr bool want_sx = std::is_same<T, bf16_t>::value || Z;
     const T *x = static_cast<const T *>(p.x) + (m0 + (col < rows ? col : rows - 1)) * p.xs_m;
     const T *sc = static_cast<const T *>(p.scales), *ze = static_cast<const T *>(p.zeros);
@@ -259,10 +264,10 @@ __global__ __launch_bounds__(64 * kMvWaves, NB * XOp<T>::n <= 4 ? 4 : 2) void mv
     } ring[NB];
     // Offsets from uniform bases fit 32 bits (tile_blocks sees to it).
     const auto fetch = [&](int tile, int r) {
-        const int b = wave + r * waves < blocks ? wave + r * waves : 0;
+        const int b = first + (wave + r * waves < blocks ? wave + r * waves : 0);
         const uint32_t n = tile * 16 + col < (int)p.N ? tile * 16 + col : (int)p.N - 1;
         ring[r].w = *reinterpret_cast<const uint4 *>(p.w + b * 64 + (n * (uint32_t)p.w_n + kb * 16));
-        const int g = GR == 128 ? b * 128 / (int)p.group : b * NG;
+        const int g = GR == 128 ? (int)((uint32_t)b * p.block_group >> 20) : b * NG;
         ring[r].s = load_raw<T, NG>(sc + g + n * (uint32_t)p.sc_n);
         if constexpr (Z) ring[r].z = load_raw<T, NG>(ze + g + n * (uint32_t)p.z_n);
     };
@@ -273,12 +278,18 @@ __global__ __launch_bounds__(64 * kMvWaves, NB * XOp<T>::n <= 4 ? 4 : 2) void mv
     Raw<T, 8> raw[NB][4];
     const auto x_at = [&](int r, int j) {
         const int b = wave + r * waves;
-        return (b < blocks ? b : 0) * 128 + (GR == 128 ? 32 * kb + 8 * j : 32 * j + 8 * kb);
+        return (first + (b < blocks ? b : 0)) * 128 + (GR == 128 ? 32 * kb + 8 * j : 32 * j + 8 * kb);
     };
 #pragma unroll
     for (int r = 0; r < NB; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) raw[r][j] = load_raw<T, 8>(x + x_at(r, j));
+        for (int j = 0; j < 4; ++j) raw[r][j].zero();
+    if (col < rows) {   // lanes of rows past the end load nothing
+#pragma unroll
+        for (int r = 0; r < NB; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw[r][j] = load_raw<T, 8>(x + x_at(r, j));
+    }
     XOp<T> xa[NB][4];
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
@@ -330,11 +341,32 @@ __global__ __launch_bounds__(64 * kMvWaves, NB * XOp<T>::n <= 4 ? 4 : 2) void mv
         const int64_t n = (int64_t)tile * 16 + col;
         if (m < rows && n < p.N) {
             const float *all = s_acc + buf * waves * (16 * 17) + m * 17 + col;
-            float v = 0.f;
-            for (int i = 0; i < waves; ++i) v += all[i * 16 * 17];
-            if (p.bias) v += to_f32(static_cast<const T *>(p.bias)[n * p.bs]);
-            static_cast<T *>(p.y)[(m0 + m) * p.ys_m + n * p.ys_n] = from_f32<T>(v);
+            float v[kTileWaves];
+#pragma unroll
+            for (int i = 0; i < kTileWaves; ++i) v[i] = i < waves ? all[i * 16 * 17] : 0.f;
+#pragma unroll
+            for (int w = 1; w < kTileWaves; w *= 2)
+#pragma unroll
+                for (int i = 0; i < kTileWaves; i += 2 * w) v[i] += v[i + w];
+            if (partial) partial[(blockIdx.z * p.M + m0 + m) * p.N + n] = v[0];
+            else {
+                if (p.bias) v[0] += to_f32(static_cast<const T *>(p.bias)[n * p.bs]);
+                static_cast<T *>(p.y)[(m0 + m) * p.ys_m + n * p.ys_n] = from_f32<T>(v[0]);
+            }
         }
+    }
+}
+
+// Sums of the parts of the columns.
+template <typename T> __global__ __launch_bounds__(256) void mv4_sums(const MvP p, const float *partial, int parts)
+{
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= p.N) return;
+    const float bias = p.bias ? to_f32(static_cast<const T *>(p.bias)[n * p.bs]) : 0.f;
+    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+        float v = 0.f;
+        for (int i = 0; i < parts; ++i) v += partial[(i * p.M + m) * p.N + n];
+        static_cast<T *>(p.y)[m * p.ys_m + n * p.ys_n] = from_f32<T>(v + bias);
     }
 }
 
@@ -346,42 +378,30 @@ template <typename T> __global__ __launch_bounds__(256) void mv4_rows(const MvP 
     for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) out[m * p.K + k] = static_cast<const T *>(p.x)[m * p.xs_m + k * p.xs_k];
 }
 
-// Blocks per wave of mv4_tiles, 0 where it does not apply: the registers hold
-// eight blocks of 16-bit rows or two of f32's terms beside eight waves.
-int tile_blocks(const lm_plan_t &p)
+template <typename T, int GR> void run_tiles(const MvP &a, int parts, float *partial, hipStream_t s)
 {
-    const int64_t group = p.K / p.G, blocks = p.K / 128;
-    const bool dense = (p.G == 1 || p.t[LM_SCALES].strides[1] == 1) &&
-                       (!p.t[LM_ZEROS].rank || p.G == 1 || p.t[LM_ZEROS].strides[1] == 1);
-    for (int s : {LM_W, LM_SCALES, LM_ZEROS})
-        if (p.t[s].rank && p.t[s].strides[0] > 0x7fffffff / (p.C + 1)) return 0;
-    if (!dense || p.C > 0x7fffff00 || p.K % 128 || (group % 128 && group != 64 && group != 32)) return 0;
-    const int most = p.dtype == CONV_F32 ? 2 : 8;
-    for (int nb = 1; nb <= most; nb *= 2)
-        if (blocks <= kMvWaves * nb) return nb;
-    return 0;
-}
-
-template <typename T, int GR> void run_tiles(const MvP &a, int nb, hipStream_t s)
-{
-    const int blocks = (int)(a.K / 128), waves = (int)lm_cdiv(blocks, nb), tiles = (int)lm_cdiv(a.N, 16);
+    // The fewest blocks per wave: a short call's time is its longest wave's.
+    const int blocks = (int)lm_cdiv(a.K / 128, parts), nb = blocks <= 16 ? 1 : blocks <= 32 ? 2 : 4;
+    const int waves = (int)lm_cdiv(blocks, nb), tiles = (int)lm_cdiv(a.N, 16);
     // At least four waves finish a tile of 16 rows.
     const int threads = 64 * (waves < 4 ? 4 : waves);
     // As many workgroups as are resident at once on 256 compute units.
-    const int per_cu = nb * XOp<T>::n <= 4 ? 1024 / threads : 1;
-    const dim3 grid((unsigned)(tiles < 256 * per_cu ? tiles : 256 * per_cu), (unsigned)lm_cdiv(a.M, 16));
+    const int resident = 256 * (1024 / threads);
+    const dim3 grid((unsigned)(tiles < resident ? tiles : resident), (unsigned)lm_cdiv(a.M, 16), (unsigned)parts);
     const size_t lds = (size_t)(threads / 64) * (nb * (128 / GR) * 16 + 2 * 16 * 17) * sizeof(float);
     const auto go = [&](auto n) {
         constexpr int NB = decltype(n)::value;
-        if (a.zeros) mv4_tiles<T, GR, NB, true><<<grid, threads, lds, s>>>(a, tiles);
-        else mv4_tiles<T, GR, NB, false><<<grid, threads, lds, s>>>(a, tiles);
+        if (a.zeros) mv4_tiles<T, GR, NB, true><<<grid, threads, lds, s>>>(a, tiles, partial);
+        else mv4_tiles<T, GR, NB, false><<<grid, threads, lds, s>>>(a, tiles, partial);
     };
     if (nb == 1) go(std::integral_constant<int, 1>());
-    else if (nb == 2) go(std::integral_constant<int, 2>());
     else if constexpr (sizeof(T) == 2) {
-        if (nb == 4) go(std::integral_constant<int, 4>());
-        else go(std::integral_constant<int, 8>());
+        if (nb == 2) go(std::integral_constant<int, 2>());
+        else go(std::integral_constant<int, 4>());
     }
+    if (partial)
+        mv4_sums<T><<<dim3((unsigned)lm_cdiv(a.N, 256), (unsigned)(a.M < 65535 ? a.M : 65535)), 256, 0, s>>>(a, partial,
+                                                                                                          parts);
 }
 
 }  // namespace
@@ -397,6 +417,8 @@ int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     a.sc_n = p.t[LM_SCALES].strides[0], a.sc_g = p.t[LM_SCALES].strides[1];
     a.z_n = p.t[LM_ZEROS].strides[0], a.z_g = p.t[LM_ZEROS].strides[1];
     a.bs = p.t[LM_BIAS].strides[0], a.ys_m = p.t[LM_Y].strides[0], a.ys_n = p.t[LM_Y].strides[1];
+    // Exact for the blocks of mv4_parts (fewer than 1024).
+    a.block_group = a.group % 128 ? 0 : (uint32_t)((1 << 20) / (a.group / 128) + 1);
     const dim3 grid((unsigned)lm_cdiv(a.N, 16), (unsigned)lm_cdiv(a.M, 16));
     const bool wide = a.group % 128 == 0;
     const auto go = [&](auto t) {
@@ -406,10 +428,11 @@ int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
                 a, static_cast<T *>(ws));
             a.x = ws, a.xs_m = a.K, a.xs_k = 1;
         }
-        if (const int nb = tile_blocks(p)) {
-            if (wide) run_tiles<T, 128>(a, nb, s);
-            else if (a.group == 64) run_tiles<T, 64>(a, nb, s);
-            else run_tiles<T, 32>(a, nb, s);
+        if (const int parts = mv4_parts(p)) {
+            float *partial = parts > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + mv4_rows_bytes(p)) : nullptr;
+            if (wide) run_tiles<T, 128>(a, parts, partial, s);
+            else if (a.group == 64) run_tiles<T, 64>(a, parts, partial, s);
+            else run_tiles<T, 32>(a, parts, partial, s);
         } else if (wide) mv4_stream<T, true><<<grid, 64 * kMvWaves, 0, s>>>(a);
         else mv4_stream<T, false><<<grid, 64 * kMvWaves, 0, s>>>(a);
     };

@@ -29,6 +29,26 @@ inline int scan_ns(int64_t S)
 inline int scan_save_steps(int64_t S) { return scan_ns(S) <= 4 ? 16 : 64 / scan_ns(S); }
 inline int64_t lm_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// 4-bit products: bytes of x made contiguous (0: x's rows are), and the parts
+// of the columns whose x fits the registers of 16 waves -- four blocks of 128
+// columns each for 16-bit types, one for f32 (three terms).  0 parts: weights or scales that
+// the register kernel does not take.
+inline int64_t mv4_rows_bytes(const lm_plan_t &p)
+{
+    const int64_t bytes = p.seqs * p.K * (p.dtype == CONV_F32 ? 4 : 2);
+    return p.t[LM_X].strides[1] != 1 && p.K > 1 ? lm_cdiv(bytes, 256) * 256 : 0;
+}
+inline int mv4_parts(const lm_plan_t &p)
+{
+    const int64_t group = p.K / p.G, blocks = p.K / 128;
+    for (int s : {LM_SCALES, LM_ZEROS})
+        if (p.t[s].rank && p.G > 1 && p.t[s].strides[1] != 1) return 0;
+    for (int s : {LM_W, LM_SCALES, LM_ZEROS})   // offsets of 32 bits
+        if (p.t[s].rank && p.t[s].strides[0] > 0x7fffffff / (p.C + 1)) return 0;
+    if (p.C > 0x7fffff00 || p.K % 128 || blocks >= 1024 || (group % 128 && group != 64 && group != 32)) return 0;
+    return (int)lm_cdiv(blocks, p.dtype == CONV_F32 ? 16 : 64);
+}
+
 typedef void *const *lm_ptrs;
 int launch_lm_conv(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
 int launch_lm_conv_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);

@@ -206,7 +206,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
             k.fail(CONV_EUNSUPPORTED, "too many rows");
             return k.status;
         }
-        if (x.strides[1] != 1 && p.K > 1) p.workspace_bytes = p.seqs * p.K * e;
+        p.workspace_bytes = mv4_rows_bytes(p) + (mv4_parts(p) > 1 ? mv4_parts(p) * p.seqs * p.C * 4 : 0);
         p.flops = 2 * p.seqs * p.K * p.C;
         p.bytes = p.C * p.K / 2 + p.C * p.G * e * (k.has(LM_ZEROS) ? 2 : 1) + (p.seqs * (p.K + p.C) + (k.has(LM_BIAS) ? p.C : 0)) * e;
         *out = p;

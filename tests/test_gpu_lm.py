@@ -339,6 +339,24 @@ def test_matvec4(dt, M, K, N, group, zeros, bias):
         assert torch.equal(lm.matvec4(x[1:2], packed, scales, zz, bb), y[1:2])
 
 
+@pytest.mark.parametrize("dt", [BF, HF, F])
+@pytest.mark.parametrize("M,K,N,group,zeros", [(2, 8320, 37, 128, False), (17, 16384, 16, 64, True), (1, 9088, 40, 32, False),
+                                               (3, 10240, 20, 2560, True)])
+def test_matvec4_long_rows(dt, M, K, N, group, zeros):
+    """Rows split over several workgroups."""
+    g = gen(M + K + N)
+    x = rnd(g, M, K, dtype=dt).cuda()
+    packed = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8).cuda()
+    scales = (torch.rand((N, K // group), generator=g) / 8).to(dt).cuda()
+    zz = torch.randint(0, 16, (N, K // group), generator=g).to(dt).cuda() if zeros else None
+    y = lm.matvec4(x, packed, scales, zz)
+    n = 128 + 2 * (K // min(group, 128)) + 16
+    R.assert_close(y, R.matvec4(x, packed, scales, zz), R.matvec4(x, packed, scales, zz, bound=True), n, "y")
+    apart = torch.zeros(K, M, dtype=dt, device="cuda").t()
+    apart.copy_(x)
+    assert torch.equal(lm.matvec4(apart, packed, scales, zz), y)
+
+
 def test_matvec4_counts_every_weight_exactly():
     """Powers of two pick single weights: the product is exact."""
     for dt in (BF, HF, F):
