@@ -13,17 +13,17 @@
 namespace miconv {
 namespace {
 
-constexpr int kTB = LM_SCAN_TB;      // steps of a tile: 8 channels of one row per staging thread
+constexpr int kTB = 32;              // steps of a tile: 8 channels of one row per staging thread
 
-template <int NS> struct FwdLds {
+template <int NS, int QW, bool PRE> struct FwdLds {
     float2 in[2][kTB][kCH];                                          // d, d x
-    __attribute__((aligned(16))) float bc[2][kTB * 8 * NS];
-    __attribute__((aligned(16))) float y[2][kTB][kRow];
+    __attribute__((aligned(16))) float bc[2][kTB * 8 * QW * NS];
+    __attribute__((aligned(16))) float y[PRE ? 1 : 2][PRE ? 1 : QW][kTB][kRow];
 };
 
 // The staging waves of one workgroup.
-template <typename T, int NS, bool PRE, bool DENSE>
-__device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdLds<NS> &sh, int tid)
+template <typename T, int NS, int QW, bool PRE, bool DENSE>
+__device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdLds<NS, QW, PRE> &sh, int tid)
 {
     const int tr = tid >> 3, tc = (tid & 7) * 8;
     const int tn = at.nc - tc;
@@ -42,7 +42,7 @@ __device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdL
     get_param<8>(p.bias, p.bias_s, sc, tn, bias);
     get_param<8>(p.D, p.D_s, sc, tn, D);
     Raw<T, 8> nx, ndt, nz, cx, cz, ox, oz;   // tile being loaded; in the core; leaving
-    BcRegs<T, NS, kTB, DENSE> bc(p, at, tid);
+    BcRegs<T, 4 * QW * NS, kTB, DENSE> bc(p, at, tid);
     const auto fetch = [&](int64_t t) {
         const int64_t l = t + tr < at.t1 ? t + tr : at.t1 - 1;
         nx = get_row<T, 8, DENSE>(px + l * p.xs.l, p.xs.c, sc, p.C);
@@ -66,14 +66,18 @@ __device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdL
         bc.put(p, sh.bc[buf], t, at.t1);
     };
     const auto leave = [&](int64_t t, int buf) {
-        if (PRE || !py || t + tr >= at.t1) return;
-        float o[8];
+        if constexpr (!PRE) {
+            if (!py || t + tr >= at.t1) return;
+            float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            o[i] = __builtin_fmaf(D[i], ox.f(i), sh.y[buf][tr][tc + i]);
-            if (has_z) o[i] *= silu(oz.f(i));
+            for (int i = 0; i < 8; ++i) {
+                float y = sh.y[buf][0][tr][tc + i];
+                if constexpr (QW == 2) y += sh.y[buf][1][tr][tc + i];
+                o[i] = __builtin_fmaf(D[i], ox.f(i), y);
+                if (has_z) o[i] *= silu(oz.f(i));
+            }
+            put_row<T, 8>(py + (t + tr) * p.ys.l, p.ys.c, tn, o);
         }
-        put_row<T, 8>(py + (t + tr) * p.ys.l, p.ys.c, tn, o);
     };
     if (at.t0 < at.t1) {
         fetch(at.t0);
@@ -98,21 +102,24 @@ __device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdL
 // PRE: only the state that leaves a chunk entered with zero, and the chunk's
 // sum of d (its decay is exp(A sum d)); the main pass folds them into the
 // state its chunk starts from.
-template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) void scan_fwd(const ScanP p)
+// Up to two states per lane of 16-bit calls fit two workgroups on a compute
+// unit (six waves per SIMD).
+template <typename T, int NS, int QW, bool PRE, bool DENSE>
+__global__ __launch_bounds__(256 * QW + kStage, sizeof(T) == 2 && DENSE && NS <= 2 && QW == 2 ? 6 : QW + 1) void scan_fwd(const ScanP p)
 {
-    constexpr int CK = NS <= 4 ? 16 : 64 / NS;
-    __shared__ FwdLds<NS> sh;
+    constexpr int W = 4 * QW * NS, CK = ScanShape{NS, QW}.save_steps();
+    __shared__ FwdLds<NS, QW, PRE> sh;
     const ScanAt at = scan_at(p, PRE ? p.chunks - 1 : p.chunks);
     if (PRE ? at.t0 + p.chunk >= at.sp.len : (at.t0 >= at.sp.len && at.ch > 0)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave >= 4) {
-        if (p.dense) fwd_stage<T, NS, PRE, true>(p, at, sh, (int)threadIdx.x - 256);
-        else fwd_stage<T, NS, PRE, false>(p, at, sh, (int)threadIdx.x - 256);
+    if (wave >= 4 * QW) {
+        fwd_stage<T, NS, QW, PRE, DENSE>(p, at, sh, (int)threadIdx.x - 256 * QW);
         return;
     }
 
-    // A quarter of one channel's states.
-    const int lane = threadIdx.x & 63, q = lane >> 4, c = wave * 16 + (lane & 15);
+    // NS states of one channel: those of row q of its 4 QW.
+    const int lane = threadIdx.x & 63, row = lane >> 4, half = wave >> 2, q = half * 4 + row,
+              c = (wave & 3) * 16 + (lane & 15);
     const bool real = c < at.nc;
     const int64_t cc = at.c0 + c;
     float A2[NS], h[NS];
@@ -126,11 +133,11 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
             const float d = p.carry_d[k];
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                h[i] = __builtin_fmaf(hw_exp2(d * A2[i]), h[i], p.carry_h[(k * 4 + q) * NS + i]);
+                h[i] = __builtin_fmaf(hw_exp2(d * A2[i]), h[i], p.carry_h[k * W + q * NS + i]);
         }
     }
     float *saved = !PRE && p.saved && real
-                       ? p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * 4 * NS + q * NS : nullptr;
+                       ? p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * W + q * NS : nullptr;
     float sum_d = 0.f;
     lds_sync();
     int buf = 0;
@@ -138,19 +145,19 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         const int steps = at.t1 - t < kTB ? (int)(at.t1 - t) : kTB;
         // Four steps at a time, their LDS reads one group ahead; steps past
         // the end have d = 0 and leave the state as it is.
-        Steps4<NS, !PRE> g[2];
+        Steps4<NS, W, !PRE> g[2];
         g[0].load(sh.in[buf], sh.bc[buf], 0, c, q, lane);
         for (int k0 = 0; k0 < steps; k0 += 16) {
             each<4>([&](auto group) {
                 constexpr int G = decltype(group)::value;
                 const int k = k0 + 4 * G;
-                const Steps4<NS, !PRE> &cur = g[G & 1];
+                const Steps4<NS, W, !PRE> &cur = g[G & 1];
                 g[(G & 1) ^ 1].load(sh.in[buf], sh.bc[buf], (k + 4) % kTB, c, q, lane);
                 // Without the barrier the reads sink to their uses.
                 __builtin_amdgcn_sched_barrier(0);
                 if (!PRE && 4 * G % CK == 0 && saved && k < steps) {
                     store_f32<float, NS>(saved, h);
-                    saved += p.C * 4 * NS;
+                    saved += p.C * W;
                 }
                 float a[4][NS], hs[4][NS], y4[4];
 #pragma unroll
@@ -164,12 +171,12 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
                         constexpr int i = decltype(state)::value;
                         h[i] = __builtin_fmaf(a[j][i], h[i], cur.v[j].y * cur.b.template at<j, i>());
                         hs[j][i] = h[i];
-                        if constexpr (!PRE && NS != 4) y4[j] = __builtin_fmaf(cur.c.template at<j, i>(), h[i], y4[j]);
+                        if constexpr (!PRE && NS != 2) y4[j] = __builtin_fmaf(cur.c.template at<j, i>(), h[i], y4[j]);
                     });
                     if (PRE) sum_d += cur.v[j].x;
                 });
-                if constexpr (!PRE && NS == 4) dot4x4(cur.c.v[0], hs, y4);
-                if (!PRE) sh.y[buf][k + q][c] = quarters4(y4);
+                if constexpr (!PRE && NS == 2) dot4x2(cur.c.v[0], hs, y4);
+                if constexpr (!PRE) sh.y[buf][half][k + row][c] = rows4(y4);
             });
         }
         lds_sync();
@@ -178,7 +185,7 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
     if (PRE) {
         const int64_t k = (at.seq * (p.chunks - 1) + at.ch) * p.C + cc;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) p.carry_h[(k * 4 + q) * NS + i] = h[i];
+        for (int i = 0; i < NS; ++i) p.carry_h[k * W + q * NS + i] = h[i];
         if (q == 0) p.carry_d[k] = sum_d;
     } else if (p.s1 && at.t1 == at.sp.len) {
         put_states<NS>(p.s1, p.s1s, at.seq, cc, q * NS, p.S, h);
@@ -260,15 +267,21 @@ int launch_lm_scan(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
 {
     ScanP a = scan_params(p, q);
     if (a.seqs == 0) return CONV_OK;
-    a.dense = scan_dense(p, a, scan_ns(p.S));
+    const bool dense = scan_dense(p, a, 8, scan_shape(p.S).width() / 4);
     a.carry_d = static_cast<float *>(ws);
     a.carry_h = a.carry_d + lm_cdiv(a.seqs * (a.chunks - 1) * a.C, 4) * 4;
+    const int pre = (int)(a.seqs * (a.chunks - 1) * a.blocks), grid = (int)(a.seqs * a.chunks * a.blocks);
     with_type(p.dtype, [&](auto t) {
-        with_ns(p.S, [&](auto n) {
+        with_ns(p.S, [&](auto n, auto w) {
             typedef decltype(t) T;
-            constexpr int NS = decltype(n)::value;
-            if (a.chunks > 1) scan_fwd<T, NS, true><<<(int)(a.seqs * (a.chunks - 1) * a.blocks), kThreads, 0, s>>>(a);
-            scan_fwd<T, NS, false><<<(int)(a.seqs * a.chunks * a.blocks), kThreads, 0, s>>>(a);
+            constexpr int NS = decltype(n)::value, QW = decltype(w)::value, threads = 256 * QW + kStage;
+            if (dense) {
+                if (pre) scan_fwd<T, NS, QW, true, true><<<pre, threads, 0, s>>>(a);
+                scan_fwd<T, NS, QW, false, true><<<grid, threads, 0, s>>>(a);
+            } else {
+                if (pre) scan_fwd<T, NS, QW, true, false><<<pre, threads, 0, s>>>(a);
+                scan_fwd<T, NS, QW, false, false><<<grid, threads, 0, s>>>(a);
+            }
         });
     });
     return lm_launch_status();
@@ -278,11 +291,17 @@ int launch_lm_scan_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
 {
     ScanP a = scan_params(p, q);
     if (a.seqs == 0) return CONV_OK;
-    a.dense = p.S == 4 * scan_ns(p.S) && a.s1s.l == 1 && a.A_s == 1 && a.Bs.s == 1 && a.Cs.s == 1;
+    int ns = 1;
+    while (4 * ns < p.S) ns *= 2;
+    a.dense = p.S == 4 * ns && a.s1s.l == 1 && a.A_s == 1 && a.Bs.s == 1 && a.Cs.s == 1;
     with_type(p.dtype, [&](auto t) {
-        with_ns(p.S, [&](auto n) {
-            scan_step<decltype(t), decltype(n)::value><<<(int)lm_cdiv(a.seqs * a.C * 4, 256), 256, 0, s>>>(a);
-        });
+        typedef decltype(t) T;
+        const int grid = (int)lm_cdiv(a.seqs * a.C * 4, 256);
+        if (ns == 1) scan_step<T, 1><<<grid, 256, 0, s>>>(a);
+        else if (ns == 2) scan_step<T, 2><<<grid, 256, 0, s>>>(a);
+        else if (ns == 4) scan_step<T, 4><<<grid, 256, 0, s>>>(a);
+        else if (ns == 8) scan_step<T, 8><<<grid, 256, 0, s>>>(a);
+        else scan_step<T, 16><<<grid, 256, 0, s>>>(a);
     });
     return lm_launch_status();
 }

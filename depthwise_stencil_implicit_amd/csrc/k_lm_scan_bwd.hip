@@ -6,7 +6,7 @@
 // and dz = gy (sum_s C h + D x) silu'(z), ddt = dd softplus'.
 //
 // States come from the saved ones: CK steps are run forward again from a saved
-// state, a and h[t-1] stay in registers (2 CK NS = 128 values per lane), then
+// state, a and h[t-1] stay in registers (2 CK NS = 64 values per lane), then
 // the same steps are run in reverse.  Running the recurrence backwards instead
 // (h[t-1] = (h[t] - d x B) / a) would divide by factors near zero.
 //
@@ -59,23 +59,25 @@ __device__ __forceinline__ float halve_quad(float a, float b, bool second, bool 
     return second ? sb : sa;
 }
 
-// Steps of a tile: what LDS holds twice.
-template <int NS> constexpr int bwd_tile() { return NS <= 4 ? 32 : 128 / NS; }
+// Steps of a tile: LDS holds two of them, and its 128 threads of B take whole
+// states.
+constexpr int bwd_tile(int W) { return W <= 4 ? 32 : W <= 32 ? 16 : 8; }
 
-template <int NS, bool PRE> struct BwdLds {
-    static constexpr int TB = bwd_tile<NS>();
+template <int NS, int QW, bool PRE> struct BwdLds {
+    static constexpr int W = 4 * QW * NS, TB = bwd_tile(W);
     float2 in[2][TB][kCH];                                         // d, d x
     float s[2][TB][kCH];                                           // gy silu(z)
-    __attribute__((aligned(16))) float bc[2][TB * 8 * NS];
-    __attribute__((aligned(16))) float o[PRE ? 1 : 2][3][PRE ? 1 : TB][kRow];   // sums over s of r B, r A a h, C h
-    float red[PRE ? 1 : 2][4][PRE ? 1 : TB][8 * NS];               // a wave's dB, dC
+    __attribute__((aligned(16))) float bc[2][TB * 2 * W];
+    // Sums over s of r B, r A a h, C h.
+    __attribute__((aligned(16))) float o[PRE ? 1 : 2][3][PRE ? 1 : QW][PRE ? 1 : TB][kRow];
+    float red[PRE ? 1 : 2][4][PRE ? 1 : TB][2 * W];                // dB, dC of 16 channels
 };
 
 // The staging waves: tiles in descending order.
-template <typename T, int NS, bool PRE, bool DENSE>
-__device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdLds<NS, PRE> &sh, int tid)
+template <typename T, int NS, int QW, bool PRE, bool DENSE>
+__device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdLds<NS, QW, PRE> &sh, int tid)
 {
-    constexpr int TB = bwd_tile<NS>(), V = TB / 4;
+    constexpr int W = 4 * QW * NS, TB = bwd_tile(W), V = TB / 4;
     const int tr = tid / (256 / TB), tc = tid % (256 / TB) * V;
     const int tn = at.nc - tc;
     const int64_t sc = at.c0 + tc;
@@ -91,7 +93,7 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
     get_param<V>(p.bias, p.bias_s, sc, tn, bias);
     get_param<V>(p.D, p.D_s, sc, tn, D);
     struct Tile { Raw<T, V> x, dt, z, gy; } nt, ct, ot;   // being loaded; in the core; leaving
-    BcRegs<T, NS, TB, DENSE> bc(p, at, tid);
+    BcRegs<T, W, TB, DENSE> bc(p, at, tid);
     const auto fetch = [&](int64_t t) {
         int64_t l = t + tr < at.t1 ? t + tr : at.t1 - 1;
         if (l < at.t0) l = at.t0;   // before the chunk: loaded for nothing
@@ -120,12 +122,17 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
         if constexpr (!PRE) {
             const int rows = at.t1 - t < TB ? (int)(at.t1 - t) : TB;
             float *part = p.part_bc + (((at.c0 - at.g * p.Cg) / kCH + at.g * p.blocks_g) * p.rows_total +
-                                       at.sp.row0 * p.L + at.sp.start + t) * 8 * NS;
+                                       at.sp.row0 * p.L + at.sp.start + t) * 2 * W;
             const float *red = &sh.red[buf][0][0][0];
-            constexpr int n = TB * 8 * NS;
-            for (int e = tid; e < rows * 8 * NS; e += 256)
+            constexpr int n = TB * 2 * W;
+            for (int e = tid; e < rows * 2 * W; e += kStage)
                 part[e] = (red[e] + red[n + e]) + (red[2 * n + e] + red[3 * n + e]);
             if (t + tr >= at.t1) return;
+            const auto sum = [&](int which, int i) {
+                float v = sh.o[buf][which][0][tr][tc + i];
+                if constexpr (QW == 2) v += sh.o[buf][which][1][tr][tc + i];
+                return v;
+            };
             float ox[V], od[V], oz[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -135,11 +142,11 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
                 if (has_z) {
                     const float zv = ot.z.f(i), qz = sigmoid(zv);
                     s *= zv * qz;
-                    oz[i] = g * __builtin_fmaf(D[i], xv, sh.o[buf][2][tr][tc + i]) * silu_slope(zv, qz);
+                    oz[i] = g * __builtin_fmaf(D[i], xv, sum(2, i)) * silu_slope(zv, qz);
                 }
-                const float rb = sh.o[buf][0][tr][tc + i];
+                const float rb = sum(0, i);
                 ox[i] = __builtin_fmaf(D[i], s, d * rb);
-                float dd = __builtin_fmaf(kLn2, sh.o[buf][1][tr][tc + i], xv * rb);   // summed with A log2(e)
+                float dd = __builtin_fmaf(kLn2, sum(1, i), xv * rb);   // summed with A log2(e)
                 if (p.softplus) dd *= sigmoid(raw);
                 od[i] = dd;
                 sum_b[i] += i < tn ? dd : 0.f;
@@ -176,8 +183,8 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
     if (tiles > 0) leave(at_tile(0), buf ^ 1);
     if constexpr (!PRE) {
         // Sums of D's and the bias's gradients over the rows of the staging waves.
-        float(*sum)[kRow] = sh.o[0][0];
-        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (4 * NS + 2);
+        float(*sum)[kRow] = sh.o[0][0][0];
+        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (W + 2);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             lds_sync();
@@ -187,7 +194,7 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
             if (tid < at.nc) {
                 float v = 0.f;
                 for (int k = 0; k < TB; ++k) v += sum[k][tid];
-                pc[tid * (4 * NS + 2) + 4 * NS + which] = v;
+                pc[tid * (W + 2) + W + which] = v;
             }
         }
     }
@@ -195,22 +202,22 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
 
 // PRE: only the gradient that leaves a chunk at its front when none enters at
 // its end, and the chunk's sum of d.
-template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) void scan_bwd(const ScanP p)
+template <typename T, int NS, int QW, bool PRE, bool DENSE>
+__global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
 {
-    constexpr int CK = NS <= 4 ? 16 : 64 / NS, TB = bwd_tile<NS>();
-    constexpr int NB = NS < 4 ? 4 : NS;      // states per lane in the exchanges
-    __shared__ BwdLds<NS, PRE> sh;
+    constexpr int W = 4 * QW * NS, CK = ScanShape{NS, QW}.save_steps(), TB = bwd_tile(W), PARTS = TB / CK;
+    __shared__ BwdLds<NS, QW, PRE> sh;
     const ScanAt at = scan_at(p, p.chunks);
     if (at.t0 >= at.sp.len && at.ch > 0) return;
     if (PRE && at.ch == 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave >= 4) {
-        if (p.dense) bwd_stage<T, NS, PRE, true>(p, at, sh, (int)threadIdx.x - 256);
-        else bwd_stage<T, NS, PRE, false>(p, at, sh, (int)threadIdx.x - 256);
+    if (wave >= 4 * QW) {
+        bwd_stage<T, NS, QW, PRE, DENSE>(p, at, sh, (int)threadIdx.x - 256 * QW);
         return;
     }
 
-    const int lane = threadIdx.x & 63, q = lane >> 4, c = wave * 16 + (lane & 15);
+    const int lane = threadIdx.x & 63, lrow = lane >> 4, half = wave >> 2, q = half * 4 + lrow,
+              c = (wave & 3) * 16 + (lane & 15);
     const bool real = c < at.nc;
     const int64_t cc = at.c0 + c;
     float A2[NS], dA[NS] = {}, r[NS] = {};   // A log2(e); r: the gradient that enters from the step behind
@@ -226,19 +233,19 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
             const float d = p.carry_d[k];
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                r[i] = __builtin_fmaf(hw_exp2(d * A2[i]), r[i], p.carry_h[(k * 4 + q) * NS + i]);
+                r[i] = __builtin_fmaf(hw_exp2(d * A2[i]), r[i], p.carry_h[k * W + q * NS + i]);
         }
     }
-    const float *saved = p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * 4 * NS + q * NS;
+    const float *saved = p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * W + q * NS;
     float sum_d = 0.f;
     const int tiles = (int)((at.t1 - at.t0 + TB - 1) / TB);
-    float nh[2][NS] = {};                    // states saved in a tile, loaded a tile ahead
+    float nh[PARTS][NS] = {};                // states saved in a tile, loaded a tile ahead
     const auto fetch = [&](int k) {
         if (PRE || k < 0) return;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < PARTS; ++j) {
             if (real && at.t0 + (int64_t)k * TB + j * CK < at.t1)
-                load_f32<float, NS>(saved + ((int64_t)k * 2 + j) * p.C * 4 * NS, nh[j]);
+                load_f32<float, NS>(saved + ((int64_t)k * PARTS + j) * p.C * W, nh[j]);
         }
     };
     fetch(tiles - 1);
@@ -251,8 +258,8 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         const float *bc = sh.bc[buf];
         if constexpr (PRE) {
             for (int k0 = TB - 4; k0 >= 0; k0 -= 4) {
-                States4<NS> cs;
-                cs.load(bc + k0 * 8 * NS + 4 * NS + q * NS, lane);
+                States4<NS, W> cs;
+                cs.load(bc + k0 * 2 * W + W + q * NS, lane);
                 each<4>([&](auto step) {
                     constexpr int j = 3 - decltype(step)::value;
                     const float d = in[k0 + j][c].x, s = ss[k0 + j][c];
@@ -264,22 +271,26 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
                 });
             }
         } else {
-            float h0[2][NS];
+            float h0[PARTS][NS];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < PARTS; ++j)
 #pragma unroll
                 for (int i = 0; i < NS; ++i) h0[j][i] = nh[j][i];
             fetch(tile - 1);
 #pragma unroll 1
-            for (int part = 1; part >= 0; --part) {
+            for (int part = PARTS - 1; part >= 0; --part) {
                 if (t + part * CK >= at.t1) continue;
                 const int row0 = part * CK;
                 float a[CK][NS], h[CK + 1][NS];   // h[k]: the state before step k
 #pragma unroll
-                for (int i = 0; i < NS; ++i) h[0][i] = part ? h0[1][i] : h0[0][i];
+                for (int i = 0; i < NS; ++i) {
+                    h[0][i] = h0[0][i];
+#pragma unroll
+                    for (int j = 1; j < PARTS; ++j) h[0][i] = part == j ? h0[j][i] : h[0][i];
+                }
                 each<CK / 4>([&](auto group) {
                     constexpr int k0 = 4 * decltype(group)::value;
-                    Steps4<NS, false> g;
+                    Steps4<NS, W, false> g;
                     g.load(in, bc, row0 + k0, c, q, lane);
                     each<4>([&](auto step) {
                         constexpr int j = decltype(step)::value, k = k0 + j;
@@ -293,18 +304,15 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
                 each<CK / 4>([&](auto group) {
                     constexpr int k0 = CK - 4 - 4 * decltype(group)::value;
                     const int row = row0 + k0;
-                    Steps4<NS, true> g;
+                    Steps4<NS, W, true> g;
                     g.load(in, bc, row, c, q, lane);
-                    float s[4], o4[3][4];
-                    float zb[NB / 4][4], zc[NB / 4][4];   // sums over a row, spread over its lanes
+                    float s[4], o4[3][4], vb[4][NS], vc[4][NS];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[j] = ss[row + j][c];
                     each<4>([&](auto step) {
                         constexpr int j = 3 - decltype(step)::value, k = k0 + j;
-                        float vb[NB], vc[NB], ra = 0.f, rb = 0.f, ch = 0.f;
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) vb[i] = vc[i] = 0.f;
-                        if constexpr (NS == 4) back4<j>(g.c.v[0], g.b.v[0], s[j], h[k + 1], r, ch, rb);
+                        float ra = 0.f, rb = 0.f, ch = 0.f;
+                        if constexpr (NS == 2) back2<j>(g.c.v[0], g.b.v[0], s[j], h[k + 1], r, ch, rb);
                         else
                             each<NS>([&](auto state) {
                                 constexpr int i = decltype(state)::value;
@@ -315,34 +323,36 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
                             });
 #pragma unroll
                         for (int i = 0; i < NS; ++i) {
-                            vb[i] = r[i] * g.v[j].y;
-                            vc[i] = s[j] * h[k + 1][i];
+                            vb[j][i] = r[i] * g.v[j].y;
+                            vc[j][i] = s[j] * h[k + 1][i];
                             r[i] *= a[k][i];
                             const float w = r[i] * h[k][i];
                             ra = __builtin_fmaf(w, A2[i], ra);
                             dA[i] = __builtin_fmaf(w, g.v[j].x, dA[i]);
                         }
                         o4[0][j] = rb, o4[1][j] = ra, o4[2][j] = ch;
-#pragma unroll
-                        for (int m = 0; m < NB / 4; ++m) {
-                            const float v8[8] = {vb[4 * m], vb[4 * m + 1], vb[4 * m + 2], vb[4 * m + 3],
-                                                 vc[4 * m], vc[4 * m + 1], vc[4 * m + 2], vc[4 * m + 3]};
-                            halve_row(v8, zb[m][j], zc[m][j]);
-                        }
                     });
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) sh.o[buf][j][row + q][c] = quarters4(o4[j]);
-                    // A lane keeps B or C by bit 1, the earlier or later of two steps by bit 0.
-                    const bool kind = lane & 2, odd = lane & 1;
+                    for (int j = 0; j < 3; ++j) sh.o[buf][j][half][row + lrow][c] = rows4(o4[j]);
+                    // Four steps' dB and dC of two states (or of one): eight
+                    // values at a time meet in halve_row -- two steps', kind by
+                    // bit 2, state by bit 3 -- then the steps by bits 1 and 0.
+                    const int bit0 = lane & 1, bit1 = lane >> 1 & 1, bit2 = lane >> 2 & 1, bit3 = lane >> 3 & 1;
 #pragma unroll
-                    for (int m = 0; m < NB / 4; ++m) {
+                    for (int m = 0; m < NS; m += 2) {
+                        const auto at2 = [&](const float (&v)[4][NS], int j, int i) { return m + i < NS ? v[j][m + i] : 0.f; };
                         float z[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) z[j] = halve_quad(zb[m][j], zc[m][j], kind, true);
-                        const int i = 4 * m + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1);
-                        float *to = &sh.red[buf][wave][row + odd][kind * 4 * NS + q * NS + i];
-                        const float e = halve_quad(z[0], z[1], odd, false), l = halve_quad(z[2], z[3], odd, false);
-                        if (i < NS) to[0] = e, to[2 * 8 * NS] = l;
+                        for (int j = 0; j < 4; j += 2) {
+                            const float v8[8] = {at2(vb, j, 0), at2(vb, j, 1), at2(vc, j, 0), at2(vc, j, 1),
+                                                 at2(vb, j + 1, 0), at2(vb, j + 1, 1), at2(vc, j + 1, 0), at2(vc, j + 1, 1)};
+                            halve_row(v8, z[j], z[j + 1]);
+                        }
+                        // Steps 0, 1 and 2, 3 by bit 0, the two pairs by bit 1.
+                        const float e = halve_quad(z[0], z[1], bit0, false), l = halve_quad(z[2], z[3], bit0, false);
+                        const float all = halve_quad(e, l, bit1, true);
+                        if (NS > 1 || bit3 == 0)
+                            sh.red[buf][wave & 3][row + 2 * bit1 + bit0][bit2 * W + q * NS + m + (NS > 1 ? bit3 : 0)] = all;
                     }
                 });
             }
@@ -353,7 +363,7 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         if (!real) return;
         const int64_t k = (at.seq * p.chunks + at.ch) * p.C + cc;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) p.carry_h[(k * 4 + q) * NS + i] = r[i];
+        for (int i = 0; i < NS; ++i) p.carry_h[k * W + q * NS + i] = r[i];
         if (q == 0) p.carry_d[k] = sum_d;
     } else {
         // The staging waves' four barriers of the last sums.
@@ -361,9 +371,9 @@ template <typename T, int NS, bool PRE> __global__ __launch_bounds__(kThreads) v
         if (!real) return;
         if (p.ds && at.ch == 0) put_states<NS>(p.ds, p.dss, at.seq, cc, q * NS, p.S, r);
         // Parts of dA (4 NS per channel), dD and the bias, laid out [part][channel][4 NS + 2].
-        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (4 * NS + 2);
+        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (W + 2);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) pc[c * (4 * NS + 2) + q * NS + i] = dA[i];
+        for (int i = 0; i < NS; ++i) pc[c * (W + 2) + q * NS + i] = dA[i];
     }
 }
 
@@ -415,21 +425,26 @@ __global__ __launch_bounds__(256) void scan_bwd_c(const ScanP p, int W, float *d
 int launch_lm_scan_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
 {
     ScanP a = scan_params(p, q);
-    const int W = 4 * scan_ns(p.S);
+    const int W = scan_shape(p.S).width(), TB = bwd_tile(W);
     float *f = static_cast<float *>(ws);
     a.part_bc = f, f += a.blocks * a.rows_total * 2 * W;
     a.part_c = f, f += lm_cdiv(a.seqs * a.chunks * a.C * (W + 2), 4) * 4;
     a.carry_d = f, f += lm_cdiv(a.seqs * a.chunks * a.C, 4) * 4;
     a.carry_h = f;
-    a.dense = scan_dense(p, a, W <= 16 ? W / 4 : 4);
+    const bool dense = scan_dense(p, a, TB / 4, TB * W / 128);
     const int grid = (int)(a.seqs * a.chunks * a.blocks);
     with_type(p.dtype, [&](auto t) {
         typedef decltype(t) T;
-        with_ns(p.S, [&](auto n) {
-            constexpr int NS = decltype(n)::value;
+        with_ns(p.S, [&](auto n, auto w) {
+            constexpr int NS = decltype(n)::value, QW = decltype(w)::value, threads = 256 * QW + kStage;
             if (grid == 0) return;
-            if (a.chunks > 1) scan_bwd<T, NS, true><<<grid, kThreads, 0, s>>>(a);
-            scan_bwd<T, NS, false><<<grid, kThreads, 0, s>>>(a);
+            if (dense) {
+                if (a.chunks > 1) scan_bwd<T, NS, QW, true, true><<<grid, threads, 0, s>>>(a);
+                scan_bwd<T, NS, QW, false, true><<<grid, threads, 0, s>>>(a);
+            } else {
+                if (a.chunks > 1) scan_bwd<T, NS, QW, true, false><<<grid, threads, 0, s>>>(a);
+                scan_bwd<T, NS, QW, false, false><<<grid, threads, 0, s>>>(a);
+            }
         });
         if (a.rows_total > 0) scan_bwd_bc<T><<<(int)lm_cdiv(a.rows_total * 2 * W * p.G, 256), 256, 0, s>>>(
             a.part_bc, a.rows_total, p.L, a.blocks_g, (int)p.G, (int)p.S, W, static_cast<T *>(q[LM_DB]),

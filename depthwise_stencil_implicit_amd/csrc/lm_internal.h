@@ -13,20 +13,21 @@ namespace miconv {
 constexpr int LM_MAX_TAPS = 8;
 constexpr int LM_MAX_STATES = 64;
 
-// Scan: channels of one workgroup, steps of one staged tile.
+// Scan: channels of one workgroup; how S states lie over lanes.  Eight rows of
+// 16 lanes share a channel (four up to four states), each holds ns of them.
 constexpr int LM_SCAN_CH = 64;
-constexpr int LM_SCAN_TB = 32;
-
-// States per lane: four lanes share a channel.
-inline int scan_ns(int64_t S)
+struct ScanShape {
+    int ns, qw;                                       // states per lane, core waves per 16 channels
+    constexpr int width() const { return 4 * qw * ns; }         // states with padding
+    constexpr int save_steps() const { return ns <= 2 ? 16 : 32 / ns; }   // steps between saved states
+};
+inline ScanShape scan_shape(int64_t S)
 {
+    if (S <= 4) return {1, 1};
     int ns = 1;
-    while (4 * ns < S) ns *= 2;
-    return ns;
+    while (8 * ns < S) ns *= 2;
+    return {ns, 2};
 }
-// Steps between saved states, the length the backward kernel keeps in
-// registers: 64 values of exp(d A) per lane.
-inline int scan_save_steps(int64_t S) { return scan_ns(S) <= 4 ? 16 : 64 / scan_ns(S); }
 inline int64_t lm_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // 4-bit products: bytes of x made contiguous (0: x's rows are), and the parts

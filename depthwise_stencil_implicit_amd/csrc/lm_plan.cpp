@@ -124,19 +124,32 @@ void conv_chunks(lm_plan_t &p, int64_t max_len, int64_t per_thread, int64_t min_
     p.chunks = std::max<int64_t>(1, lm_cdiv(max_len, rows));
 }
 
-// The scan along one sequence is serial, and one workgroup per 64 channels
-// keeps a compute unit's four SIMDs at work.  With fewer workgroups than
-// compute units the long axis is split, at the price of a first pass over
-// the chunks for the states between them (about 0.9 of the main pass).
+// The scan along one sequence is serial; a workgroup per 64 channels fills the
+// SIMDs of one compute unit.  Splitting the long axis fills more of them, at
+// the price of a first pass over the chunks for the states between them (0.6
+// of the main pass).  Of the chunk counts up to 64 the one with the least
+// estimated time is taken: rounds of 256 workgroups times the chunk's length,
+// plus 48 steps that a workgroup's start costs.
 void scan_chunks(lm_plan_t &p, int64_t max_len)
 {
-    const int64_t units = p.seqs * p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH);
+    constexpr int64_t tile = 32;
+    const int64_t blocks = p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH);
+    const bool packed = p.t[LM_OFFSETS].rank > 0;
     int64_t rows = p.args.chunk;
     if (rows <= 0) {
-        const int64_t want = units < 160 ? lm_cdiv(512, std::max<int64_t>(units, 1)) : 1;
-        rows = std::max<int64_t>(lm_cdiv(std::max<int64_t>(max_len, 1), want), 2 * LM_SCAN_TB);
+        rows = std::max<int64_t>(max_len, 1);
+        double best = 0;
+        for (int64_t n = 1; n <= 64; ++n) {
+            const int64_t chunk = lm_cdiv(lm_cdiv(std::max<int64_t>(max_len, 1), n), tile) * tile;
+            if (n > 1 && chunk < 2 * tile) break;
+            // Packed sequences are of unlike lengths: whole chunks of all rows and a half each.
+            const double groups = (packed ? (double)p.L / chunk + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(max_len, chunk)) * blocks;
+            const double rounds = packed ? std::max(1.0, groups / 256) : (double)lm_cdiv((int64_t)groups, 256);
+            const double cost = rounds * (chunk + 48) * (n > 1 ? 1.6 : 1.0) + (n > 1 ? 48 : 0);
+            if (n == 1 || cost < best) best = cost, rows = chunk;
+        }
     }
-    p.chunk = lm_cdiv(rows, LM_SCAN_TB) * LM_SCAN_TB;
+    p.chunk = lm_cdiv(rows, tile) * tile;
     p.chunks = std::max<int64_t>(1, lm_cdiv(max_len, p.chunk));
 }
 
@@ -292,7 +305,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
         p.bytes = cells * e * (bwd ? 2 + k.has(LM_DX) : 2) + st + (bwd ? 2 : 1) * p.C * (p.K + k.has(LM_BIAS)) * e;
         p.flops = cells * (bwd ? 6 * p.K + 2 * act : 2 * p.K + act);
     } else {
-        const int ns = scan_ns(p.S), W = 4 * ns, ck = scan_save_steps(p.S);
+        const int W = scan_shape(p.S).width(), ck = scan_shape(p.S).save_steps();
         if (!step) scan_chunks(p, max_len);
         else p.chunk = p.chunks = 1;
         p.saved_floats = step ? 0 : (packed ? p.L / ck + p.seqs + 1 : N * lm_cdiv(p.L, ck)) * p.C * W;

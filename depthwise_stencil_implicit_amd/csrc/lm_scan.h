@@ -1,19 +1,24 @@
 // What the scan's kernels share: parameters, the staged tile and cross-lane sums.
 //
 // A workgroup owns 64 channels of one group and walks along the sequence in
-// tiles.  Four core waves run the recurrence, 16 channels each: lane 16 q + c
-// holds NS states of channel c, a quarter (S <= 4 NS; states past S have A = B =
-// C = 0).  B and C are the same for all channels, so a row of 16 lanes loads 16
-// different values of its quarter -- four steps of four states -- with one LDS
-// read and takes each by a row broadcast in the instruction that uses it;
-// reading them to every lane kept LDS busy 100 of the 195 clocks of a step.
-// Four staging waves work a tile ahead of them and one behind: they load a
+// tiles.  Its core waves run the recurrence: a row of 16 lanes holds NS states
+// of 16 channels, a wave four such rows, and QW = 2 waves share the channels
+// (S <= 4 QW NS = W; states past S have A = B = C = 0).  One wave alone issues a
+// vector instruction every 5 clocks or so, two every 3, hence the eight rows
+// where four would need a tenth fewer instructions.
+//
+// B and C are the same for all channels, so a row loads 16 different values of
+// its states with one LDS read and takes each by a row broadcast in the
+// instruction that uses it; reading them to every lane kept LDS busy half the
+// time.
+//
+// Four staging waves work a tile ahead of the core and one behind: they load a
 // tile, put d = softplus(dt + dt_bias) and d x -- one transcendental chain per
-// (step, channel), not four -- and B and C in f32 into LDS, and take the core's
-// sums out again through D, the gate and the stores.  x, dt and z cross from
-// HBM once and stay in the staging waves' registers between the two.  With one
-// kind of wave that did both in turn, a SIMD stood idle at every barrier and
-// behind every store: 200 us for 8 x 1024 x 2048 channels of 16 states.
+// (step, channel), not one per lane -- and B and C in f32 into LDS, and take the
+// core's sums out again through D, the gate and the stores.  x, dt and z cross
+// from HBM once and stay in the staging waves' registers between the two.  With
+// one kind of wave that did both in turn, a SIMD stood idle at every barrier
+// and behind every store (twice the time).
 #pragma once
 
 #include <type_traits>
@@ -43,7 +48,7 @@ struct ScanP {
 };
 
 constexpr int kCH = LM_SCAN_CH;
-constexpr int kThreads = 512;        // four core waves, four staging waves
+constexpr int kStage = 256;          // staging threads, behind the core's
 constexpr int kRow = kCH + 16;       // padded f32 row: four rows x 16 channels on 64 banks
 
 // Loads of a staging thread never stand behind a branch: a register that two
@@ -131,8 +136,8 @@ template <int CK> __device__ __forceinline__ int64_t saved_at(const ScanP &p, co
 // B and C of a tile on their way to LDS: threads 0 .. 127 hold n neighbouring
 // states of one row of B, threads 128 .. 255 of C.  DENSE: states are
 // contiguous and S a multiple of n.
-template <typename T, int NS, int TB, bool DENSE> struct BcRegs {
-    static constexpr int n = TB * 4 * NS / 128;
+template <typename T, int W, int TB, bool DENSE> struct BcRegs {
+    static constexpr int n = TB * W / 128;
     Raw<T, n> v;
     const T *base;
     int64_t sl;
@@ -141,8 +146,8 @@ template <typename T, int NS, int TB, bool DENSE> struct BcRegs {
     {
         const int e = tid % 128 * n;
         const S4 &st = tid < 128 ? p.Bs : p.Cs;
-        row = e / (4 * NS), s0 = e % (4 * NS);
-        to = row * (8 * NS) + (tid < 128 ? 0 : 4 * NS) + s0;
+        row = e / W, s0 = e % W;
+        to = row * (2 * W) + (tid < 128 ? 0 : W) + s0;
         base = static_cast<const T *>(tid < 128 ? p.Bm : p.Cm) + a.sp.row0 * st.n + a.g * st.g + a.sp.start * st.l;
         if (DENSE) base += s0 < p.S ? s0 : 0;
         sl = st.l;
@@ -153,12 +158,12 @@ template <typename T, int NS, int TB, bool DENSE> struct BcRegs {
         if constexpr (DENSE) v = load_raw<T, n>(q);
         else {
             v.zero();
-            const int64_t ss = threadIdx.x % 256 < 128 ? p.Bs.s : p.Cs.s;
+            const int64_t ss = threadIdx.x % kStage < 128 ? p.Bs.s : p.Cs.s;
 #pragma unroll
             for (int i = 0; i < n; ++i) v.set(i, q[(s0 + i < p.S ? s0 + i : p.S - 1) * ss]);
         }
     }
-    __device__ __forceinline__ void put(const ScanP &p, float *sh, int64_t t, int64_t t1) const   // [TB][2][4 NS]
+    __device__ __forceinline__ void put(const ScanP &p, float *sh, int64_t t, int64_t t1) const   // [TB][2][W]
     {
 #pragma unroll
         for (int i = 0; i < n; ++i) sh[to + i] = t + row < t1 && s0 + i < p.S ? v.f(i) : 0.f;
@@ -178,17 +183,17 @@ template <int N> __device__ __forceinline__ float row_bcast(float v)
     return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), 0x150 + N, 0xf, 0xf, true));
 }
 
-// A quarter's states of B or C for four steps: value j NS + i (step j, state
-// i) in register / 16, lane % 16 of the quarter's row.
-template <int NS> struct States4 {
+// A row's states of B or C for four steps: value j NS + i (step j, state i) in
+// register / 16, lane % 16.
+template <int NS, int W> struct States4 {
     static constexpr int n = NS < 4 ? 1 : NS / 4;
     float v[n];
-    __device__ __forceinline__ void load(const float *bc, int lane)   // bc: the quarter's states of the first step
+    __device__ __forceinline__ void load(const float *bc, int lane)   // bc: the row's states of the first step
     {
 #pragma unroll
         for (int m = 0; m < n; ++m) {
             const int f = (m * 16 + (lane & 15)) % (4 * NS);
-            v[m] = bc[f / NS * (8 * NS) + f % NS];
+            v[m] = bc[f / NS * (2 * W) + f % NS];
         }
     }
     template <int J, int I> __device__ __forceinline__ float at() const
@@ -197,69 +202,53 @@ template <int NS> struct States4 {
     }
 };
 
-// y[j] = sum_i C[j][i] h[j][i] of four steps and four states.  The compiler
+// y[j] = sum_i C[j][i] h[j][i] of four steps and two states.  The compiler
 // folds a row broadcast into a multiplication but not into a multiply-add.
 // The s_nop gives c the two wait states that a cross-lane read needs, should
 // it have been moved by the vector unit just before.
-__device__ __forceinline__ void dot4x4(float c, const float (&h)[4][4], float (&y)[4])
+__device__ __forceinline__ void dot4x2(float c, const float (&h)[4][2], float (&y)[4])
 {
     asm("s_nop 1\n\t"
         "v_mul_f32_dpp %0, %4, %5 row_newbcast:0 row_mask:0xf bank_mask:0xf\n\t"
-        "v_mul_f32_dpp %1, %4, %9 row_newbcast:4 row_mask:0xf bank_mask:0xf\n\t"
-        "v_mul_f32_dpp %2, %4, %13 row_newbcast:8 row_mask:0xf bank_mask:0xf\n\t"
-        "v_mul_f32_dpp %3, %4, %17 row_newbcast:12 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %4, %7 row_newbcast:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %4, %9 row_newbcast:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %4, %11 row_newbcast:6 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %4, %6 row_newbcast:1 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %1, %4, %10 row_newbcast:5 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %2, %4, %14 row_newbcast:9 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %3, %4, %18 row_newbcast:13 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %4, %7 row_newbcast:2 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %1, %4, %11 row_newbcast:6 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %2, %4, %15 row_newbcast:10 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %3, %4, %19 row_newbcast:14 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %4, %8 row_newbcast:3 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %1, %4, %12 row_newbcast:7 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %2, %4, %16 row_newbcast:11 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %3, %4, %20 row_newbcast:15 row_mask:0xf bank_mask:0xf"
+        "v_fmac_f32_dpp %1, %4, %8 row_newbcast:3 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %10 row_newbcast:5 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %12 row_newbcast:7 row_mask:0xf bank_mask:0xf"
         : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
-        : "v"(c), "v"(h[0][0]), "v"(h[0][1]), "v"(h[0][2]), "v"(h[0][3]), 
-          "v"(h[1][0]), "v"(h[1][1]), "v"(h[1][2]), "v"(h[1][3]), "v"(h[2][0]), "v"(h[2][1]), "v"(h[2][2]), "v"(h[2][3]), 
-          "v"(h[3][0]), "v"(h[3][1]), "v"(h[3][2]), "v"(h[3][3]));
+        : "v"(c), "v"(h[0][0]), "v"(h[0][1]), "v"(h[1][0]), "v"(h[1][1]), "v"(h[2][0]), "v"(h[2][1]), "v"(h[3][0]),
+          "v"(h[3][1]));
 }
 
-// One step of the backward recurrence for four states: r[i] += C[J][i] s,
+// One step of the backward recurrence for two states: r[i] += C[J][i] s,
 // ch = sum_i C[J][i] h[i], rb = sum_i B[J][i] r[i] (the new r).
 template <int J>
-__device__ __forceinline__ void back4(float c, float b, float s, const float (&h)[4], float (&r)[4], float &ch, float &rb)
+__device__ __forceinline__ void back2(float c, float b, float s, const float (&h)[2], float (&r)[2], float &ch, float &rb)
 {
     asm("s_nop 1\n\t"
-        "v_fmac_f32_dpp %0, %6, %8 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %1, %6, %8 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %3, %6, %8 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
-        "v_mul_f32_dpp %4, %6, %9 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
-        "v_mul_f32_dpp %5, %7, %0 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %6, %10 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %5, %7, %1 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %6, %11 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %5, %7, %2 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %6, %12 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %5, %7, %3 row_newbcast:%16 row_mask:0xf bank_mask:0xf"
-        : "+&v"(r[0]), "+&v"(r[1]), "+&v"(r[2]), "+&v"(r[3]), "=&v"(ch), "=&v"(rb)
-        : "v"(c), "v"(b), "v"(s), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]), "n"(4 * J), "n"(4 * J + 1),
-          "n"(4 * J + 2), "n"(4 * J + 3));
+        "v_fmac_f32_dpp %0, %4, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %6 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %4, %7 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %5, %0 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %8 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %5, %1 row_newbcast:%10 row_mask:0xf bank_mask:0xf"
+        : "+&v"(r[0]), "+&v"(r[1]), "=&v"(ch), "=&v"(rb)
+        : "v"(c), "v"(b), "v"(s), "v"(h[0]), "v"(h[1]), "n"(2 * J), "n"(2 * J + 1));
 }
 
 // What a lane reads from LDS for four steps: d and d x of its channel, B and
 // (WITH_C) C of its row.
-template <int NS, bool WITH_C> struct Steps4 {
+template <int NS, int W, bool WITH_C> struct Steps4 {
     float2 v[4];
-    States4<NS> b, c;
+    States4<NS, W> b, c;
     __device__ __forceinline__ void load(const float2 (*in)[kCH], const float *bc, int k, int ch, int q, int lane)
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = in[k + j][ch];
-        b.load(bc + k * 8 * NS + q * NS, lane);
-        if constexpr (WITH_C) c.load(bc + k * 8 * NS + 4 * NS + q * NS, lane);
+        b.load(bc + k * 2 * W + q * NS, lane);
+        if constexpr (WITH_C) c.load(bc + k * 2 * W + W + q * NS, lane);
     }
 };
 
@@ -295,8 +284,8 @@ __device__ __forceinline__ float halve32(float a, float b)
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// Sums over the four quarters of four values; quarter q receives that of v[q].
-__device__ __forceinline__ float quarters4(const float (&v)[4])
+// Sums over a wave's four rows of four values; row r receives that of v[r].
+__device__ __forceinline__ float rows4(const float (&v)[4])
 {
     return halve32(halve16(v[0], v[1]), halve16(v[2], v[3]));
 }
@@ -330,13 +319,12 @@ inline ScanP scan_params(const lm_plan_t &p, lm_ptrs q)
     return a;
 }
 
-// Whether the staging waves may load V = 8 (backward: fewer above 16 states)
-// channels and n states at once.
-inline bool scan_dense(const lm_plan_t &p, const ScanP &a, int n)
+// Whether the staging waves may load V channels and n states at once.
+inline bool scan_dense(const lm_plan_t &p, const ScanP &a, int V, int n)
 {
     for (int s : {LM_X, LM_DT, LM_Z, LM_GY})
         if (p.t[s].rank && p.t[s].strides[1] != 1 && p.C > 1) return false;
-    return p.C >= 8 && p.S % n == 0 && (a.Bs.s == 1 || p.S == 1) && (a.Cs.s == 1 || p.S == 1);
+    return p.C >= V && p.S % n == 0 && (a.Bs.s == 1 || p.S == 1) && (a.Cs.s == 1 || p.S == 1);
 }
 
 // f(T) for the element type, f(NS) for the states per lane.
@@ -348,13 +336,12 @@ template <typename F> void with_type(int32_t dtype, F f)
 }
 template <typename F> void with_ns(int64_t S, F f)
 {
-    switch (scan_ns(S)) {
-    case 1: f(std::integral_constant<int, 1>()); break;
-    case 2: f(std::integral_constant<int, 2>()); break;
-    case 4: f(std::integral_constant<int, 4>()); break;
-    case 8: f(std::integral_constant<int, 8>()); break;
-    case 16: f(std::integral_constant<int, 16>()); break;
-    }
+    const ScanShape s = scan_shape(S);
+    if (s.qw == 1) f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    else if (s.ns == 1) f(std::integral_constant<int, 1>(), std::integral_constant<int, 2>());
+    else if (s.ns == 2) f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
+    else if (s.ns == 4) f(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+    else f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
 }
 
 }  // namespace miconv

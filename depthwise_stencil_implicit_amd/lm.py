@@ -290,12 +290,12 @@ _abi_scan = A.LM_SCAN
 def _new_saved(x, A_, offsets) -> torch.Tensor:
     """Room for the states before every 16th step (fewer steps above 16 states)."""
     s = A_.shape[-1]
-    ns = 1
-    while 4 * ns < s:
+    ns, rows = 1, 4 if s <= 4 else 8
+    while rows * ns < s:
         ns *= 2
-    ck = 16 if ns <= 4 else max(1, 64 // ns)
+    ck = 16 if ns <= 2 else max(1, 32 // ns)
     count = x.shape[0] * -(-x.shape[2] // ck) if offsets is None else x.shape[2] // ck + offsets.shape[0]
-    return torch.empty(count * x.shape[1] * 4 * ns, device=x.device)
+    return torch.empty(count * x.shape[1] * rows * ns, device=x.device)
 
 
 def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False, state=None,
