@@ -19,10 +19,8 @@
 namespace miconv {
 namespace {
 
-// Loads past the end repeat the last row: behind a branch their registers
-// would be waited for where the paths meet.
-constexpr int kRowsAhead = 8;   // rows whose loads are in flight while the previous ones are used
-constexpr int kRowsAheadBwd = 4;
+// Rows of a block: their loads are in flight while the block before is used.
+constexpr int kRows = 8, kRowsBwd = 4;
 
 struct ConvP {
     const void *x, *w, *b, *s0, *gy, *gs;
@@ -58,7 +56,7 @@ template <typename T, int V> __device__ __forceinline__ void get(const T *p, int
 template <typename T, int V> __device__ __forceinline__ void put(T *p, int64_t cs, const float (&v)[V])
 {
     if constexpr (V == 1) *p = from_f32<T>(v[0]);
-    else store_f32<T, V>(p, v);
+    else store_f32<T, V, true>(p, v);
 }
 // V channels of one row at any channel stride (state rows, parameters).
 template <typename T, int V> __device__ __forceinline__ void get_strided(const T *p, int64_t cs, float (&o)[V])
@@ -98,6 +96,17 @@ __device__ __forceinline__ void get_weights(const ConvP &p, int64_t c, float (&w
     if (p.b) get_strided<T, V>(static_cast<const T *>(p.b) + c * p.bs, p.bs, b);
 }
 
+// R rows of V channels from row t of a walk on, p at row t.  Rows past the last
+// repeat it: behind a branch their registers would be waited for where the
+// paths meet.
+template <typename T, int V, int R>
+__device__ __forceinline__ void get_rows(const T *p, int64_t stride, int64_t t, int64_t last, Raw<T, V> (&o)[R])
+{
+    const int left = last - t < R ? (int)(last - t) : R;
+#pragma unroll
+    for (int r = 0; r < R; ++r) o[r] = load_raw<T, V>(p + (r < left ? r : left) * stride);
+}
+
 // Row t of the extended input (t >= -(K-1)): x, the incoming state, or zero.
 template <typename T, int K, int V>
 __device__ __forceinline__ void get_front(const ConvP &p, int64_t seq, const T *x, int64_t c, int64_t t, float (&o)[V])
@@ -120,50 +129,51 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
     const int64_t t0 = ch * p.chunk;
     if (t0 >= sp.len && ch > 0) return;
     const int64_t t1 = ch == p.chunks - 1 ? sp.len : (t0 + p.chunk < sp.len ? t0 + p.chunk : sp.len);
-    const T *x = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
-    T *y = static_cast<T *>(p.y) + sp.row0 * p.ys.n + c * p.ys.c + sp.start * p.ys.l;
+    const T *x0 = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
+    const T *x = x0 + t0 * p.xs.l;
+    T *y = static_cast<T *>(p.y) + sp.row0 * p.ys.n + c * p.ys.c + (sp.start + t0) * p.ys.l;
 
+    Raw<T, V> next[kRows];
+    if (t0 < t1) get_rows(x, p.xs.l, t0, t1 - 1, next);
     float w[K][V], b[V];
     get_weights<T, K, V>(p, c, w, b);
-    float h[K][V];   // h[0 .. K-2]: the rows in front, oldest first; h[K-1]: the current row
+    float h[K - 1 + kRows][V];   // the K-1 rows in front of the block, then the block
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) get_front<T, K, V>(p, seq, x, c, t0 - (K - 1) + k, h[k]);
-
-    Raw<T, V> next[kRowsAhead];
-    auto fetch = [&](int64_t t) {
+    for (int k = 0; k < K - 1; ++k) get_front<T, K, V>(p, seq, x0, c, t0 - (K - 1) + k, h[k]);
+    for (int64_t t = t0; t < t1; t += kRows) {
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r)
-            next[r] = load_raw<T, V>(x + (t + r < t1 ? t + r : t1 - 1) * p.xs.l);
-    };
-    if (t0 < t1) fetch(t0);
-    for (int64_t t = t0; t < t1; t += kRowsAhead) {
-        Raw<T, V> cur[kRowsAhead];
+        for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r) cur[r] = next[r];
-        fetch(t + kRowsAhead);
+            for (int i = 0; i < V; ++i) h[K - 1 + r][i] = next[r].f(i);
+        x += kRows * p.xs.l;
+        get_rows(x, p.xs.l, t + kRows, t1 - 1, next);
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r) {
+        for (int r = 0; r < kRows; ++r) {
             if (t + r >= t1) break;
             float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                h[K - 1][i] = cur[r].f(i);
                 float a = b[i];
 #pragma unroll
-                for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[k][i], a);
+                for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[r + k][i], a);
                 o[i] = p.silu ? silu(a) : a;
             }
-            put<T, V>(y + (t + r) * p.ys.l, p.ys.c, o);
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                for (int i = 0; i < V; ++i) h[k][i] = h[k + 1][i];
+            put<T, V>(y + r * p.ys.l, p.ys.c, o);
         }
+        y += kRows * p.ys.l;
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[k][i] = h[kRows + k][i];
     }
     if (K > 1 && p.s1 && t1 == sp.len) {
         T *s1 = static_cast<T *>(p.s1) + seq * p.s1s.n + c * p.s1s.c;
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) put_strided<T, V>(s1 + k * p.s1s.l, p.s1s.c, h[k]);
+        for (int k = 0; k < K - 1; ++k) {
+            float v[V];
+            get_front<T, K, V>(p, seq, x0, c, t1 - (K - 1) + k, v);
+            put_strided<T, V>(s1 + k * p.s1s.l, p.s1s.c, v);
+        }
     }
 }
 
@@ -209,13 +219,15 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
     }
 }
 
-// Gradients in one walk: at row r the pre-activation is recomputed from x,
-// g[r] = gy act'(p) joins a window of K rows, dx[r-K+1] leaves it, and dw, db
-// gather over the chunk's own rows.  The walk runs K-1 rows past the chunk for
-// dx's window (their dw belongs to the next chunk).  The sums of a chunk go to
-// part [seq * chunks + chunk][C][K+1]; conv_bwd_sums adds them in a fixed order.
+// Gradients in one walk, a block of rows at a time: the pre-activations are
+// recomputed from x, g = gy act'(p) joins the K-1 rows of g before the block,
+// dx leaves K-1 rows behind it, and dw, db gather over the chunk's own rows.
+// The walk runs K-1 rows past the chunk for dx (their dw belongs to the next
+// chunk).  The sums of a chunk go to part [seq * chunks + chunk][C][K+1];
+// conv_bwd_sums adds them in a fixed order.
 template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_bwd(const ConvP p)
 {
+    constexpr int R = kRowsBwd;
     int64_t seq, ch, c;
     if (!conv_item<V>(p, seq, ch, c)) return;
     const SeqSpan sp = seq_span(p.off, seq, p.L);
@@ -223,79 +235,69 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
     float dw[K][V] = {}, db[V] = {};
     if (t0 < sp.len || ch == 0) {
         const int64_t t1 = ch == p.chunks - 1 ? sp.len : (t0 + p.chunk < sp.len ? t0 + p.chunk : sp.len);
-        const T *x = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
-        const T *gy = static_cast<const T *>(p.gy) + sp.row0 * p.gys.n + c * p.gys.c + sp.start * p.gys.l;
-        T *dx = p.dx ? static_cast<T *>(p.dx) + sp.row0 * p.dxs.n + c * p.dxs.c + sp.start * p.dxs.l : nullptr;
+        const T *x0 = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
+        const T *x = x0 + t0 * p.xs.l;
+        const T *gy = static_cast<const T *>(p.gy) + sp.row0 * p.gys.n + c * p.gys.c + (sp.start + t0) * p.gys.l;
+        // Where the row of the gradient that the block's first row completes goes.
+        T *dx = p.dx ? static_cast<T *>(p.dx) + sp.row0 * p.dxs.n + c * p.dxs.c + (sp.start + t0 - (K - 1)) * p.dxs.l : nullptr;
+        const int64_t end = t1 + (K - 1);                       // rows walked
+        const int64_t has = end < sp.len ? end : sp.len;        // rows that exist
+        Raw<T, V> nx[R], ng[R];
+        if (has > 0) get_rows(x, p.xs.l, t0, has - 1, nx), get_rows(gy, p.gys.l, t0, has - 1, ng);
         float w[K][V], b[V];
         get_weights<T, K, V>(p, c, w, b);
-        float h[K][V], g[K][V];   // g[k]: the gradient at row r - k
+        float h[K - 1 + R][V], g[K - 1 + R][V];   // the K-1 rows in front of the block, then the block
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) {
-            get_front<T, K, V>(p, seq, x, c, t0 - (K - 1) + k, h[k]);
+            get_front<T, K, V>(p, seq, x0, c, t0 - (K - 1) + k, h[k]);
 #pragma unroll
             for (int i = 0; i < V; ++i) g[k][i] = 0.f;
         }
-        const int64_t end = t1 + (K - 1);                       // rows walked
-        const int64_t has = end < sp.len ? end : sp.len;        // rows that exist
-        Raw<T, V> nx[kRowsAheadBwd], ng[kRowsAheadBwd];
-        auto fetch = [&](int64_t t) {
+        for (int64_t t = t0; t < end; t += R) {
 #pragma unroll
-            for (int r = 0; r < kRowsAheadBwd; ++r) {
-                const int64_t l = t + r < has ? t + r : has - 1;
-                nx[r] = load_raw<T, V>(x + l * p.xs.l);
-                ng[r] = load_raw<T, V>(gy + l * p.gys.l);
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[K - 1 + r][i] = nx[r].f(i), g[K - 1 + r][i] = ng[r].f(i);
+            if (has > 0) {
+                x += R * p.xs.l, gy += R * p.gys.l;
+                get_rows(x, p.xs.l, t + R, has - 1, nx), get_rows(gy, p.gys.l, t + R, has - 1, ng);
             }
-        };
-        if (has > 0) fetch(t0);
-        for (int64_t t = t0; t < end; t += kRowsAheadBwd) {
-            Raw<T, V> cx[kRowsAheadBwd], cg[kRowsAheadBwd];
+            // MASK: rows past the chunk's end, at most in its last blocks.
+            const auto gather = [&](auto masked) {
+                constexpr bool MASK = decltype(masked)::value;
 #pragma unroll
-            for (int r = 0; r < kRowsAheadBwd; ++r) cx[r] = nx[r], cg[r] = ng[r];
-            if (has > 0) fetch(t + kRowsAheadBwd);
-#pragma unroll
-            for (int r = 0; r < kRowsAheadBwd; ++r) {
-                const int64_t row = t + r;
-                if (row >= end) break;
-#pragma unroll
-                for (int k = K - 1; k > 0; --k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[k][i] = g[k - 1][i];
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[0][i] = 0.f;
-                if (row < has) {
+                for (int r = 0; r < R; ++r) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        h[K - 1][i] = cx[r].f(i);
-                        float gi = cg[r].f(i);
+                        float v = g[K - 1 + r][i];
                         if (p.silu) {
                             float a = b[i];
 #pragma unroll
-                            for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[k][i], a);
-                            gi *= silu_slope(a, sigmoid(a));
+                            for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[r + k][i], a);
+                            v *= silu_slope(a, sigmoid(a));
                         }
-                        g[0][i] = gi;
+                        if (MASK && t + r >= has) v = 0.f;
+                        g[K - 1 + r][i] = v;
+                        if (MASK && t + r >= t1) continue;
+                        db[i] += v;
+#pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k][i] = __builtin_fmaf(v, h[r + k][i], dw[k][i]);
                     }
-                    if (row < t1) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            db[i] += g[0][i];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) dw[k][i] = __builtin_fmaf(g[0][i], h[k][i], dw[k][i]);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) h[k][i] = h[k + 1][i];
                 }
-                const int64_t to = row - (K - 1);   // the row whose gradient is complete
+            };
+            if (t + R <= t1) gather(std::false_type());
+            else gather(std::true_type());
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t to = t + r - (K - 1);   // the row whose gradient is complete
+                if (to >= t1) break;
                 if (to < t0 && !(ch == 0 && to < 0)) continue;
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     o[i] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < K; ++k) o[i] = __builtin_fmaf(w[k][i], g[k][i], o[i]);
+                    for (int k = 0; k < K; ++k) o[i] = __builtin_fmaf(w[k][i], g[K - 1 + r - k][i], o[i]);
                 }
                 if (p.gs && to >= sp.len - (K - 1)) {
                     float v[V];
@@ -306,12 +308,17 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
                     for (int i = 0; i < V; ++i) o[i] += v[i];
                 }
                 if (to >= 0) {
-                    if (dx) put<T, V>(dx + to * p.dxs.l, p.dxs.c, o);
+                    if (dx) put<T, V>(dx + r * p.dxs.l, p.dxs.c, o);
                 } else if (p.ds) {
                     put_strided<T, V>(static_cast<T *>(p.ds) + seq * p.dss.n + c * p.dss.c + (K - 1 + to) * p.dss.l,
                                       p.dss.c, o);
                 }
             }
+            if (dx) dx += R * p.dxs.l;
+#pragma unroll
+            for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[k][i] = h[R + k][i], g[k][i] = g[R + k][i];
         }
     }
     if (p.part) {
@@ -432,7 +439,7 @@ template <typename T> void step(const lm_plan_t &p, ConvP a, hipStream_t s)
 
 template <typename T> void bwd(const lm_plan_t &p, ConvP a, lm_ptrs q, hipStream_t s)
 {
-    constexpr int V = 4;
+    constexpr int V = 2;
     const bool vec = a.xs.c == 1 && a.gys.c == 1 && (!a.dx || a.dxs.c == 1) && a.C >= V;
     with_taps(p.K, [&](auto k) {
         constexpr int K = decltype(k)::value;

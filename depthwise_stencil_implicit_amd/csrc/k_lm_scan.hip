@@ -102,10 +102,9 @@ __device__ __forceinline__ void fwd_stage(const ScanP &p, const ScanAt &at, FwdL
 // PRE: only the state that leaves a chunk entered with zero, and the chunk's
 // sum of d (its decay is exp(A sum d)); the main pass folds them into the
 // state its chunk starts from.
-// Up to two states per lane of 16-bit calls fit two workgroups on a compute
-// unit (six waves per SIMD).
+// Up to 16 states two workgroups fit a compute unit.
 template <typename T, int NS, int QW, bool PRE, bool DENSE>
-__global__ __launch_bounds__(256 * QW + kStage, sizeof(T) == 2 && DENSE && NS <= 2 && QW == 2 ? 6 : QW + 1) void scan_fwd(const ScanP p)
+__global__ __launch_bounds__(256 * QW + kStage, DENSE && QW == 1 ? 4 : QW + 1) void scan_fwd(const ScanP p)
 {
     constexpr int W = 4 * QW * NS, CK = ScanShape{NS, QW}.save_steps();
     __shared__ FwdLds<NS, QW, PRE> sh;
@@ -171,11 +170,11 @@ __global__ __launch_bounds__(256 * QW + kStage, sizeof(T) == 2 && DENSE && NS <=
                         constexpr int i = decltype(state)::value;
                         h[i] = __builtin_fmaf(a[j][i], h[i], cur.v[j].y * cur.b.template at<j, i>());
                         hs[j][i] = h[i];
-                        if constexpr (!PRE && NS != 2) y4[j] = __builtin_fmaf(cur.c.template at<j, i>(), h[i], y4[j]);
+                        if constexpr (!PRE && NS != 2 && NS != 4) y4[j] = __builtin_fmaf(cur.c.template at<j, i>(), h[i], y4[j]);
                     });
                     if (PRE) sum_d += cur.v[j].x;
                 });
-                if constexpr (!PRE && NS == 2) dot4x2(cur.c.v[0], hs, y4);
+                if constexpr (!PRE && (NS == 2 || NS == 4)) dot4(cur.c.v[0], hs, y4);
                 if constexpr (!PRE) sh.y[buf][half][k + row][c] = rows4(y4);
             });
         }

@@ -6,7 +6,7 @@
 // and dz = gy (sum_s C h + D x) silu'(z), ddt = dd softplus'.
 //
 // States come from the saved ones: CK steps are run forward again from a saved
-// state, a and h[t-1] stay in registers (2 CK NS = 64 values per lane), then
+// state, a and h[t-1] stay in registers (2 CK NS = 128 values per lane, 64 above 16 states), then
 // the same steps are run in reverse.  Running the recurrence backwards instead
 // (h[t-1] = (h[t] - d x B) / a) would divide by factors near zero.
 //
@@ -61,7 +61,7 @@ __device__ __forceinline__ float halve_quad(float a, float b, bool second, bool 
 
 // Steps of a tile: LDS holds two of them, and its 128 threads of B take whole
 // states.
-constexpr int bwd_tile(int W) { return W <= 4 ? 32 : W <= 32 ? 16 : 8; }
+constexpr int bwd_tile(int W) { return W <= 16 ? 32 : W <= 32 ? 16 : 8; }
 
 template <int NS, int QW, bool PRE> struct BwdLds {
     static constexpr int W = 4 * QW * NS, TB = bwd_tile(W);
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
                     each<4>([&](auto step) {
                         constexpr int j = 3 - decltype(step)::value, k = k0 + j;
                         float ra = 0.f, rb = 0.f, ch = 0.f;
-                        if constexpr (NS == 2) back2<j>(g.c.v[0], g.b.v[0], s[j], h[k + 1], r, ch, rb);
+                        if constexpr (NS == 2 || NS == 4) back<j>(g.c.v[0], g.b.v[0], s[j], h[k + 1], r, ch, rb);
                         else
                             each<NS>([&](auto state) {
                                 constexpr int i = decltype(state)::value;

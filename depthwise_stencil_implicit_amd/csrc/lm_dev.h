@@ -83,7 +83,8 @@ template <typename T, int V> __device__ __forceinline__ void load_f32(const T *p
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = r.f(i);
 }
-template <typename T, int V> __device__ __forceinline__ void store_f32(T *p, const float (&v)[V])
+// ONCE: 16 bytes that the kernel does not read again, past the L2's lines in use.
+template <typename T, int V, bool ONCE = false> __device__ __forceinline__ void store_f32(T *p, const float (&v)[V])
 {
     if constexpr (V == 1) *p = from_f32<T>(v[0]);
     else {
@@ -95,7 +96,10 @@ template <typename T, int V> __device__ __forceinline__ void store_f32(T *p, con
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) r.w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
         }
-        __builtin_memcpy(reinterpret_cast<Pack<T, V> *>(p), r.w, sizeof(r));
+        if constexpr (ONCE && sizeof(r) == 16) {
+            typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
+            __builtin_nontemporal_store(any4{r.w[0], r.w[1], r.w[2], r.w[3]}, reinterpret_cast<any4 *>(p));
+        } else __builtin_memcpy(reinterpret_cast<Pack<T, V> *>(p), r.w, sizeof(r));
     }
 }
 

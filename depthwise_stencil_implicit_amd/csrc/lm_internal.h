@@ -13,20 +13,20 @@ namespace miconv {
 constexpr int LM_MAX_TAPS = 8;
 constexpr int LM_MAX_STATES = 64;
 
-// Scan: channels of one workgroup; how S states lie over lanes.  Eight rows of
-// 16 lanes share a channel (four up to four states), each holds ns of them.
+// Scan: channels of one workgroup; how S states lie over lanes.  Four rows of
+// 16 lanes share a channel, eight above 16 states; each holds ns of them.
 constexpr int LM_SCAN_CH = 64;
 struct ScanShape {
     int ns, qw;                                       // states per lane, core waves per 16 channels
-    constexpr int width() const { return 4 * qw * ns; }         // states with padding
-    constexpr int save_steps() const { return ns <= 2 ? 16 : 32 / ns; }   // steps between saved states
+    constexpr int width() const { return 4 * qw * ns; }                       // states with padding
+    constexpr int save_steps() const { return qw == 1 ? 16 : 32 / ns; }       // steps between saved states
 };
 inline ScanShape scan_shape(int64_t S)
 {
-    if (S <= 4) return {1, 1};
+    const int qw = S <= 16 ? 1 : 2;
     int ns = 1;
-    while (8 * ns < S) ns *= 2;
-    return {ns, 2};
+    while (4 * qw * ns < S) ns *= 2;
+    return {ns, qw};
 }
 inline int64_t lm_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -1,6 +1,7 @@
 // lm_plan: checks of the sequence operators' descriptors and arguments, and
 // how their long axis is split.  lm_run: checks of the pointers, dispatch.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -125,27 +126,29 @@ void conv_chunks(lm_plan_t &p, int64_t max_len, int64_t per_thread, int64_t min_
 }
 
 // The scan along one sequence is serial; a workgroup per 64 channels fills the
-// SIMDs of one compute unit.  Splitting the long axis fills more of them, at
-// the price of a first pass over the chunks for the states between them (0.6
+// SIMDs of one compute unit by itself, two together (up to 16 states, forward)
+// take about 1.5 times as long.  Splitting the long axis fills more units, at
+// the price of a first pass over the chunks for the states between them (0.7
 // of the main pass).  Of the chunk counts up to 64 the one with the least
-// estimated time is taken: rounds of 256 workgroups times the chunk's length,
-// plus 48 steps that a workgroup's start costs.
+// estimated time is taken; a workgroup's start costs about 48 steps.
 void scan_chunks(lm_plan_t &p, int64_t max_len)
 {
     constexpr int64_t tile = 32;
     const int64_t blocks = p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH);
     const bool packed = p.t[LM_OFFSETS].rank > 0;
+    const double pair = p.op == LM_SCAN && p.S <= 16 ? 1.5 : 2.0;
     int64_t rows = p.args.chunk;
     if (rows <= 0) {
-        rows = std::max<int64_t>(max_len, 1);
+        const int64_t len = std::max<int64_t>(max_len, 1);
         double best = 0;
         for (int64_t n = 1; n <= 64; ++n) {
-            const int64_t chunk = lm_cdiv(lm_cdiv(std::max<int64_t>(max_len, 1), n), tile) * tile;
+            const int64_t chunk = lm_cdiv(lm_cdiv(len, n), tile) * tile;
             if (n > 1 && chunk < 2 * tile) break;
-            // Packed sequences are of unlike lengths: whole chunks of all rows and a half each.
-            const double groups = (packed ? (double)p.L / chunk + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(max_len, chunk)) * blocks;
-            const double rounds = packed ? std::max(1.0, groups / 256) : (double)lm_cdiv((int64_t)groups, 256);
-            const double cost = rounds * (chunk + 48) * (n > 1 ? 1.6 : 1.0) + (n > 1 ? 48 : 0);
+            // Packed sequences are of unlike lengths: whole chunks of all rows and half a one each.
+            const double groups = (packed ? (double)p.L / chunk + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(len, chunk)) * blocks;
+            const double per_cu = std::max(1.0, packed ? groups / 256 : (double)lm_cdiv((int64_t)groups, 256));
+            const double time = per_cu < 2 ? per_cu : pair * std::floor(per_cu / 2) + std::fmod(per_cu, 2.0);
+            const double cost = time * (chunk + 48) * (n > 1 ? 1.7 : 1.0) + (n > 1 ? 48 : 0);
             if (n == 1 || cost < best) best = cost, rows = chunk;
         }
     }
@@ -297,7 +300,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
 
     const int64_t rows = packed ? p.L : N * p.L, cells = rows * p.C;
     if (conv) {
-        if (!step) conv_chunks(p, max_len, bwd ? 4 : 16 / e, bwd ? 32 : 8);
+        if (!step) conv_chunks(p, max_len, bwd ? 2 : 16 / e, bwd ? 32 : 8);
         else p.chunk = p.chunks = 1;
         if (bwd && (k.has(LM_DW) || k.has(LM_DBIAS))) p.workspace_bytes = p.seqs * p.chunks * p.C * (p.K + 1) * 4;
         const int64_t st = p.seqs * p.C * (p.K - 1) * e * ((k.has(LM_STATE_IN) || step) + k.has(LM_STATE_OUT) + k.has(LM_GSTATE) + k.has(LM_DSTATE));

@@ -2,10 +2,10 @@
 //
 // A workgroup owns 64 channels of one group and walks along the sequence in
 // tiles.  Its core waves run the recurrence: a row of 16 lanes holds NS states
-// of 16 channels, a wave four such rows, and QW = 2 waves share the channels
-// (S <= 4 QW NS = W; states past S have A = B = C = 0).  One wave alone issues a
-// vector instruction every 5 clocks or so, two every 3, hence the eight rows
-// where four would need a tenth fewer instructions.
+// of 16 channels, a wave four such rows, and QW waves share the channels (S <=
+// 4 QW NS = W; states past S have A = B = C = 0).  Up to 16 states one wave does;
+// two waves with half the states each issue a tenth more instructions and took
+// a tenth longer (97 for 87 us).
 //
 // B and C are the same for all channels, so a row loads 16 different values of
 // its states with one LDS read and takes each by a row broadcast in the
@@ -206,7 +206,7 @@ template <int NS, int W> struct States4 {
 // folds a row broadcast into a multiplication but not into a multiply-add.
 // The s_nop gives c the two wait states that a cross-lane read needs, should
 // it have been moved by the vector unit just before.
-__device__ __forceinline__ void dot4x2(float c, const float (&h)[4][2], float (&y)[4])
+__device__ __forceinline__ void dot4(float c, const float (&h)[4][2], float (&y)[4])
 {
     asm("s_nop 1\n\t"
         "v_mul_f32_dpp %0, %4, %5 row_newbcast:0 row_mask:0xf bank_mask:0xf\n\t"
@@ -222,10 +222,36 @@ __device__ __forceinline__ void dot4x2(float c, const float (&h)[4][2], float (&
           "v"(h[3][1]));
 }
 
+// The same for four states.
+__device__ __forceinline__ void dot4(float c, const float (&h)[4][4], float (&y)[4])
+{
+    asm("s_nop 1\n\t"
+        "v_mul_f32_dpp %0, %4, %5 row_newbcast:0 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %1, %4, %9 row_newbcast:4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %2, %4, %13 row_newbcast:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %3, %4, %17 row_newbcast:12 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %4, %6 row_newbcast:1 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %10 row_newbcast:5 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %14 row_newbcast:9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %18 row_newbcast:13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %4, %7 row_newbcast:2 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %11 row_newbcast:6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %15 row_newbcast:10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %19 row_newbcast:14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %4, %8 row_newbcast:3 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %12 row_newbcast:7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %16 row_newbcast:11 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %20 row_newbcast:15 row_mask:0xf bank_mask:0xf"
+        : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+        : "v"(c), "v"(h[0][0]), "v"(h[0][1]), "v"(h[0][2]), "v"(h[0][3]), 
+          "v"(h[1][0]), "v"(h[1][1]), "v"(h[1][2]), "v"(h[1][3]), "v"(h[2][0]), "v"(h[2][1]), "v"(h[2][2]), "v"(h[2][3]), 
+          "v"(h[3][0]), "v"(h[3][1]), "v"(h[3][2]), "v"(h[3][3]));
+}
+
 // One step of the backward recurrence for two states: r[i] += C[J][i] s,
 // ch = sum_i C[J][i] h[i], rb = sum_i B[J][i] r[i] (the new r).
 template <int J>
-__device__ __forceinline__ void back2(float c, float b, float s, const float (&h)[2], float (&r)[2], float &ch, float &rb)
+__device__ __forceinline__ void back(float c, float b, float s, const float (&h)[2], float (&r)[2], float &ch, float &rb)
 {
     asm("s_nop 1\n\t"
         "v_fmac_f32_dpp %0, %4, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
@@ -236,6 +262,28 @@ __device__ __forceinline__ void back2(float c, float b, float s, const float (&h
         "v_fmac_f32_dpp %3, %5, %1 row_newbcast:%10 row_mask:0xf bank_mask:0xf"
         : "+&v"(r[0]), "+&v"(r[1]), "=&v"(ch), "=&v"(rb)
         : "v"(c), "v"(b), "v"(s), "v"(h[0]), "v"(h[1]), "n"(2 * J), "n"(2 * J + 1));
+}
+
+// The same for four states.
+template <int J>
+__device__ __forceinline__ void back(float c, float b, float s, const float (&h)[4], float (&r)[4], float &ch, float &rb)
+{
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %6, %8 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %6, %8 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %6, %8 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %6, %8 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %4, %6, %9 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32_dpp %5, %7, %0 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %6, %10 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %5, %7, %1 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %6, %11 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %5, %7, %2 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %6, %12 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %5, %7, %3 row_newbcast:%16 row_mask:0xf bank_mask:0xf"
+        : "+&v"(r[0]), "+&v"(r[1]), "+&v"(r[2]), "+&v"(r[3]), "=&v"(ch), "=&v"(rb)
+        : "v"(c), "v"(b), "v"(s), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]), "n"(4 * J), "n"(4 * J + 1),
+          "n"(4 * J + 2), "n"(4 * J + 3));
 }
 
 // What a lane reads from LDS for four steps: d and d x of its channel, B and
@@ -337,11 +385,14 @@ template <typename F> void with_type(int32_t dtype, F f)
 template <typename F> void with_ns(int64_t S, F f)
 {
     const ScanShape s = scan_shape(S);
-    if (s.qw == 1) f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    else if (s.ns == 1) f(std::integral_constant<int, 1>(), std::integral_constant<int, 2>());
-    else if (s.ns == 2) f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
-    else if (s.ns == 4) f(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
-    else f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    if (s.qw == 2 && s.ns == 8) f(std::integral_constant<int, 8>(), two);
+    else if (s.qw == 2) f(four, two);
+    else if (s.ns == 4) f(four, one);
+    else if (s.ns == 2) f(two, one);
+    else f(one, one);
 }
 
 }  // namespace miconv

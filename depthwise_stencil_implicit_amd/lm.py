@@ -290,10 +290,10 @@ _abi_scan = A.LM_SCAN
 def _new_saved(x, A_, offsets) -> torch.Tensor:
     """Room for the states before every 16th step (fewer steps above 16 states)."""
     s = A_.shape[-1]
-    ns, rows = 1, 4 if s <= 4 else 8
+    ns, rows = 1, 4 if s <= 16 else 8
     while rows * ns < s:
         ns *= 2
-    ck = 16 if ns <= 2 else max(1, 32 // ns)
+    ck = 16 if rows == 4 else max(1, 32 // ns)
     count = x.shape[0] * -(-x.shape[2] // ck) if offsets is None else x.shape[2] // ck + offsets.shape[0]
     return torch.empty(count * x.shape[1] * rows * ns, device=x.device)
 
