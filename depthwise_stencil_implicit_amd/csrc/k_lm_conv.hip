@@ -9,6 +9,11 @@
 // rows in front of each chunk.  Lanes lie along the channels: with channels
 // contiguous a wave reads and writes whole lines (V elements per lane, at any
 // element alignment); other strides take V = 1.
+//
+// Measured, bf16, K = 4: 4 x 2048 x 4096 in 28 us (4.9 TB/s; a large copy
+// reaches 5.1); output and gradients of 8 x 2048 x 2048 in 88 us, of which the
+// backward walk takes 55 (2 channels per thread and 64-row chunks; 4 channels
+// and 32 rows read a seventh more and took 64).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

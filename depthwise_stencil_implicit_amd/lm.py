@@ -28,7 +28,6 @@ import torch
 from . import _abi as A
 from .api import ConvError, _TORCH_DT
 
-_SLOT = {name: i for i, name in enumerate(A.LM_SLOTS)}
 (_X, _W, _BIAS, _Y, _S0, _S1, _OFF, _GY, _GS, _DX, _DW, _DBIAS, _DS, _DT, _A, _B, _C, _D, _Z, _DTB, _DDT, _DA, _DB, _DC,
  _DD, _DZ, _DDTB, _SAVED, _ROWS, _SCALES, _ZEROS) = range(A.LM_NSLOT)
 _TYPES = {**_TORCH_DT, torch.int32: A.LM_I32, torch.uint8: A.LM_U8}
@@ -94,50 +93,59 @@ def _make_plan(op, tensors, flags=0, max_len=0, chunk=0) -> A.LmPlan:
 _plans: dict = {}
 
 
-def _plan_for(op, inputs, outputs, flags=0, max_len=0, chunk=0, extra=None) -> A.LmPlan:
-    """The plan of a call.  ``outputs`` are allocated from the inputs'
-    descriptors and so need no place in the key; ``extra`` says which exist."""
-    key = (op, flags, max_len, chunk, extra,
-           tuple([(k, t.shape, t.stride(), t.dtype) for k, t in inputs.items() if t is not None]))
+def _call(op, ins, outs, flags=0, max_len=None, chunk=None, extra=None) -> None:
+    """Plan (or its cached copy) and launch of a call on ``ins`` and ``outs``,
+    lists of (place, tensor or None).  Outputs are allocated from the inputs'
+    descriptors and so have no place in the key; ``extra`` says which exist."""
+    key = [op, flags, max_len, chunk, extra]
+    dev = -1
+    for slot, t in ins:
+        if t is None:
+            key.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
+            if dev >= 0:
+                raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+            dev = d
+        key += (t.shape, t.stride(), t.dtype)
+    key = tuple(key)
     p = _plans.get(key)
     if p is None:
-        p = _make_plan(op, {**inputs, **outputs}, flags, max_len, chunk)
+        p = _make_plan(op, dict(ins + outs), flags, max_len or 0, chunk or 0)
         if len(_plans) >= 512:
             _plans.clear()
         _plans[key] = p
-    return p
-
-
-def _check_device(inputs) -> torch.device:
-    dev = None
-    for slot, t in inputs.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    return dev
-
-
-def _launch(p: A.LmPlan, tensors, dev: torch.device, stream: Optional[int] = None) -> None:
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch(p, tensors, dev, stream)
     q = _Ptrs()
-    for slot, t in tensors.items():
+    for slot, t in ins:
         if t is not None:
             q[slot] = t.data_ptr()
-    ws, n = None, p.workspace_bytes
-    if n:
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    for slot, t in outs:
+        if t is not None:
+            q[slot] = t.data_ptr()
+    _run(p, q, dev)
+
+
+def _run(p: A.LmPlan, q, dev: int, stream: Optional[int] = None) -> None:
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(p, q, dev, stream)
+    n = p.workspace_bytes
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
     st = A.lib().lm_run(ctypes.byref(p), q, ws.data_ptr() if n else None, n, stream)
     if st != A.OK:
         raise ConvError(st)
+
+
+def _on_gpu(*tensors) -> None:
+    """Before outputs are allocated: a clear refusal of CPU tensors."""
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
 
 
 def _rows_like(n, c, l, ref, dtype=None):
@@ -172,13 +180,11 @@ def causal_conv(x, w, b=None, *, activation=None, state=None, offsets=None, max_
     sequence (zeros without it); ``return_state`` gives those in front of what
     follows it.  ``chunk`` forces the rows one thread walks."""
     w = _taps(w)
-    ins = {_X: x, _W: w, _BIAS: b, _S0: state, _OFF: offsets}
-    dev = _check_device(ins)
+    _on_gpu(x)
     y = torch.empty_like(x)
-    last = _rows_like(_seqs(x, offsets), x.shape[1], w.shape[1] - 1, x) if return_state and w.dim() == 2 else None
-    outs = {_Y: y, _S1: last}
-    p = _plan_for(A.LM_CONV, ins, outs, _act(activation), max_len or 0, chunk or 0, return_state)
-    _launch(p, {**ins, **outs}, dev)
+    last = _rows_like(_seqs(x, offsets), x.shape[1], w.shape[-1] - 1, x) if return_state else None
+    _call(A.LM_CONV, [(_X, x), (_W, w), (_BIAS, b), (_S0, state), (_OFF, offsets)], [(_Y, y), (_S1, last)], _act(activation),
+          max_len, chunk, return_state)
     return ConvOut(y, last)
 
 
@@ -188,15 +194,13 @@ def causal_conv_backward(gy, x, w, b=None, *, activation=None, state=None, offse
     that of the returned state.  db comes with a bias, dstate with a state;
     ``need_dw`` covers dw and db."""
     shape, w = w.shape, _taps(w)
-    ins = {_GY: gy, _X: x, _W: w, _BIAS: b, _S0: state, _OFF: offsets, _GS: gstate}
-    dev = _check_device(ins)
+    _on_gpu(x)
     dx = torch.empty_like(x) if need_dx else None
-    dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
-    db = torch.empty(b.shape, dtype=b.dtype, device=dev) if need_dw and b is not None else None
+    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if need_dw else None
+    db = torch.empty(b.shape, dtype=b.dtype, device=b.device) if need_dw and b is not None else None
     ds = torch.empty_like(state) if state is not None else None
-    outs = {_DX: dx, _DW: dw, _DBIAS: db, _DS: ds}
-    p = _plan_for(A.LM_CONV_BWD, ins, outs, _act(activation), max_len or 0, chunk or 0, (need_dx, need_dw))
-    _launch(p, {**ins, **outs}, dev)
+    _call(A.LM_CONV_BWD, [(_GY, gy), (_X, x), (_W, w), (_BIAS, b), (_S0, state), (_OFF, offsets), (_GS, gstate)],
+          [(_DX, dx), (_DW, dw), (_DBIAS, db), (_DS, ds)], _act(activation), max_len, chunk, (need_dx, need_dw))
     return ConvGrads(dx, dw.view(shape) if dw is not None else None, db, ds)
 
 
@@ -204,27 +208,18 @@ class _Step:
     """A plan whose output is a new contiguous tensor of the plan's shape."""
 
     def __init__(self, op, tensors, shape, ref, flags=0):
-        self.device = _check_device(tensors)
+        _on_gpu(*[t for t in tensors.values() if t is not None])
+        self.device = ref.device
+        if any(t is not None and t.device != ref.device for t in tensors.values()):
+            raise ValueError("tensors on several devices")
         self.shape, self.dtype = shape, ref.dtype
         self.plan = _make_plan(op, {**tensors, _Y: self.empty_output()}, flags)
-        self._plan_ref = ctypes.byref(self.plan)
-        self.workspace_bytes = int(self.plan.workspace_bytes)
-        self._run = A.lib().lm_run
 
     def empty_output(self) -> torch.Tensor:
         return torch.empty(self.shape, dtype=self.dtype, device=self.device)
 
     def _launch(self, q, stream):
-        dev = self.device.index
-        if dev != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return self._launch(q, stream)
-        n = self.workspace_bytes
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
-        st = self._run(self._plan_ref, q, ws.data_ptr() if n else None, n,
-                       torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
-        if st != A.OK:
-            raise ConvError(st)
+        _run(self.plan, q, self.device.index, stream)
 
 
 class PreparedCausalConvStep(_Step):
@@ -272,19 +267,15 @@ def selective_scan(x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus
     state f32 [sequences, C, S].  ``save`` returns what ``selective_scan_backward``
     takes as ``saved``.  ``chunk`` forces how many steps run in one piece."""
     B, C = _grouped(B, 4), _grouped(C, 4)
-    ins = {_X: x, _DT: dt, _A: A_, _B: B, _C: C, _D: D, _Z: z, _DTB: dt_bias, _S0: state, _OFF: offsets}
-    dev = _check_device(ins)
-    n = _seqs(x, offsets)
-    outs = {_Y: torch.empty_like(x) if want_y else None,
-            _S1: torch.empty((n, x.shape[1], A_.shape[-1]), device=dev) if return_state else None,
-            _SAVED: _new_saved(x, A_, offsets) if save else None}
-    p = _plan_for(_abi_scan, ins, outs, A.LM_SOFTPLUS if dt_softplus else 0, max_len or 0, chunk or 0,
-                  (want_y, return_state, save))
-    _launch(p, {**ins, **outs}, dev)
-    return ScanOut(outs[_Y], outs[_S1], outs[_SAVED])
-
-
-_abi_scan = A.LM_SCAN
+    _on_gpu(x)
+    y = torch.empty_like(x) if want_y else None
+    last = torch.empty((_seqs(x, offsets), x.shape[1], A_.shape[-1]), device=x.device) if return_state else None
+    saved = _new_saved(x, A_, offsets) if save else None
+    _call(A.LM_SCAN,
+          [(_X, x), (_DT, dt), (_A, A_), (_B, B), (_C, C), (_D, D), (_Z, z), (_DTB, dt_bias), (_S0, state), (_OFF, offsets)],
+          [(_Y, y), (_S1, last), (_SAVED, saved)], A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk,
+          (want_y, return_state, save))
+    return ScanOut(y, last, saved)
 
 
 def _new_saved(x, A_, offsets) -> torch.Tensor:
@@ -304,21 +295,20 @@ def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None
     ``gstate``, that of the returned state.  ``saved`` comes from the forward
     call (``save=True``) on the same tensors; without it the states are computed
     again.  dD, dz, ddt_bias and dstate come with D, z, dt_bias and state."""
+    _on_gpu(x)
     if saved is None:
         saved = selective_scan(x, dt, A_, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, state=state,
                                offsets=offsets, max_len=max_len, save=True, want_y=False, chunk=chunk).saved
     b_shape, c_shape, B, C = B.shape, C.shape, _grouped(B, 4), _grouped(C, 4)
-    ins = {_GY: gy, _X: x, _DT: dt, _A: A_, _B: B, _C: C, _D: D, _Z: z, _DTB: dt_bias, _OFF: offsets, _GS: gstate,
-           _SAVED: saved}
-    dev = _check_device(ins)
-    new = lambda t: torch.empty_like(t) if t is not None else None  # noqa: E731
-    outs = {_DX: new(x), _DDT: new(dt), _DA: new(A_), _DB: new(B), _DC: new(C), _DD: new(D), _DZ: new(z), _DDTB: new(dt_bias),
-            _DS: new(state)}
-    p = _plan_for(A.LM_SCAN_BWD, ins, outs, A.LM_SOFTPLUS if dt_softplus else 0, max_len or 0, chunk or 0,
-                  (state.shape, state.stride()) if state is not None else None)
-    _launch(p, {**ins, **outs}, dev)
-    return ScanGrads(outs[_DX], outs[_DDT], outs[_DA], outs[_DB].view(b_shape), outs[_DC].view(c_shape), outs[_DD], outs[_DZ],
-                     outs[_DDTB], outs[_DS])
+    new = lambda v: torch.empty_like(v) if v is not None else None  # noqa: E731
+    dx, ddt, dA, dB, dC = (torch.empty_like(v) for v in (x, dt, A_, B, C))
+    dD, dz, db, ds = new(D), new(z), new(dt_bias), new(state)
+    _call(A.LM_SCAN_BWD,
+          [(_GY, gy), (_X, x), (_DT, dt), (_A, A_), (_B, B), (_C, C), (_D, D), (_Z, z), (_DTB, dt_bias), (_OFF, offsets),
+           (_GS, gstate), (_SAVED, saved)],
+          [(_DX, dx), (_DDT, ddt), (_DA, dA), (_DB, dB), (_DC, dC), (_DD, dD), (_DZ, dz), (_DDTB, db), (_DS, ds)],
+          A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk, (state.shape, state.stride()) if state is not None else None)
+    return ScanGrads(dx, ddt, dA, dB.view(b_shape), dC.view(c_shape), dD, dz, db, ds)
 
 
 class PreparedSelectiveScanStep(_Step):
