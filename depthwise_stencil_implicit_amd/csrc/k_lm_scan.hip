@@ -134,13 +134,7 @@ __global__ __launch_bounds__(256 * QW + kStage, DENSE && QW == 1 ? 4 : QW + 1) v
         A2[i] = real && q * NS + i < p.S ? kLog2e * p.A[cc * p.A_c + (q * NS + i) * p.A_s] : 0.f, h[i] = 0.f;
     if (!PRE && real) {
         if (p.s0) get_states<NS>(p.s0, p.s0s, at.seq, cc, q * NS, p.S, h);
-        for (int64_t j = 0; j < at.ch; ++j) {
-            const int64_t k = (at.seq * (p.chunks - 1) + j) * p.C + cc;
-            const float d = p.carry_d[k];
-#pragma unroll
-            for (int i = 0; i < NS; ++i)
-                h[i] = __builtin_fmaf(hw_exp2(d * A2[i]), h[i], p.carry_h[k * W + q * NS + i]);
-        }
+        fold_chunks<NS, W>(p, at.seq * (p.chunks - 1), 1, at.ch, cc, q * NS, A2, h);
     }
     float *saved = !PRE && p.saved && real
                        ? p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * W + q * NS : nullptr;

@@ -232,13 +232,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
         if (p.gs) get_states<NS>(p.gs, p.gss, at.seq, cc, q * NS, p.S, r);
         int64_t last = (at.sp.len - 1) / p.chunk;
         if (last > p.chunks - 1) last = p.chunks - 1;
-        for (int64_t j = last; j > at.ch; --j) {
-            const int64_t k = (at.seq * p.chunks + j) * p.C + cc;
-            const float d = p.carry_d[k];
-#pragma unroll
-            for (int i = 0; i < NS; ++i)
-                r[i] = __builtin_fmaf(hw_exp2(d * A2[i]), r[i], p.carry_h[k * W + q * NS + i]);
-        }
+        if (last > at.ch) fold_chunks<NS, W>(p, at.seq * p.chunks + last, -1, last - at.ch, cc, q * NS, A2, r);
     }
     const float *saved = p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * W + q * NS;
     float sum_d = 0.f;

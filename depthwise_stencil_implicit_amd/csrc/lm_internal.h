@@ -47,9 +47,7 @@ inline int mv4_parts(const lm_plan_t &p)
     for (int s : {LM_W, LM_SCALES, LM_ZEROS})   // offsets of 32 bits
         if (p.t[s].rank && p.t[s].strides[0] > 0x7fffffff / (p.C + 1)) return 0;
     if (p.C > 0x7fffff00 || p.K % 128 || blocks >= 1024 || (group % 128 && group != 64 && group != 32)) return 0;
-    const int64_t least = lm_cdiv(blocks, p.dtype == CONV_F32 ? 16 : 64), tiles = lm_cdiv(p.C, 16) * lm_cdiv(p.seqs, 16);
-    const int64_t fill = 512 / (tiles > 0 ? tiles : 1), most = lm_cdiv(blocks, 16);
-    return (int)(least > (fill < most ? fill : most) ? least : (fill < most ? fill : most));
+    return (int)lm_cdiv(blocks, p.dtype == CONV_F32 ? 16 : 64);
 }
 
 typedef void *const *lm_ptrs;

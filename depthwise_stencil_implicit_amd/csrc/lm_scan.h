@@ -320,6 +320,30 @@ __device__ __forceinline__ void put_states(float *p, const S3 &st, int64_t row, 
         if (s0 + i < S) q[i * st.l] = h[i];
 }
 
+// What enters a chunk: v <- exp(A d[k]) v + left[k] over `count` chunks from
+// `first` on, `by` chunks apart, d and left as the pass before stored them.
+// Eight chunks' loads are in flight together.
+template <int NS, int W>
+__device__ __forceinline__ void fold_chunks(const ScanP &p, int64_t first, int64_t by, int64_t count, int64_t c, int s0,
+                                            const float (&A2)[NS], float (&v)[NS])
+{
+    for (int64_t j0 = 0; j0 < count; j0 += 8) {
+        float d[8], left[8][NS];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t k = (first + (j0 + j < count ? j0 + j : count - 1) * by) * p.C + c;
+            d[j] = p.carry_d[k];
+            load_f32<float, NS>(p.carry_h + k * W + s0, left[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j0 + j >= count) break;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) v[i] = __builtin_fmaf(hw_exp2(d[j] * A2[i]), v[i], left[j][i]);
+        }
+    }
+}
+
 // Sums of lane pairs 16 (32) apart: lanes of even rows (of the lower half)
 // receive that of a, the others that of b.
 __device__ __forceinline__ float halve16(float a, float b)
