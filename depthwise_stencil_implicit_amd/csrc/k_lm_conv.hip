@@ -45,11 +45,10 @@ template <int V> __device__ __forceinline__ bool conv_item(const ConvP &p, int64
 {
     const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (item >= p.cvs * p.chunks * p.seqs) return false;
-    const int64_t r = item / p.cvs;
-    c = (item - r * p.cvs) * V;
+    const int64_t r = divide(item, p.cvs, c);
+    c *= V;
     if (c > p.C - V) c = p.C - V;
-    seq = r / p.chunks;
-    ch = r - seq * p.chunks;
+    seq = divide(r, p.chunks, ch);
     return true;
 }
 
@@ -361,8 +360,8 @@ __global__ __launch_bounds__(1024) void conv_bwd_sums(const float *part, int64_t
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) v += sh[i][threadIdx.x];
-        const int64_t c = out / (K + 1);
-        const int k = (int)(out - c * (K + 1));
+        int64_t k;
+        const int64_t c = divide(out, K + 1, k);
         if (k < K) {
             if (dw) dw[c * dws_c + k * dws_k] = from_f32<T>(v);
         } else if (db) db[c * dbs] = from_f32<T>(v);

@@ -210,7 +210,8 @@ template <typename T, int NS> __global__ __launch_bounds__(256) void scan_step(c
     const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 2;
     const int q = threadIdx.x & 3;
     if (item >= p.seqs * p.C) return;   // the four lanes of an item leave together
-    const int64_t n = item / p.C, c = item - n * p.C;
+    int64_t c, in_g;
+    const int64_t n = divide(item, p.C, c);
     T *y = static_cast<T *>(p.y) + n * p.ys.n + c * p.ys.c;
     int64_t row = n;
     if (p.rows) {
@@ -221,7 +222,7 @@ template <typename T, int NS> __global__ __launch_bounds__(256) void scan_step(c
         }
     }
     float h[NS], A[NS], b[NS], cv[NS];
-    const int64_t g = c / p.Cg;
+    const int64_t g = divide(c, p.Cg, in_g);
     const T *pb = static_cast<const T *>(p.Bm) + n * p.Bs.n + g * p.Bs.g + q * NS * p.Bs.s;
     const T *pc = static_cast<const T *>(p.Cm) + n * p.Cs.n + g * p.Cs.g + q * NS * p.Cs.s;
     float *ph = p.s1 + row * p.s1s.n + c * p.s1s.c + q * NS * p.s1s.l;

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
         A2[i] = real && q * NS + i < p.S ? kLog2e * p.A[cc * p.A_c + (q * NS + i) * p.A_s] : 0.f;
     if (!PRE && real) {
         if (p.gs) get_states<NS>(p.gs, p.gss, at.seq, cc, q * NS, p.S, r);
-        int64_t last = (at.sp.len - 1) / p.chunk;
+        int64_t rest, last = at.sp.len > 0 ? divide(at.sp.len - 1, p.chunk, rest) : 0;
         if (last > p.chunks - 1) last = p.chunks - 1;
         if (last > at.ch) fold_chunks<NS, W>(p, at.seq * p.chunks + last, -1, last - at.ch, cc, q * NS, A2, r);
     }
@@ -382,8 +382,9 @@ __global__ __launch_bounds__(256) void scan_bwd_bc(const float *part, int64_t ro
 {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e >= rows * 2 * W * G) return;
-    const int64_t per = rows * 2 * W, g = e / per, in = e - g * per, row = in / (2 * W);
-    const int j = (int)(in - row * 2 * W), s = j % W;
+    const int64_t per = rows * 2 * W;
+    int64_t in, j, l;
+    const int64_t g = divide(e, per, in), row = divide(in, 2 * W, j), s = j < W ? j : j - W;
     if (s >= S) return;
     const float *q = part + g * blocks_g * per + in;
     float a[4] = {};
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(256) void scan_bwd_bc(const float *part, int64_t ro
         for (int k = 0; k < 4; ++k) a[k] += q[(i + k) * per];
     for (; i < blocks_g; ++i) a[0] += q[i * per];
     const T v = from_f32<T>((a[0] + a[1]) + (a[2] + a[3]));
-    const int64_t n = row / L, l = row - n * L;
+    const int64_t n = divide(row, L, l);
     if (j < W) dB[n * bs.n + g * bs.g + s * bs.s + l * bs.l] = v;
     else dC[n * cs.n + g * cs.g + s * cs.s + l * cs.l] = v;
 }
@@ -411,8 +412,8 @@ __global__ __launch_bounds__(256) void scan_bwd_c(const ScanP p, int W, float *d
         for (int64_t ch = 0; ch < p.chunks && (ch == 0 || ch * p.chunk < sp.len); ++ch)
             v += p.part_c[(seq * p.chunks + ch) * n + e];
     }
-    const int64_t c = e / (W + 2);
-    const int j = (int)(e - c * (W + 2));
+    int64_t j;
+    const int64_t c = divide(e, W + 2, j);
     if (j < p.S) dA[c * a_c + j * a_s] = v;
     else if (j == W && dD) dD[c * d_s] = v;
     else if (j == W + 1 && db) db[c * b_s] = v;

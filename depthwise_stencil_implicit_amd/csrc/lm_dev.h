@@ -17,6 +17,20 @@ __device__ __forceinline__ SeqSpan seq_span(const int32_t *offsets, int64_t s, i
     return {0, a, b - a};
 }
 
+// Quotient and remainder; 64-bit division is a long sequence without a unit of
+// its own, and nearly all indexes fit 32.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t &rest)
+{
+    if (((a | b) >> 32) == 0) {
+        const uint32_t q = (uint32_t)a / (uint32_t)b;
+        rest = (uint32_t)a - q * (uint32_t)b;
+        return q;
+    }
+    const int64_t q = a / b;
+    rest = a - q * b;
+    return q;
+}
+
 // exp2, log2 and reciprocal of the hardware (1 ulp).  The compiler's exp2f
 // would add a rescaling for subnormal results, which here are factors that
 // vanish against the rest of a sum.

@@ -112,12 +112,12 @@ struct ScanAt {
 __device__ __forceinline__ ScanAt scan_at(const ScanP &p, int64_t chunks)
 {
     ScanAt a;
-    const int64_t b = blockIdx.x, r = b / p.blocks;
-    const int64_t cb = b - r * p.blocks;
-    a.seq = r / chunks;
-    a.ch = r - a.seq * chunks;
-    a.g = (int)(cb / p.blocks_g);
-    const int64_t in_g = (cb - a.g * p.blocks_g) * kCH;
+    // All of these are below 2^31.
+    const uint32_t b = blockIdx.x, r = b / (uint32_t)p.blocks, cb = b - r * (uint32_t)p.blocks;
+    const uint32_t seq = r / (uint32_t)chunks;
+    a.seq = seq, a.ch = r - seq * (uint32_t)chunks;
+    a.g = (int)(cb / (uint32_t)p.blocks_g);
+    const int64_t in_g = (int64_t)(cb - a.g * (uint32_t)p.blocks_g) * kCH;
     a.c0 = a.g * p.Cg + in_g;
     a.nc = (int)(p.Cg - in_g < kCH ? p.Cg - in_g : kCH);
     a.sp = seq_span(p.off, a.seq, p.L);
