@@ -39,7 +39,7 @@ struct MvP {
     const void *x, *scales, *zeros, *bias;
     const uint8_t *w;
     void *y;
-    int64_t M, N, K, group, groups;
+    int64_t M, N, K, group;
     uint32_t block_group;   // 2^20 group 128ths of a block, rounded up: block -> group
     int64_t xs_m, xs_k, w_n, sc_n, sc_g, z_n, z_g, bs, ys_m, ys_n;
 };
@@ -416,7 +416,7 @@ int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     a.x = q[LM_X], a.scales = q[LM_SCALES], a.zeros = q[LM_ZEROS], a.bias = q[LM_BIAS];
     a.w = static_cast<const uint8_t *>(q[LM_W]);
     a.y = q[LM_Y];
-    a.M = p.seqs, a.N = p.C, a.K = p.K, a.groups = p.G, a.group = p.K / p.G;
+    a.M = p.seqs, a.N = p.C, a.K = p.K, a.group = p.K / p.G;
     a.xs_m = p.t[LM_X].strides[0], a.xs_k = p.t[LM_X].strides[1], a.w_n = p.t[LM_W].strides[0];
     a.sc_n = p.t[LM_SCALES].strides[0], a.sc_g = p.t[LM_SCALES].strides[1];
     a.z_n = p.t[LM_ZEROS].strides[0], a.z_g = p.t[LM_ZEROS].strides[1];

@@ -15,7 +15,7 @@
  * [1, C, T] with an LM_OFFSETS tensor (int32 [sequences + 1], on the device,
  * ascending from 0 to T): sequence s is the rows offsets[s] .. offsets[s+1]-1,
  * of any length, zero included.  Offsets are clamped to 0..T by the kernels;
- * rows that no sequence covers are not written.
+ * outputs at rows that no sequence covers mean nothing.
  *
  * Formulas (f32 arithmetic and sums, one rounding to the output's type):
  *
@@ -34,7 +34,9 @@
  *   y[c] = (sum_s C[g,s] h[c,s] + D[c] x[c]) * silu(z[c])
  *   x, dt, z, y, B and C share one dtype; A [C, S], D, dt_bias [C] and the
  *   states [N, C, S] are f32; B and C are [N, G, S, L].  S is 1 .. 64.
- *   Gradients have the types of what they are gradients of.
+ *   Gradients have the types of what they are gradients of.  d = 0 (dt the
+ *   type's lowest value, with softplus) leaves a state as it is.  A state that
+ *   has overflowed to infinity may turn into NaN where the axis is split.
  *   LM_SAVED (f32, lm_plan_t.saved_floats elements): the states every few
  *   steps, written by LM_SCAN and read by LM_SCAN_BWD.
  *

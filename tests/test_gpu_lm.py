@@ -398,3 +398,72 @@ def test_another_stream():
         got = lm.selective_scan(*args, **kw, **extra, return_state=True)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got.y, want.y) and torch.equal(got.state, want.state)
+
+
+def test_parts_of_the_gradients():
+    """Selected gradients, a depthwise [C, 1, K] weight, one group without its
+    dim, a broadcast output gradient."""
+    g = gen(21)
+    x, w, b = to_layout(rnd(g, 2, 20, 33), "nlc"), rnd(g, 20, 4).cuda(), rnd(g, 20).cuda()
+    gy = rnd(g, 2, 20, 1).cuda().expand(2, 20, 33)
+    whole = lm.causal_conv_backward(gy, x, w[:, None], b, activation="silu")
+    assert whole.dw.shape == (20, 1, 4)
+    one = lm.causal_conv_backward(gy.contiguous(), x, w, b, activation="silu", need_dx=False)
+    two = lm.causal_conv_backward(gy, x, w, b, activation="silu", need_dw=False)
+    assert one.dx is None and two.dw is None and two.db is None
+    assert torch.equal(one.dw, whole.dw[:, 0]) and torch.equal(one.db, whole.db) and torch.equal(two.dx, whole.dx)
+    dt, A = to_layout(rnd(g, 2, 20, 33), "nlc"), -torch.exp(rnd(g, 20, 6)).cuda()
+    B, C = to_layout(rnd(g, 2, 1, 6, 33), "nlc"), to_layout(rnd(g, 2, 1, 6, 33), "nlc")
+    D = torch.ones(1, device="cuda").expand(20)
+    args = dict(D=D, dt_softplus=True)
+    a = lm.selective_scan_backward(gy, x, dt, A, B, C, **args)
+    c = lm.selective_scan_backward(gy, x, dt, A, B[:, 0], C[:, 0], **args)
+    assert c.dB.shape == (2, 6, 33) and torch.equal(c.dB, a.dB[:, 0]) and torch.equal(c.dx, a.dx)
+    assert a.dD.shape == (20,) and torch.equal(a.dD, c.dD)
+
+
+def test_decoding_in_a_graph():
+    """One token through convolution, scan and projection in a captured graph,
+    replayed with eager work and synchronisation between."""
+    g = gen(22)
+    n, c, s = 3, 64, 16
+    w, b, A = rnd(g, c, 4, dtype=BF).cuda(), rnd(g, c, dtype=BF).cuda(), -torch.exp(rnd(g, c, s)).cuda()
+    B, C = rnd(g, n, 1, s, dtype=BF).cuda(), rnd(g, n, 1, s, dtype=BF).cuda()
+    packed = torch.randint(0, 256, (40, c // 2), generator=g, dtype=torch.uint8).cuda()
+    scales = (torch.rand((40, 2), generator=g) / 8).to(BF).cuda()
+    xs = [rnd(g, n, c, dtype=BF).cuda() for _ in range(4)]
+    start = rnd(g, n, c, 3, dtype=BF).cuda(), rnd(g, n, c, s).cuda()
+
+    def step(x, conv, ssm):
+        u = lm.causal_conv_step(x, w, b, conv, activation="silu")
+        y = lm.selective_scan_step(u, u, A, B, C, ssm, dt_softplus=True)
+        return lm.matvec4(y, packed, scales)
+
+    eager = tuple(t.clone() for t in start)
+    want = [step(x, *eager) for x in xs]
+    state, x = tuple(t.clone() for t in start), xs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x, *(t.clone() for t in start))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, *state)
+    for t, v in zip(state, start):
+        t.copy_(v)
+    for k, v in enumerate(xs):
+        x.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k]), k
+        torch.empty(1 << 20, device="cuda").fill_(float(k))
+    assert all(torch.equal(t, v) for t, v in zip(state, eager))
+
+
+def test_refuses_tensors_elsewhere():
+    x = torch.zeros(1, 8, 4, device="cuda")
+    with pytest.raises(ValueError, match="GPU only"):
+        lm.causal_conv(x, torch.zeros(8, 4))
+    with pytest.raises(RuntimeError, match="element type"):
+        lm.causal_conv(x, torch.zeros(8, 4, device="cuda", dtype=HF))
