@@ -24,7 +24,7 @@ constexpr int kTB = 32;              // steps of a tile: 8 channels of one row p
 
 template <int NS, int QW, bool PRE> struct FwdLds {
     float2 in[2][kTB][kCH];                                          // d, d x
-    __attribute__((aligned(16))) float bc[2][kTB * 8 * QW * NS];
+    __attribute__((aligned(16))) float bc[2][kTB * bc_row(4 * QW * NS)];
     __attribute__((aligned(16))) float y[PRE ? 1 : 2][PRE ? 1 : QW][kTB][kRow];
 };
 

@@ -71,7 +71,7 @@ template <int NS, int QW, bool PRE> struct BwdLds {
     static constexpr int W = 4 * QW * NS, TB = bwd_tile(W);
     float2 in[2][TB][kCH];                                         // d, d x
     float s[2][TB][kCH];                                           // gy silu(z)
-    __attribute__((aligned(16))) float bc[2][TB * 2 * W];
+    __attribute__((aligned(16))) float bc[2][TB * bc_row(W)];
     // Sums over s of r B, r A a h, C h.
     __attribute__((aligned(16))) float o[PRE ? 1 : 2][3][PRE ? 1 : QW][PRE ? 1 : TB][kRow];
     float red[PRE ? 1 : 2][4][PRE ? 1 : TB][2 * W];                // dB, dC of 16 channels
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
         if constexpr (PRE) {
             for (int k0 = TB - 4; k0 >= 0; k0 -= 4) {
                 States4<NS, W> cs;
-                cs.load(bc + k0 * 2 * W + W + q * NS, lane);
+                cs.load(bc + k0 * bc_row(W) + W + q * NS, lane);
                 each<4>([&](auto step) {
                     constexpr int j = 3 - decltype(step)::value;
                     const float d = in[k0 + j][c].x, s = ss[k0 + j][c];

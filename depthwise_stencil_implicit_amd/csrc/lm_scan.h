@@ -133,6 +133,10 @@ template <int CK> __device__ __forceinline__ int64_t saved_at(const ScanP &p, co
     return p.off ? a.sp.start / CK + a.seq : a.seq * ((p.L + CK - 1) / CK);
 }
 
+// Words of a step's B and C in LDS: the steps that a row broadcast gathers lie
+// on different banks.
+constexpr int bc_row(int W) { return W <= 8 ? 2 * W : W == 16 ? 48 : W == 32 ? 80 : 160; }
+
 // B and C of a tile on their way to LDS: threads 0 .. 127 hold n neighbouring
 // states of one row of B, threads 128 .. 255 of C.  DENSE: states are
 // contiguous and S a multiple of n.
@@ -147,7 +151,7 @@ template <typename T, int W, int TB, bool DENSE> struct BcRegs {
         const int e = tid % 128 * n;
         const S4 &st = tid < 128 ? p.Bs : p.Cs;
         row = e / W, s0 = e % W;
-        to = row * (2 * W) + (tid < 128 ? 0 : W) + s0;
+        to = row * bc_row(W) + (tid < 128 ? 0 : W) + s0;
         base = static_cast<const T *>(tid < 128 ? p.Bm : p.Cm) + a.sp.row0 * st.n + a.g * st.g + a.sp.start * st.l;
         if (DENSE) base += s0 < p.S ? s0 : 0;
         sl = st.l;
@@ -193,7 +197,7 @@ template <int NS, int W> struct States4 {
 #pragma unroll
         for (int m = 0; m < n; ++m) {
             const int f = (m * 16 + (lane & 15)) % (4 * NS);
-            v[m] = bc[f / NS * (2 * W) + f % NS];
+            v[m] = bc[f / NS * bc_row(W) + f % NS];
         }
     }
     template <int J, int I> __device__ __forceinline__ float at() const
@@ -295,8 +299,8 @@ template <int NS, int W, bool WITH_C> struct Steps4 {
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = in[k + j][ch];
-        b.load(bc + k * 2 * W + q * NS, lane);
-        if constexpr (WITH_C) c.load(bc + k * 2 * W + W + q * NS, lane);
+        b.load(bc + k * bc_row(W) + q * NS, lane);
+        if constexpr (WITH_C) c.load(bc + k * bc_row(W) + W + q * NS, lane);
     }
 };
 
