@@ -16,10 +16,10 @@
 // A workgroup works on tiles of 16 outputs; its waves take blocks of 128
 // columns in turn (each lane 16 bytes = 32 weights of one output) and join
 // through LDS.  mv4_tiles keeps the rows of x in registers over many tiles, so
-// its loop only streams weights; mv4_stream, for other groups and row lengths,
-// loads x with each block.
+// its loop only streams weights; mv4_stream, for other groups, rows under 128
+// columns and over 130944, loads x with each block.
 //
-// Measured: 4 rows, 8192 x 65536 bf16 in 68 us (4.1 TB/s; mv4_stream 177), one
+// Measured: 4 rows, 8192 x 65536 bf16 in 67 us (4.1 TB/s; mv4_stream 177), one
 // row, 4096 x 8192 in 8.2 us, of which a launch is 1.8 and the weights' bytes
 // 3.4; 11 rows, 5120 x 2501 f16 with zeros in 12 us.
 #include <hip/hip_runtime.h>
@@ -239,20 +239,42 @@ template <typename T, bool WIDE> __global__ __launch_bounds__(64 * kMvWaves) voi
     }
 }
 
-// At most eight NB blocks of columns, GR columns per group (128: one group
-// holds a block or more), NB blocks of every wave with their x in registers.  Each
-// block's weights of the next tile are requested as soon as the present ones
-// are used, so NB KiB per wave stay in flight across the barrier of a tile.
+// V elements (2 or 4) moved down by `by` < V places.
+template <int V, typename R> __device__ __forceinline__ void move_down(R &r, int by)
+{
+    if constexpr (R::n == V) {   // words
+#pragma unroll
+        for (int s = 1; s < V; s *= 2)
+#pragma unroll
+            for (int i = 0; i + s < V; ++i) r.w[i] ^= (r.w[i] ^ r.w[i + s]) & (by & s ? ~0u : 0u);
+    } else if constexpr (V == 2) r.w[0] >>= 16 * by;
+    else {
+        const uint64_t v = ((uint64_t)r.w[1] << 32 | r.w[0]) >> (16 * by);
+        r.w[0] = (uint32_t)v, r.w[1] = (uint32_t)(v >> 32);
+    }
+}
+
+// GR columns per group (128: one group holds a block or more), NB blocks of
+// every wave with their x in registers.  With GR < 128 the last block may be
+// cut short at a multiple of 32 columns: its missing weights and scales are
+// read from columns that exist, against zeros in x.  Not with NB = 4, whose
+// registers are full: mv4_parts gives a cut row's parts at most 32 blocks.
+// (4 rows, 8160 x 32768 in groups of 32: 50 us for bf16, 116 with mv4_stream;
+// 4160 x 16384 f32 25 and 50; one row, 8160 x 4000 f32 24 and 23.)
+// Each block's weights of the next tile are requested as soon as the present
+// ones are used, so NB KiB per wave stay in flight across the barrier of a tile.
 template <typename T, int GR, int NB, bool Z>
 __global__ __launch_bounds__(64 * kTileWaves) void mv4_tiles(const MvP p, int tiles, float *partial)
 {
     constexpr int NG = 128 / GR;
+    constexpr bool cut = GR < 128 && NB < 4;
     extern __shared__ __attribute__((aligned(16))) float sh[];   // sums of x [block][group][16], then [2][wave][16][17]
     const int waves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kb = lane >> 4,
               col = lane & 15;
     // Blocks of this part of the columns: first .. first + blocks - 1.
-    const int all = (int)p.K / 128, first = (int)(blockIdx.z * (int64_t)all / gridDim.z),
+    const int K = (int)p.K, all = (K + 127) / 128, groups = K / GR,
+              first = (int)(blockIdx.z * (int64_t)all / gridDim.z),
               blocks = (int)((blockIdx.z + 1) * (int64_t)all / gridDim.z) - first;
     const int m0 = blockIdx.y * 16, rows = p.M - m0 < 16 ? (int)p.M - m0 : 16;
     constexpr bool want_sx = std::is_same<T, bf16_t>::value || Z;
@@ -266,12 +288,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void mv4_tiles(const MvP p, int ti
         Raw<T, NG> s;
         Raw<T, Z ? NG : 1> z;
     } ring[NB];
-    // Offsets from uniform bases fit 32 bits (tile_blocks sees to it).
+    // Offsets from uniform bases fit 32 bits (mv4_parts sees to it).
     const auto fetch = [&](int tile, int r) {
         const int b = first + (wave + r * waves < blocks ? wave + r * waves : 0);
         const uint32_t n = tile * 16 + col < (int)p.N ? tile * 16 + col : (int)p.N - 1;
-        ring[r].w = *reinterpret_cast<const uint4 *>(p.w + b * 64 + (n * (uint32_t)p.w_n + kb * 16));
-        const int g = GR == 128 ? (int)((uint32_t)b * p.block_group >> 20) : b * NG;
+        const uint32_t in_block = !cut || b * 128 + 32 * kb < K ? kb * 16 : 0;
+        ring[r].w = *reinterpret_cast<const uint4 *>(p.w + b * 64 + (n * (uint32_t)p.w_n + in_block));
+        const int g = GR == 128 ? (int)((uint32_t)b * p.block_group >> 20) : !cut || b * NG < groups - NG ? b * NG : groups - NG;
         ring[r].s = load_raw<T, NG>(sc + g + n * (uint32_t)p.sc_n);
         if constexpr (Z) ring[r].z = load_raw<T, NG>(ze + g + n * (uint32_t)p.z_n);
     };
@@ -282,7 +305,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void mv4_tiles(const MvP p, int ti
     Raw<T, 8> raw[NB][4];
     const auto x_at = [&](int r, int j) {
         const int b = wave + r * waves;
-        return (first + (b < blocks ? b : 0)) * 128 + (GR == 128 ? 32 * kb + 8 * j : 32 * j + 8 * kb);
+        const int k = (first + (b < blocks ? b : 0)) * 128;
+        return GR == 128 ? k + 32 * kb + 8 * j : (!cut || k + 32 * j < K ? k + 32 * j : 0) + 8 * kb;
     };
 #pragma unroll
     for (int r = 0; r < NB; ++r)
@@ -300,7 +324,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void mv4_tiles(const MvP p, int ti
         f32x4 sx = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (wave + r * waves >= blocks) raw[r][j].zero();
+            if (wave + r * waves >= blocks || (cut && (first + wave + r * waves) * 128 + 32 * j >= K)) raw[r][j].zero();
             xa[r][j].set(raw[r][j]);
             xa[r][j].times(ones<typename MvOp<T>::in>(), sx);
             if ((j + 1) * 32 % GR == 0) {   // the same in every column: the first lane of each four rows keeps it
@@ -315,8 +339,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void mv4_tiles(const MvP p, int ti
 #pragma unroll
         for (int r = 0; r < NB; ++r) {
             uint32_t word[4] = {ring[r].w.x, ring[r].w.y, ring[r].w.z, ring[r].w.w};
-            const Raw<T, NG> s = ring[r].s;
-            const auto z = ring[r].z;
+            Raw<T, NG> s = ring[r].s;
+            auto z = ring[r].z;
+            if constexpr (cut) {   // the cut block's scales were read with those before them
+                const int over = (first + wave + r * waves + 1) * NG - groups, by = over > 0 && over < NG ? over : 0;
+                move_down<NG>(s, by);
+                if constexpr (Z) move_down<NG>(z, by);
+            }
             fetch(tile + (int)gridDim.x < tiles ? tile + (int)gridDim.x : tile, r);
             if (GR < 128) transpose_words(word);
             f32x4 acc = {0, 0, 0, 0};
@@ -385,7 +414,7 @@ template <typename T> __global__ __launch_bounds__(256) void mv4_rows(const MvP 
 template <typename T, int GR> void run_tiles(const MvP &a, int parts, float *partial, hipStream_t s)
 {
     // The fewest blocks per wave: a short call's time is its longest wave's.
-    const int blocks = (int)lm_cdiv(a.K / 128, parts), nb = blocks <= 16 ? 1 : blocks <= 32 ? 2 : 4;
+    const int blocks = (int)lm_cdiv(lm_cdiv(a.K, 128), parts), nb = blocks <= 16 ? 1 : blocks <= 32 ? 2 : 4;
     const int waves = (int)lm_cdiv(blocks, nb), tiles = (int)lm_cdiv(a.N, 16);
     // At least four waves finish a tile of 16 rows.
     const int threads = 64 * (waves < 4 ? 4 : waves);

@@ -41,13 +41,13 @@ inline int64_t mv4_rows_bytes(const lm_plan_t &p)
 }
 inline int mv4_parts(const lm_plan_t &p)
 {
-    const int64_t group = p.K / p.G, blocks = p.K / 128;
+    const int64_t group = p.K / p.G, blocks = lm_cdiv(p.K, 128);
     for (int s : {LM_SCALES, LM_ZEROS})
         if (p.t[s].rank && p.G > 1 && p.t[s].strides[1] != 1) return 0;
     for (int s : {LM_W, LM_SCALES, LM_ZEROS})   // offsets of 32 bits
         if (p.t[s].rank && p.t[s].strides[0] > 0x7fffffff / (p.C + 1)) return 0;
-    if (p.C > 0x7fffff00 || p.K % 128 || blocks >= 1024 || (group % 128 && group != 64 && group != 32)) return 0;
-    return (int)lm_cdiv(blocks, p.dtype == CONV_F32 ? 16 : 64);
+    if (p.C > 0x7fffff00 || p.K < 128 || blocks >= 1024 || (group % 128 && group != 64 && group != 32)) return 0;
+    return (int)lm_cdiv(blocks, p.dtype == CONV_F32 ? 16 : p.K % 128 ? 32 : 64);
 }
 
 typedef void *const *lm_ptrs;

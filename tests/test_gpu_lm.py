@@ -316,7 +316,8 @@ def test_selective_scan_step(dt, C, S, G):
 @pytest.mark.parametrize("M,K,N,group,zeros,bias", [
     (1, 128, 16, 128, False, False), (1, 32, 1, 32, True, True), (16, 256, 33, 64, True, False), (17, 160, 40, 32, False, True),
     (3, 1152, 50, 128, True, True), (5, 1152, 70, 384, False, False), (40, 96, 19, 96, True, True), (2, 4096, 17, 4096, False, True),
-    (0, 64, 8, 32, False, False), (7, 2080, 31, 32, True, False)])
+    (0, 64, 8, 32, False, False), (7, 2080, 31, 32, True, False), (2, 192, 35, 64, True, True), (3, 224, 20, 32, False, False),
+    (1, 1120, 50, 224, True, False)])
 def test_matvec4(dt, M, K, N, group, zeros, bias):
     g = gen(M + K + N)
     x = rnd(g, M, K, dtype=dt).cuda()
@@ -341,7 +342,7 @@ def test_matvec4(dt, M, K, N, group, zeros, bias):
 
 @pytest.mark.parametrize("dt", [BF, HF, F])
 @pytest.mark.parametrize("M,K,N,group,zeros", [(2, 8320, 37, 128, False), (17, 16384, 16, 64, True), (1, 9088, 40, 32, False),
-                                               (3, 10240, 20, 2560, True)])
+                                               (3, 10240, 20, 2560, True), (2, 8224, 33, 32, True), (5, 4160, 18, 64, False)])
 def test_matvec4_long_rows(dt, M, K, N, group, zeros):
     """Rows split over several workgroups."""
     g = gen(M + K + N)
