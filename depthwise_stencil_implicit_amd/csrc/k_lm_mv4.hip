@@ -19,7 +19,7 @@
 // its loop only streams weights; mv4_stream, for other groups, rows under 128
 // columns and over 130944, loads x with each block.
 //
-// Measured: 4 rows, 8192 x 65536 bf16 in 67 us (4.1 TB/s; mv4_stream 177), one
+// Measured: 4 rows, 8192 x 65536 bf16 in 68 us (4.1 TB/s; mv4_stream 177), one
 // row, 4096 x 8192 in 8.2 us, of which a launch is 1.8 and the weights' bytes
 // 3.4; 11 rows, 5120 x 2501 f16 with zeros in 12 us.
 #include <hip/hip_runtime.h>
