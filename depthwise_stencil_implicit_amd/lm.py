@@ -269,7 +269,9 @@ def selective_scan(x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus
     B, C = _grouped(B, 4), _grouped(C, 4)
     _on_gpu(x)
     y = torch.empty_like(x) if want_y else None
-    last = torch.empty((_seqs(x, offsets), x.shape[1], A_.shape[-1]), device=x.device) if return_state else None
+    # Their type is said: without it they would have torch's default one.
+    last = (torch.empty((_seqs(x, offsets), x.shape[1], A_.shape[-1]), dtype=torch.float32, device=x.device)
+            if return_state else None)
     saved = _new_saved(x, A_, offsets) if save else None
     _call(A.LM_SCAN,
           [(_X, x), (_DT, dt), (_A, A_), (_B, B), (_C, C), (_D, D), (_Z, z), (_DTB, dt_bias), (_S0, state), (_OFF, offsets)],
@@ -286,7 +288,7 @@ def _new_saved(x, A_, offsets) -> torch.Tensor:
         ns *= 2
     ck = 16 if rows == 4 else max(1, 32 // ns)
     count = x.shape[0] * -(-x.shape[2] // ck) if offsets is None else x.shape[2] // ck + offsets.shape[0]
-    return torch.empty(count * x.shape[1] * rows * ns, device=x.device)
+    return torch.empty(count * x.shape[1] * rows * ns, dtype=torch.float32, device=x.device)
 
 
 def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False, state=None,
