@@ -89,17 +89,18 @@ def _make_plan(op, tensors, flags=0, max_len=0, chunk=0) -> A.LmPlan:
     return p
 
 
-# Plans by operator, arguments, shapes, strides and types (host structs only).
+# Plans by operator, arguments and every tensor's shape, strides and type (host structs only).
 _plans: dict = {}
 
 
-def _call(op, ins, outs, flags=0, max_len=None, chunk=None, extra=None) -> None:
+def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
     """Plan (or its cached copy) and launch of a call on ``ins`` and ``outs``,
-    lists of (place, tensor or None).  Outputs are allocated from the inputs'
-    descriptors and so have no place in the key; ``extra`` says which exist."""
-    key = [op, flags, max_len, chunk, extra]
+    lists of (place, tensor or None).  Outputs are part of the key too: not all
+    of them follow from the inputs (dstate from a state that the call does not
+    read), and lm_run sees pointers only."""
+    key = [op, flags, max_len, chunk]
     dev = -1
-    for slot, t in ins:
+    for slot, t in ins + outs:
         if t is None:
             key.append(None)
             continue
@@ -114,15 +115,12 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None, extra=None) -> None:
     key = tuple(key)
     p = _plans.get(key)
     if p is None:
-        p = _make_plan(op, dict(ins + outs), flags, max_len or 0, chunk or 0)
+        p = _make_plan(op, dict(ins + outs), flags, max_len, chunk)
         if len(_plans) >= 512:
             _plans.clear()
         _plans[key] = p
     q = _Ptrs()
-    for slot, t in ins:
-        if t is not None:
-            q[slot] = t.data_ptr()
-    for slot, t in outs:
+    for slot, t in ins + outs:
         if t is not None:
             q[slot] = t.data_ptr()
     _run(p, q, dev)
@@ -184,7 +182,7 @@ def causal_conv(x, w, b=None, *, activation=None, state=None, offsets=None, max_
     y = torch.empty_like(x)
     last = _rows_like(_seqs(x, offsets), x.shape[1], w.shape[-1] - 1, x) if return_state else None
     _call(A.LM_CONV, [(_X, x), (_W, w), (_BIAS, b), (_S0, state), (_OFF, offsets)], [(_Y, y), (_S1, last)], _act(activation),
-          max_len, chunk, return_state)
+          max_len, chunk)
     return ConvOut(y, last)
 
 
@@ -200,7 +198,7 @@ def causal_conv_backward(gy, x, w, b=None, *, activation=None, state=None, offse
     db = torch.empty(b.shape, dtype=b.dtype, device=b.device) if need_dw and b is not None else None
     ds = torch.empty_like(state) if state is not None else None
     _call(A.LM_CONV_BWD, [(_GY, gy), (_X, x), (_W, w), (_BIAS, b), (_S0, state), (_OFF, offsets), (_GS, gstate)],
-          [(_DX, dx), (_DW, dw), (_DBIAS, db), (_DS, ds)], _act(activation), max_len, chunk, (need_dx, need_dw))
+          [(_DX, dx), (_DW, dw), (_DBIAS, db), (_DS, ds)], _act(activation), max_len, chunk)
     return ConvGrads(dx, dw.view(shape) if dw is not None else None, db, ds)
 
 
@@ -275,8 +273,7 @@ def selective_scan(x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus
     saved = _new_saved(x, A_, offsets) if save else None
     _call(A.LM_SCAN,
           [(_X, x), (_DT, dt), (_A, A_), (_B, B), (_C, C), (_D, D), (_Z, z), (_DTB, dt_bias), (_S0, state), (_OFF, offsets)],
-          [(_Y, y), (_S1, last), (_SAVED, saved)], A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk,
-          (want_y, return_state, save))
+          [(_Y, y), (_S1, last), (_SAVED, saved)], A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk)
     return ScanOut(y, last, saved)
 
 
@@ -309,7 +306,7 @@ def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None
           [(_GY, gy), (_X, x), (_DT, dt), (_A, A_), (_B, B), (_C, C), (_D, D), (_Z, z), (_DTB, dt_bias), (_OFF, offsets),
            (_GS, gstate), (_SAVED, saved)],
           [(_DX, dx), (_DDT, ddt), (_DA, dA), (_DB, dB), (_DC, dC), (_DD, dD), (_DZ, dz), (_DDTB, db), (_DS, ds)],
-          A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk, (state.shape, state.stride()) if state is not None else None)
+          A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk)
     return ScanGrads(dx, ddt, dA, dB.view(b_shape), dC.view(c_shape), dD, dz, db, ds)
 
 

@@ -47,3 +47,26 @@ def test_states_are_f32_under_any_default_type(calls, default_dtype, other):
     for s in (1, 12, 20, 64):
         x, _, a, _, _ = scan_args(s=s)
         assert lm._new_saved(x, a, None).dtype == F
+
+
+def test_a_kept_plan_serves_only_its_own_outputs(calls, monkeypatch):
+    """dstate has the state's type and layout: a state that the kept plan was
+    not made for is checked anew, and one elsewhere is refused."""
+    args, gy = scan_args(), torch.zeros(2, 8, 20)
+    state = torch.zeros(2, 8, 16)
+    lm.selective_scan_backward(gy, *args, state=state, saved=lm._new_saved(args[0], args[2], None))
+    saved = lm._new_saved(args[0], args[2], None)
+    for other in (BF, HF):
+        with pytest.raises(lm.ConvError, match="element type"):
+            lm.selective_scan_backward(gy, *args, state=state.to(other), saved=saved)
+    turned = torch.zeros(2, 16, 8).transpose(1, 2)
+    lm.selective_scan_backward(gy, *args, state=turned, saved=saved)
+    assert list(calls[-1][0].t[lm._DS].strides[:3]) == [128, 1, 8]
+    made = len(calls)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: -1 if self.dim() == 3 and self.shape[2] == 16 else 0)
+    with pytest.raises(ValueError, match="GPU only"):
+        lm.selective_scan_backward(gy, *args, state=state, saved=saved)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1 if self.dim() == 3 and self.shape[2] == 16 else 0)
+    with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        lm.selective_scan_backward(gy, *args, state=state, saved=saved)
+    assert len(calls) == made
