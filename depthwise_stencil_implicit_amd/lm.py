@@ -126,15 +126,14 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
     _run(p, q, dev)
 
 
-def _run(p: A.LmPlan, q, dev: int, stream: Optional[int] = None) -> None:
+def _run(p: A.LmPlan, q, dev: int) -> None:
+    """Launch on the device's current stream, which the workspace belongs to."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _run(p, q, dev, stream)
+            return _run(p, q, dev)
     n = p.workspace_bytes
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    st = A.lib().lm_run(ctypes.byref(p), q, ws.data_ptr() if n else None, n, stream)
+    st = A.lib().lm_run(ctypes.byref(p), q, ws.data_ptr() if n else None, n, torch._C._cuda_getCurrentRawStream(dev))
     if st != A.OK:
         raise ConvError(st)
 
@@ -203,7 +202,11 @@ def causal_conv_backward(gy, x, w, b=None, *, activation=None, state=None, offse
 
 
 class _Step:
-    """A plan whose output is a new contiguous tensor of the plan's shape."""
+    """A plan whose output is a new contiguous tensor of the plan's shape.
+
+    ``run`` launches on ``stream`` (a raw handle; the current stream without
+    one).  A new output belongs to that stream, as if it had been made the
+    current one for the call."""
 
     def __init__(self, op, tensors, shape, ref, flags=0):
         _on_gpu(*[t for t in tensors.values() if t is not None])
@@ -216,8 +219,19 @@ class _Step:
     def empty_output(self) -> torch.Tensor:
         return torch.empty(self.shape, dtype=self.dtype, device=self.device)
 
-    def _launch(self, q, stream):
-        _run(self.plan, q, self.device.index, stream)
+    def _launch(self, q, y, stream) -> torch.Tensor:
+        dev = self.device.index
+        if stream is not None and stream != torch._C._cuda_getCurrentRawStream(dev):
+            # Memory of the present stream's pool could be given out again
+            # there while the kernels use it: allocate on the other stream.
+            s = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+            with torch.cuda.stream(s):
+                return self._launch(q, y, None)
+        if y is None:
+            y = self.empty_output()
+        q[_Y] = y.data_ptr()
+        _run(self.plan, q, dev)
+        return y
 
 
 class PreparedCausalConvStep(_Step):
@@ -228,16 +242,13 @@ class PreparedCausalConvStep(_Step):
                          _act(activation))
 
     def run(self, x, w, b, state, rows=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
-        if y is None:
-            y = self.empty_output()
         q = _Ptrs()
-        q[_X], q[_W], q[_S1], q[_Y] = x.data_ptr(), w.data_ptr(), state.data_ptr(), y.data_ptr()
+        q[_X], q[_W], q[_S1] = x.data_ptr(), w.data_ptr(), state.data_ptr()
         if b is not None:
             q[_BIAS] = b.data_ptr()
         if rows is not None:
             q[_ROWS] = rows.data_ptr()
-        self._launch(q, stream)
-        return y
+        return self._launch(q, y, stream)
 
 
 def causal_conv_step(x, w, b, state, *, activation=None, rows=None) -> torch.Tensor:
@@ -320,11 +331,9 @@ class PreparedSelectiveScanStep(_Step):
 
     def run(self, x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None, rows=None, y=None,
             stream: Optional[int] = None) -> torch.Tensor:
-        if y is None:
-            y = self.empty_output()
         q = _Ptrs()
         q[_X], q[_DT], q[_A], q[_B], q[_C] = x.data_ptr(), dt.data_ptr(), A_.data_ptr(), B.data_ptr(), C.data_ptr()
-        q[_S1], q[_Y] = state.data_ptr(), y.data_ptr()
+        q[_S1] = state.data_ptr()
         if D is not None:
             q[_D] = D.data_ptr()
         if z is not None:
@@ -333,8 +342,7 @@ class PreparedSelectiveScanStep(_Step):
             q[_DTB] = dt_bias.data_ptr()
         if rows is not None:
             q[_ROWS] = rows.data_ptr()
-        self._launch(q, stream)
-        return y
+        return self._launch(q, y, stream)
 
 
 def selective_scan_step(x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
@@ -355,16 +363,13 @@ class PreparedMatvec4(_Step):
                          (x.shape[0], packed.shape[0]), x)
 
     def run(self, x, packed, scales, zeros=None, bias=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
-        if y is None:
-            y = self.empty_output()
         q = _Ptrs()
-        q[_X], q[_W], q[_SCALES], q[_Y] = x.data_ptr(), packed.data_ptr(), scales.data_ptr(), y.data_ptr()
+        q[_X], q[_W], q[_SCALES] = x.data_ptr(), packed.data_ptr(), scales.data_ptr()
         if zeros is not None:
             q[_ZEROS] = zeros.data_ptr()
         if bias is not None:
             q[_BIAS] = bias.data_ptr()
-        self._launch(q, stream)
-        return y
+        return self._launch(q, y, stream)
 
 
 def matvec4(x, packed, scales, zeros=None, bias=None) -> torch.Tensor:

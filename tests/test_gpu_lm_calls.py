@@ -1,0 +1,91 @@
+"""Calls of the sequence operators as programs make them: prepared steps with
+an output and a stream of the caller's, steps by name, extreme values, packed
+batches, products that are exact."""
+import pytest
+import torch
+
+import lm_reference as R
+from depthwise_stencil_implicit_amd import lm
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F = torch.bfloat16, torch.float16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rnd(g, *shape, dtype=F, scale=1.0):
+    return (scale * torch.randn(shape, generator=g)).to(dtype).cuda()
+
+
+def pool_of(t):
+    """The stream whose memory holds t."""
+    at = t.data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not in the allocator's memory")
+
+
+def prepared(kind, dt=BF):
+    """(run(**kw), state or None, its start, y of the plain call, that call's state)."""
+    g = gen(31)
+    if kind == "conv":
+        x, w, b, st = rnd(g, 3, 70, dtype=dt), rnd(g, 70, 4, dtype=dt), rnd(g, 70, dtype=dt), rnd(g, 3, 70, 3, dtype=dt)
+        p = lm.PreparedCausalConvStep(x, w, b, st, activation="silu")
+        run = lambda s, **kw: p.run(x, w, b, s, **kw)  # noqa: E731
+        plain = lambda s: lm.causal_conv_step(x, w, b, s, activation="silu")  # noqa: E731
+    elif kind == "scan":
+        x, d, z, B, C = rnd(g, 3, 70, dtype=dt), rnd(g, 3, 70, dtype=dt), rnd(g, 3, 70, dtype=dt), rnd(g, 3, 1, 16, dtype=dt), rnd(g, 3, 1, 16, dtype=dt)
+        A, D, st = -torch.exp(rnd(g, 70, 16)), rnd(g, 70), rnd(g, 3, 70, 16)
+        p = lm.PreparedSelectiveScanStep(x, d, A, B, C, st, D=D, z=z, dt_softplus=True)
+        run = lambda s, **kw: p.run(x, d, A, B, C, s, D=D, z=z, **kw)  # noqa: E731
+        plain = lambda s: lm.selective_scan_step(x, d, A, B, C, s, D=D, z=z, dt_softplus=True)  # noqa: E731
+    else:
+        # More columns than one workgroup takes, and in "apart" an x to be gathered first.
+        k = 8448 if kind == "split" else 256
+        x = rnd(g, 3, k, dtype=dt) if kind == "split" else rnd(g, k, 3, dtype=dt).t()
+        packed = torch.randint(0, 256, (50, k // 2), generator=g, dtype=torch.uint8).cuda()
+        scales, st = (torch.rand((50, k // 32), generator=g) / 8).to(dt).cuda(), None
+        p = lm.PreparedMatvec4(x, packed, scales)
+        assert p.plan.workspace_bytes > 0
+        run = lambda s, **kw: p.run(x, packed, scales, **kw)  # noqa: E731
+        plain = lambda s: lm.matvec4(x, packed, scales)  # noqa: E731
+    copy = lambda: st.clone() if st is not None else None  # noqa: E731
+    after = copy()
+    return run, copy, plain(after), after
+
+
+@pytest.mark.parametrize("kind", ["conv", "scan", "split", "apart"])
+def test_prepared_run_on_a_given_stream(kind):
+    """With and without an output of the caller's, on the current stream, on
+    another one that is busy while the current one allocates, and on the default
+    stream from within another."""
+    run, copy, want, after = prepared(kind)
+    s = torch.cuda.Stream()
+    for stream in (None, torch.cuda.current_stream().cuda_stream, s.cuda_stream):
+        for given in (False, True):
+            state = copy()
+            y = torch.full_like(want, 5.0) if given else None
+            big = torch.zeros(1 << 26, device="cuda")
+            torch.cuda.synchronize()
+            if stream == s.cuda_stream:
+                with torch.cuda.stream(s):
+                    for _ in range(8):
+                        big.add_(1.0)
+            out = run(state, y=y, stream=stream)
+            for size in (want.numel() * want.element_size(), 50 * 3 * 2 * 4, 3 * 256 * 2, 1 << 16):
+                torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+            torch.cuda.synchronize()
+            assert not given or out is y
+            assert given or pool_of(out) == (s.cuda_stream if stream == s.cuda_stream else torch.cuda.current_stream().cuda_stream)
+            assert torch.equal(out, want), (stream, given)
+            assert state is None or torch.equal(state, after)
+    state = copy()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        out = run(state, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and pool_of(out) == 0

@@ -1,6 +1,8 @@
 """What the binding of the sequence operators hands to the library, on the CPU:
 the outputs it allocates and the plans it keeps.  ``calls`` stands in for the
 launch and records each call's plan and tensors."""
+import contextlib
+
 import pytest
 import torch
 
@@ -70,3 +72,38 @@ def test_a_kept_plan_serves_only_its_own_outputs(calls, monkeypatch):
     with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
         lm.selective_scan_backward(gy, *args, state=state, saved=saved)
     assert len(calls) == made
+
+
+def test_prepared_calls_allocate_on_the_stream_they_launch_on(monkeypatch):
+    """The output and the workspace of ``run(stream=...)`` belong to that
+    stream: the current one's next tensor could else take their memory while
+    the kernels still use it."""
+    here, log = [7], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, here[0] = here[0], s
+        yield
+        here[0] = before
+
+    class Fake(lm._Step):
+        def __init__(self):
+            self.plan, self.device = None, torch.device("cuda", 0)
+
+        def empty_output(self):
+            log.append(("output", here[0]))
+            return torch.zeros(1)
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: here[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device: s)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: 0)
+    monkeypatch.setattr(lm, "_run", lambda *a: log.append(("launch", here[0])))
+    for given, used in ((None, 7), (7, 7), (9, 9), (0, 0)):
+        log.clear()
+        q, y = lm._Ptrs(), Fake()._launch
+        out = y(q, None, given)
+        assert log == [("output", used), ("launch", used)] and q[lm._Y] == out.data_ptr() and here == [7]
+        log.clear()
+        mine = torch.zeros(1)
+        assert y(q, mine, given) is mine and q[lm._Y] == mine.data_ptr() and log == [("launch", used)]
