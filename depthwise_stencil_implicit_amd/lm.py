@@ -255,7 +255,9 @@ def causal_conv_step(x, w, b, state, *, activation=None, rows=None) -> torch.Ten
     """One token: x [N, C], state [N, C, K-1] updated in place.  With ``rows``
     (int32 [N], distinct) batch row n uses state row rows[n]; a row outside
     the state is left out and its y is zero."""
-    return PreparedCausalConvStep(x, w, b, state, activation=activation, rows=rows).run(x, _taps(w), b, state, rows)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _call(A.LM_CONV_STEP, [(_X, x), (_W, _taps(w)), (_BIAS, b), (_S1, state), (_ROWS, rows)], [(_Y, y)], _act(activation))
+    return y
 
 
 # --------------------------------------------------------- selective scan --
@@ -349,8 +351,10 @@ def selective_scan_step(x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None,
                         rows=None) -> torch.Tensor:
     """One token: x, dt, z [N, C], B and C [N, G, S] (or [N, S]), state f32
     [N, C, S] updated in place; ``rows`` as in ``causal_conv_step``."""
-    p = PreparedSelectiveScanStep(x, dt, A_, B, C, state, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, rows=rows)
-    return p.run(x, dt, A_, B, C, state, D=D, z=z, dt_bias=dt_bias, rows=rows)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _call(A.LM_SCAN_STEP, [(_X, x), (_DT, dt), (_A, A_), (_B, _grouped(B, 3)), (_C, _grouped(C, 3)), (_S1, state), (_D, D),
+                           (_Z, z), (_DTB, dt_bias), (_ROWS, rows)], [(_Y, y)], A.LM_SOFTPLUS if dt_softplus else 0)
+    return y
 
 
 # ---------------------------------------------------------- 4-bit products --
@@ -381,7 +385,8 @@ def matvec4(x, packed, scales, zeros=None, bias=None) -> torch.Tensor:
     few rows: 16 cost about what one does, more repeat the weights' pass.  A
     row whose sums pass f32's range at 256 times x gives infinities or NaN."""
     x2 = x.reshape(-1, x.shape[-1])
-    y = PreparedMatvec4(x2, packed, scales, zeros, bias).run(x2, packed, scales, zeros, bias)
+    y = torch.empty((x2.shape[0], packed.shape[0]), dtype=x.dtype, device=x.device)
+    _call(A.LM_MV4, [(_X, x2), (_W, packed), (_SCALES, scales), (_ZEROS, zeros), (_BIAS, bias)], [(_Y, y)])
     return y.view(x.shape[:-1] + (packed.shape[0],))
 
 

@@ -107,3 +107,39 @@ def test_prepared_calls_allocate_on_the_stream_they_launch_on(monkeypatch):
         log.clear()
         mine = torch.zeros(1)
         assert y(q, mine, given) is mine and q[lm._Y] == mine.data_ptr() and log == [("launch", used)]
+
+
+def test_steps_by_name_plan_once(calls, monkeypatch):
+    """A decoding loop calls them once per token and layer: only the first call
+    of a shape checks and plans."""
+    plans, make = [], lm._make_plan
+    monkeypatch.setattr(lm, "_make_plan", lambda *a, **k: plans.append(a) or make(*a, **k))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    x, w, st = torch.zeros(3, 8), torch.zeros(8, 4), torch.zeros(3, 8, 3)
+    dt, a, bc, h = torch.zeros(3, 8), torch.zeros(8, 16), torch.zeros(3, 16), torch.zeros(3, 8, 16)
+    packed, scales, wide = torch.zeros(5, 32, dtype=torch.uint8), torch.zeros(5, 2), torch.zeros(2, 3, 64)
+    for call in (lambda: lm.causal_conv_step(x, w[:, None], None, st, activation="silu"),
+                 lambda: lm.selective_scan_step(x, dt, a, bc, bc, h, dt_softplus=True),
+                 lambda: lm.matvec4(wide, packed, scales)):
+        plans.clear()
+        out = [call() for _ in range(3)]
+        assert len(plans) == 1 and len(calls) == 3, call
+        assert all(o.shape == out[0].shape and o.is_contiguous() for o in out)
+        assert calls[2][1][lm._Y] == out[2].data_ptr()
+        calls.clear()
+    assert out[0].shape == (2, 3, 5)
+    # Other rows of the same table are another call, an absent bias too.
+    lm.causal_conv_step(x, w, torch.zeros(8), st)
+    lm.causal_conv_step(x, w, torch.zeros(8), st, rows=torch.zeros(3, dtype=torch.int32))
+    assert lm._BIAS in calls[0][1] and lm._ROWS not in calls[0][1] and lm._ROWS in calls[1][1]
+
+
+def test_steps_by_name_refuse(calls):
+    x, w, st = torch.zeros(3, 8), torch.zeros(8, 4), torch.zeros(3, 8, 3)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        lm.causal_conv_step(x, w, None, st, rows=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(lm.ConvError, match="rows"):
+        lm.causal_conv_step(x, w, None, torch.zeros(5, 8, 3))
+    with pytest.raises(lm.ConvError, match="groups"):
+        lm.matvec4(torch.zeros(1, 64), torch.zeros(5, 32, dtype=torch.uint8), torch.zeros(5, 3))
+    assert not calls
