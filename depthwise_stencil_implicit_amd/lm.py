@@ -99,8 +99,8 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
     of them follow from the inputs (dstate from a state that the call does not
     read), and lm_run sees pointers only."""
     key = [op, flags, max_len, chunk]
-    dev = -1
-    for slot, t in ins + outs:
+    dev, q, tensors = -1, _Ptrs(), ins + outs
+    for slot, t in tensors:
         if t is None:
             key.append(None)
             continue
@@ -112,17 +112,14 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
                 raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
             dev = d
         key += (t.shape, t.stride(), t.dtype)
+        q[slot] = t.data_ptr()
     key = tuple(key)
     p = _plans.get(key)
     if p is None:
-        p = _make_plan(op, dict(ins + outs), flags, max_len, chunk)
+        p = _make_plan(op, dict(tensors), flags, max_len, chunk)
         if len(_plans) >= 512:
             _plans.clear()
         _plans[key] = p
-    q = _Ptrs()
-    for slot, t in ins + outs:
-        if t is not None:
-            q[slot] = t.data_ptr()
     _run(p, q, dev)
 
 
@@ -145,9 +142,9 @@ def _on_gpu(*tensors) -> None:
             raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
 
 
-def _rows_like(n, c, l, ref, dtype=None):
+def _rows_like(n, c, l, ref):
     """[n, c, l] stored as l rows of c channels."""
-    return torch.empty((n, l, c), dtype=dtype or ref.dtype, device=ref.device).transpose(1, 2)
+    return torch.empty_strided((n, c, l), (l * c, 1, c), dtype=ref.dtype, device=ref.device)
 
 
 def _act(activation) -> int:
