@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256 * QW + kStage, DENSE && QW == 1 ? 4 : QW + 1) v
     float A2[NS], h[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        A2[i] = real && q * NS + i < p.S ? kLog2e * p.A[cc * p.A_c + (q * NS + i) * p.A_s] : 0.f, h[i] = 0.f;
+        A2[i] = real && q * NS + i < p.S ? rate(p.A[cc * p.A_c + (q * NS + i) * p.A_s]) : 0.f, h[i] = 0.f;
     if (!PRE && real) {
         if (p.s0) get_states<NS>(p.s0, p.s0s, at.seq, cc, q * NS, p.S, h);
         fold_chunks<NS, W>(p, at.seq * (p.chunks - 1), 1, at.ch, cc, q * NS, A2, h);
@@ -246,11 +246,11 @@ template <typename T, int NS> __global__ __launch_bounds__(256) void scan_step(c
     float d = to_f32(static_cast<const T *>(p.dt)[n * p.dts.n + c * p.dts.c]);
     if (p.bias) d += p.bias[c * p.bias_s];
     if (p.softplus) d = softplus(d);
-    const float dx = d * x, d2 = d * kLog2e;
+    const float dx = d * x;
     float o = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        h[i] = __builtin_fmaf(hw_exp2(d2 * A[i]), h[i], dx * b[i]);
+        h[i] = __builtin_fmaf(hw_exp2(d * rate(A[i])), h[i], dx * b[i]);
         o = __builtin_fmaf(cv[i], h[i], o);
     }
     if (p.dense) store_f32<float, NS>(ph, h);

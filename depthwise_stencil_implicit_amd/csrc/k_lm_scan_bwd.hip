@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
     float A2[NS], dA[NS] = {}, r[NS] = {};   // A log2(e); r: the gradient that enters from the step behind
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        A2[i] = real && q * NS + i < p.S ? kLog2e * p.A[cc * p.A_c + (q * NS + i) * p.A_s] : 0.f;
+        A2[i] = real && q * NS + i < p.S ? rate(p.A[cc * p.A_c + (q * NS + i) * p.A_s]) : 0.f;
     if (!PRE && real) {
         if (p.gs) get_states<NS>(p.gs, p.gss, at.seq, cc, q * NS, p.S, r);
         int64_t rest, last = at.sp.len > 0 ? divide(at.sp.len - 1, p.chunk, rest) : 0;

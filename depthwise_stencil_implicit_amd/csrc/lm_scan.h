@@ -95,6 +95,15 @@ template <typename T, int V> __device__ __forceinline__ void put_row(T *p, int64
             if (i < n) p[i * cs] = from_f32<T>(v[i]);
     }
 }
+// A log2(e), the decay's exponent per unit of d.  An infinite A stands at the
+// largest number: exp2(d A2) keeps its limit 0 for any d that counts, and steps
+// with d = 0 (those past the end among them) leave the state as it is, where 0
+// times infinity would be NaN.
+__device__ __forceinline__ float rate(float A)
+{
+    const float v = kLog2e * A;
+    return __builtin_isinf(v) ? __builtin_copysignf(__FLT_MAX__, v) : v;
+}
 // V values per channel of an f32 parameter, zero without it or past the end.
 template <int V> __device__ __forceinline__ void get_param(const float *p, int64_t st, int64_t c0, int n, float (&o)[V])
 {

@@ -35,8 +35,10 @@
  *   x, dt, z, y, B and C share one dtype; A [C, S], D, dt_bias [C] and the
  *   states [N, C, S] are f32; B and C are [N, G, S, L].  S is 1 .. 64.
  *   Gradients have the types of what they are gradients of.  d = 0 (dt the
- *   type's lowest value, with softplus) leaves a state as it is.  A state that
- *   has overflowed to infinity may turn into NaN where the axis is split.
+ *   type's lowest value, with softplus) leaves a state as it is, also for an
+ *   infinite A, which counts as the largest number: A = -inf forgets the state
+ *   at every step of d > 0.  A state that has overflowed to infinity may turn
+ *   into NaN where the axis is split.
  *   LM_SAVED (f32, lm_plan_t.saved_floats elements): the states every few
  *   steps, written by LM_SCAN and read by LM_SCAN_BWD.
  *

@@ -89,3 +89,32 @@ def test_prepared_run_on_a_given_stream(kind):
         out = run(state, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and pool_of(out) == 0
+
+
+@pytest.mark.parametrize("dt,C,S,L,chunk", [(F, 20, 16, 37, None), (BF, 70, 12, 100, 32), (HF, 8, 40, 21, None), (F, 5, 64, 70, 32)])
+def test_scan_of_rates_that_forget_at_once(dt, C, S, L, chunk):
+    """A = -inf: exp(d A) is 0 for every d > 0, also where the axis ends inside
+    a block of steps; the gradients of A and d through that factor are 0."""
+    g = gen(C + L)
+    lay = lambda *s: rnd(g, *s, dtype=dt).movedim(-1, 1).contiguous().movedim(1, -1)  # noqa: E731
+    x, d, z, gy, B, Cm = lay(1, C, L), lay(1, C, L), lay(1, C, L), lay(1, C, L), lay(1, 1, S, L), lay(1, 1, S, L)
+    A, D, st, gs = -torch.exp(rnd(g, C, S, scale=0.5)), rnd(g, C), rnd(g, 1, C, S), rnd(g, 1, C, S)
+    A[::3, 1::2] = -torch.inf
+    kw = dict(D=D, z=z, state=st)
+    ref = lambda **k: R.scan(x, d, A.clamp(min=-1e30), B, Cm, softplus_dt=True, **kw, **k)  # noqa: E731  exp(-1e30 d) is 0 in 64 bits too
+    n = 8 * L + 4 * S + 128
+    got = lm.selective_scan(x, d, A, B, Cm, dt_softplus=True, return_state=True, chunk=chunk, **kw)
+    o, b = ref(), ref(bound=True)
+    R.assert_close(got.state, o["state"], b["state"], n, "state")
+    R.assert_close(got.y, o["y"], b["y"], n, "y")
+    grads = lm.selective_scan_backward(gy, x, d, A, B, Cm, dt_softplus=True, gstate=gs, chunk=chunk, **kw)
+    o, b = ref(gy=gy, gstate=gs), ref(gy=gy, gstate=gs, bound=True)
+    for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dstate"):
+        R.assert_close(getattr(grads, k), o[k], b[k], n + (L if k in ("dA", "dD") else C), k)
+    h = st.clone()
+    y = lm.selective_scan_step(x[:, :, 0], d[:, :, 0], A, B[..., 0], Cm[..., 0], h, D=D, z=z[:, :, 0], dt_softplus=True)
+    one = [v[..., :1] for v in (x, d, B, Cm, z)]
+    args = (one[0], one[1], A.clamp(min=-1e30), one[2], one[3])
+    o, b = R.scan(*args, D=D, z=one[4], softplus_dt=True, state=st), R.scan(*args, D=D, z=one[4], softplus_dt=True, state=st, bound=True)
+    R.assert_close(y, o["y"][..., 0], b["y"][..., 0], n, "step's y")
+    R.assert_close(h, o["state"], b["state"], n, "step's state")
