@@ -449,7 +449,7 @@ int launch_lm_scan_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
             a.part_bc, a.rows_total, p.L, a.blocks_g, (int)p.G, (int)p.S, W, static_cast<T *>(q[LM_DB]),
             lm_s4(p.t[LM_DB]), static_cast<T *>(q[LM_DC]), lm_s4(p.t[LM_DC]));
     });
-    scan_bwd_c<<<(int)lm_cdiv(p.C * (W + 2), 256), 256, 0, s>>>(
+    if (p.C > 0) scan_bwd_c<<<(int)lm_cdiv(p.C * (W + 2), 256), 256, 0, s>>>(
         a, W, static_cast<float *>(q[LM_DA]), p.t[LM_DA].strides[0], p.t[LM_DA].strides[1], static_cast<float *>(q[LM_DD]),
         p.t[LM_DD].strides[0], static_cast<float *>(q[LM_DDT_BIAS]), p.t[LM_DDT_BIAS].strides[0]);
     return lm_launch_status();

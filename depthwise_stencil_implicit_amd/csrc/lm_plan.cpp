@@ -353,8 +353,9 @@ extern "C" int lm_run(const lm_plan_t *p, void *const *q, void *workspace, size_
         if (!workspace || workspace_bytes < (size_t)p->workspace_bytes) return CONV_EINVAL;
         if (reinterpret_cast<uintptr_t>(workspace) % 256) return CONV_EALIGN;
     }
-    // Without sequences the sums over them (dw, dA ...) are still written: zeros.
-    if (p->C == 0 || (p->op == LM_MV4 && p->seqs == 0)) return CONV_OK;
+    // Sums are written without their terms too, as zeros: those over sequences
+    // (dw, dA ...) without sequences, those over channels (dB, dC) without channels.
+    if ((p->C == 0 && p->op != LM_SCAN_BWD) || (p->op == LM_MV4 && p->seqs == 0)) return CONV_OK;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (p->op) {
     case LM_CONV: return launch_lm_conv(*p, q, s);

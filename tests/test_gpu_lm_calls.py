@@ -118,3 +118,21 @@ def test_scan_of_rates_that_forget_at_once(dt, C, S, L, chunk):
     o, b = R.scan(*args, D=D, z=one[4], softplus_dt=True, state=st), R.scan(*args, D=D, z=one[4], softplus_dt=True, state=st, bound=True)
     R.assert_close(y, o["y"][..., 0], b["y"][..., 0], n, "step's y")
     R.assert_close(h, o["state"], b["state"], n, "step's state")
+
+
+@pytest.mark.parametrize("lens", [None, [3, 0, 4]])
+def test_scan_gradients_without_channels(lens):
+    """dB and dC are sums over the channels: zeros when there are none."""
+    from depthwise_stencil_implicit_amd import _abi as A
+    N, G, S, L = (1, 2, 5, 7) if lens else (2, 1, 5, 7)
+    x, B, rate = torch.zeros(N, 0, L, device="cuda"), rnd(gen(1), N, G, S, L), torch.zeros(0, S, device="cuda")
+    off = torch.tensor([0, 3, 3, 7], dtype=torch.int32, device="cuda") if lens else None
+    dB, dC = torch.full_like(B, 5.0), torch.full_like(B, 5.0)
+    ins = [(lm._GY, x), (lm._X, x), (lm._DT, x), (lm._A, rate), (lm._B, B), (lm._C, B), (lm._OFF, off),
+           (lm._SAVED, lm._new_saved(x, rate, off))]
+    lm._call(A.LM_SCAN_BWD, ins, [(lm._DX, x.clone()), (lm._DDT, x.clone()), (lm._DA, rate.clone()), (lm._DB, dB), (lm._DC, dC)])
+    assert bool((dB == 0).all()) and bool((dC == 0).all())
+    got = lm.selective_scan_backward(x, x, x, rate, B, B, offsets=off)
+    assert got.dx.shape == x.shape and bool((got.dB == 0).all()) and bool((got.dC == 0).all())
+    out = lm.selective_scan(x, x, rate, B, B, offsets=off, return_state=True)
+    assert out.y.shape == x.shape and out.state.shape == (len(lens) if lens else N, 0, S)
