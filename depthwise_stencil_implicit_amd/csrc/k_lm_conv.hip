@@ -34,22 +34,46 @@ struct ConvP {
     const int32_t *off, *rows;
     S3 xs, ys, s0s, s1s, gys, gss, dxs, dss;
     int64_t ws_c, ws_k, bs;
-    int64_t seqs, C, L, chunk, chunks, cvs, state_rows;
-    int silu, w_dense;
+    int64_t seqs, C, L, chunk, chunks, parts, cvs, state_rows;
+    int silu, w_dense, slots;
 };
 
-// Thread -> (sequence, chunk, first channel).  Neighbouring threads take
-// neighbouring channels; the last group of V is moved back inside C and
-// repeats its neighbour's results.
-template <int V> __device__ __forceinline__ bool conv_item(const ConvP &p, int64_t &seq, int64_t &ch, int64_t &c)
+// Where a thread works: chunk ch of sequence seq, which is chunk `part` of all,
+// and the first channel.  Neighbouring threads take neighbouring channels; the
+// last group of V is moved back inside C and repeats its neighbour's results.
+// ch is -1 at a place between packed sequences that no chunk has.
+struct ConvAt {
+    int64_t seq, ch, c, part;
+    SeqSpan sp;
+};
+template <int V> __device__ __forceinline__ bool conv_item(const ConvP &p, ConvAt &a)
 {
     const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (item >= p.cvs * p.chunks * p.seqs) return false;
-    const int64_t r = divide(item, p.cvs, c);
-    c *= V;
-    if (c > p.C - V) c = p.C - V;
-    seq = divide(r, p.chunks, ch);
-    return true;
+    a.part = divide(item, p.cvs, a.c);
+    if (!p.slots && a.part >= p.parts) return false;
+    if (__builtin_expect(p.slots, 0)) {
+        // The first lane's sequence by the whole wave, then on to the lane's own.
+        const int part = (int)a.part;
+        int seq, first;
+        a.sp = seq_of_slot(p.off, (int)p.seqs, (int)p.L, (uint32_t)p.chunk, __builtin_amdgcn_readfirstlane(part), seq, first);
+        while (seq + 1 < p.seqs && a.sp.start + a.sp.len < (part - seq) * p.chunk) {
+            a.sp = seq_span(p.off, ++seq, p.L);
+            first = (int)((uint32_t)a.sp.start / (uint32_t)p.chunk) + seq;
+        }
+        a.seq = seq, a.ch = part - first;
+        if (a.ch * p.chunk >= a.sp.len && a.ch > 0) a.ch = -1;
+    } else {
+        a.seq = divide(a.part, p.chunks, a.ch);
+        a.sp = seq_span(p.off, a.seq, p.L);
+    }
+    a.c *= V;
+    if (a.c > p.C - V) a.c = p.C - V;
+    return a.part < p.parts;
+}
+__device__ __forceinline__ int64_t chunk_end(const ConvP &p, const ConvAt &a)
+{
+    const int64_t end = (a.ch + 1) * p.chunk;
+    return end < a.sp.len ? end : a.sp.len;
 }
 
 template <typename T, int V> __device__ __forceinline__ void get(const T *p, int64_t cs, float (&o)[V])
@@ -127,12 +151,10 @@ __device__ __forceinline__ void get_front(const ConvP &p, int64_t seq, const T *
 
 template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_fwd(const ConvP p)
 {
-    int64_t seq, ch, c;
-    if (!conv_item<V>(p, seq, ch, c)) return;
-    const SeqSpan sp = seq_span(p.off, seq, p.L);
-    const int64_t t0 = ch * p.chunk;
-    if (t0 >= sp.len && ch > 0) return;
-    const int64_t t1 = ch == p.chunks - 1 ? sp.len : (t0 + p.chunk < sp.len ? t0 + p.chunk : sp.len);
+    ConvAt at;
+    if (!conv_item<V>(p, at) || at.ch < 0) return;
+    const SeqSpan sp = at.sp;
+    const int64_t seq = at.seq, c = at.c, t0 = at.ch * p.chunk, t1 = chunk_end(p, at);
     const T *x0 = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
     const T *x = x0 + t0 * p.xs.l;
     T *y = static_cast<T *>(p.y) + sp.row0 * p.ys.n + c * p.ys.c + (sp.start + t0) * p.ys.l;
@@ -184,8 +206,9 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
 // One token for each batch row; the state row moves up by one in place.
 template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_step(const ConvP p)
 {
-    int64_t n, ch, c;
-    if (!conv_item<V>(p, n, ch, c)) return;
+    ConvAt at;
+    if (!conv_item<V>(p, at)) return;
+    const int64_t n = at.seq, c = at.c;
     T *y = static_cast<T *>(p.y) + n * p.ys.n + c * p.ys.c;
     int64_t row = n;
     if (p.rows) {
@@ -227,111 +250,115 @@ template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_
 // recomputed from x, g = gy act'(p) joins the K-1 rows of g before the block,
 // dx leaves K-1 rows behind it, and dw, db gather over the chunk's own rows.
 // The walk runs K-1 rows past the chunk for dx (their dw belongs to the next
-// chunk).  The sums of a chunk go to part [seq * chunks + chunk][C][K+1];
+// chunk).  The sums of a chunk go to part [number of the chunk][C][K+1];
 // conv_bwd_sums adds them in a fixed order.
 template <typename T, int K, int V> __global__ __launch_bounds__(256) void conv_bwd(const ConvP p)
 {
     constexpr int R = kRowsBwd;
-    int64_t seq, ch, c;
-    if (!conv_item<V>(p, seq, ch, c)) return;
-    const SeqSpan sp = seq_span(p.off, seq, p.L);
-    const int64_t t0 = ch * p.chunk;
-    float dw[K][V] = {}, db[V] = {};
-    if (t0 < sp.len || ch == 0) {
-        const int64_t t1 = ch == p.chunks - 1 ? sp.len : (t0 + p.chunk < sp.len ? t0 + p.chunk : sp.len);
-        const T *x0 = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
-        const T *x = x0 + t0 * p.xs.l;
-        const T *gy = static_cast<const T *>(p.gy) + sp.row0 * p.gys.n + c * p.gys.c + (sp.start + t0) * p.gys.l;
-        // Where the row of the gradient that the block's first row completes goes.
-        T *dx = p.dx ? static_cast<T *>(p.dx) + sp.row0 * p.dxs.n + c * p.dxs.c + (sp.start + t0 - (K - 1)) * p.dxs.l : nullptr;
-        const int64_t end = t1 + (K - 1);                       // rows walked
-        const int64_t has = end < sp.len ? end : sp.len;        // rows that exist
-        Raw<T, V> nx[R], ng[R];
-        if (has > 0) get_rows(x, p.xs.l, t0, has - 1, nx), get_rows(gy, p.gys.l, t0, has - 1, ng);
-        float w[K][V], b[V];
-        get_weights<T, K, V>(p, c, w, b);
-        float h[K - 1 + R][V], g[K - 1 + R][V];   // the K-1 rows in front of the block, then the block
+    ConvAt at;
+    if (!conv_item<V>(p, at)) return;
+    float *part = p.part ? p.part + (at.part * p.C + at.c) * (K + 1) : nullptr;
+    if (at.ch < 0) {
+        if (part) {
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) {
-            get_front<T, K, V>(p, seq, x0, c, t0 - (K - 1) + k, h[k]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) g[k][i] = 0.f;
+            for (int i = 0; i < V * (K + 1); ++i) part[i] = 0.f;
         }
-        for (int64_t t = t0; t < end; t += R) {
+        return;
+    }
+    const SeqSpan sp = at.sp;
+    const int64_t seq = at.seq, ch = at.ch, c = at.c, t0 = ch * p.chunk, t1 = chunk_end(p, at);
+    float dw[K][V] = {}, db[V] = {};
+    const T *x0 = static_cast<const T *>(p.x) + sp.row0 * p.xs.n + c * p.xs.c + sp.start * p.xs.l;
+    const T *x = x0 + t0 * p.xs.l;
+    const T *gy = static_cast<const T *>(p.gy) + sp.row0 * p.gys.n + c * p.gys.c + (sp.start + t0) * p.gys.l;
+    // Where the row of the gradient that the block's first row completes goes.
+    T *dx = p.dx ? static_cast<T *>(p.dx) + sp.row0 * p.dxs.n + c * p.dxs.c + (sp.start + t0 - (K - 1)) * p.dxs.l : nullptr;
+    const int64_t end = t1 + (K - 1);                       // rows walked
+    const int64_t has = end < sp.len ? end : sp.len;        // rows that exist
+    Raw<T, V> nx[R], ng[R];
+    if (has > 0) get_rows(x, p.xs.l, t0, has - 1, nx), get_rows(gy, p.gys.l, t0, has - 1, ng);
+    float w[K][V], b[V];
+    get_weights<T, K, V>(p, c, w, b);
+    float h[K - 1 + R][V], g[K - 1 + R][V];   // the K-1 rows in front of the block, then the block
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+    for (int k = 0; k < K - 1; ++k) {
+        get_front<T, K, V>(p, seq, x0, c, t0 - (K - 1) + k, h[k]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) h[K - 1 + r][i] = nx[r].f(i), g[K - 1 + r][i] = ng[r].f(i);
-            if (has > 0) {
-                x += R * p.xs.l, gy += R * p.gys.l;
-                get_rows(x, p.xs.l, t + R, has - 1, nx), get_rows(gy, p.gys.l, t + R, has - 1, ng);
-            }
-            // MASK: rows past the chunk's end, at most in its last blocks.
-            const auto gather = [&](auto masked) {
-                constexpr bool MASK = decltype(masked)::value;
+        for (int i = 0; i < V; ++i) g[k][i] = 0.f;
+    }
+    for (int64_t t = t0; t < end; t += R) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float v = g[K - 1 + r][i];
-                        if (p.silu) {
-                            float a = b[i];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[r + k][i], a);
-                            v *= silu_slope(a, sigmoid(a));
-                        }
-                        if (MASK && t + r >= has) v = 0.f;
-                        g[K - 1 + r][i] = v;
-                        if (MASK && t + r >= t1) continue;
-                        db[i] += v;
-#pragma unroll
-                        for (int k = 0; k < K; ++k) dw[k][i] = __builtin_fmaf(v, h[r + k][i], dw[k][i]);
-                    }
-                }
-            };
-            if (t + R <= t1) gather(std::false_type());
-            else gather(std::true_type());
+            for (int i = 0; i < V; ++i) h[K - 1 + r][i] = nx[r].f(i), g[K - 1 + r][i] = ng[r].f(i);
+        if (has > 0) {
+            x += R * p.xs.l, gy += R * p.gys.l;
+            get_rows(x, p.xs.l, t + R, has - 1, nx), get_rows(gy, p.gys.l, t + R, has - 1, ng);
+        }
+        // MASK: rows past the chunk's end, at most in its last blocks.
+        const auto gather = [&](auto masked) {
+            constexpr bool MASK = decltype(masked)::value;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int64_t to = t + r - (K - 1);   // the row whose gradient is complete
-                if (to >= t1) break;
-                if (to < t0 && !(ch == 0 && to < 0)) continue;
-                float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    o[i] = 0.f;
+                    float v = g[K - 1 + r][i];
+                    if (p.silu) {
+                        float a = b[i];
 #pragma unroll
-                    for (int k = 0; k < K; ++k) o[i] = __builtin_fmaf(w[k][i], g[K - 1 + r - k][i], o[i]);
-                }
-                if (p.gs && to >= sp.len - (K - 1)) {
-                    float v[V];
-                    get_strided<T, V>(static_cast<const T *>(p.gs) + seq * p.gss.n + c * p.gss.c +
-                                          (to - (sp.len - (K - 1))) * p.gss.l,
-                                      p.gss.c, v);
+                        for (int k = 0; k < K; ++k) a = __builtin_fmaf(w[k][i], h[r + k][i], a);
+                        v *= silu_slope(a, sigmoid(a));
+                    }
+                    if (MASK && t + r >= has) v = 0.f;
+                    g[K - 1 + r][i] = v;
+                    if (MASK && t + r >= t1) continue;
+                    db[i] += v;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] += v[i];
-                }
-                if (to >= 0) {
-                    if (dx) put<T, V>(dx + r * p.dxs.l, p.dxs.c, o);
-                } else if (p.ds) {
-                    put_strided<T, V>(static_cast<T *>(p.ds) + seq * p.dss.n + c * p.dss.c + (K - 1 + to) * p.dss.l,
-                                      p.dss.c, o);
+                    for (int k = 0; k < K; ++k) dw[k][i] = __builtin_fmaf(v, h[r + k][i], dw[k][i]);
                 }
             }
-            if (dx) dx += R * p.dxs.l;
+        };
+        if (t + R <= t1) gather(std::false_type());
+        else gather(std::true_type());
 #pragma unroll
-            for (int k = 0; k < K - 1; ++k)
+        for (int r = 0; r < R; ++r) {
+            const int64_t to = t + r - (K - 1);   // the row whose gradient is complete
+            if (to >= t1) break;
+            if (to < t0 && !(ch == 0 && to < 0)) continue;
+            float o[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) h[k][i] = h[R + k][i], g[k][i] = g[R + k][i];
+            for (int i = 0; i < V; ++i) {
+                o[i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) o[i] = __builtin_fmaf(w[k][i], g[K - 1 + r - k][i], o[i]);
+            }
+            if (p.gs && to >= sp.len - (K - 1)) {
+                float v[V];
+                get_strided<T, V>(static_cast<const T *>(p.gs) + seq * p.gss.n + c * p.gss.c +
+                                      (to - (sp.len - (K - 1))) * p.gss.l,
+                                  p.gss.c, v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] += v[i];
+            }
+            if (to >= 0) {
+                if (dx) put<T, V>(dx + r * p.dxs.l, p.dxs.c, o);
+            } else if (p.ds) {
+                put_strided<T, V>(static_cast<T *>(p.ds) + seq * p.dss.n + c * p.dss.c + (K - 1 + to) * p.dss.l,
+                                  p.dss.c, o);
+            }
         }
+        if (dx) dx += R * p.dxs.l;
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[k][i] = h[R + k][i], g[k][i] = g[R + k][i];
     }
-    if (p.part) {
-        float *o = p.part + ((seq * p.chunks + ch) * p.C + c) * (K + 1);
+    if (part) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) o[i * (K + 1) + k] = dw[k][i];
-            o[i * (K + 1) + K] = db[i];
+            for (int k = 0; k < K; ++k) part[i * (K + 1) + k] = dw[k][i];
+            part[i * (K + 1) + K] = db[i];
         }
     }
 }
@@ -380,7 +407,9 @@ ConvP base(const lm_plan_t &p, lm_ptrs q)
     a.xs = s3(p.t[LM_X]), a.ys = s3(p.t[LM_Y]), a.s0s = s3(p.t[LM_STATE_IN]), a.s1s = s3(p.t[LM_STATE_OUT]);
     a.gys = s3(p.t[LM_GY]), a.gss = s3(p.t[LM_GSTATE]), a.dxs = s3(p.t[LM_DX]), a.dss = s3(p.t[LM_DSTATE]);
     a.ws_c = p.t[LM_W].strides[0], a.ws_k = p.t[LM_W].strides[1], a.bs = p.t[LM_BIAS].strides[0];
-    a.seqs = p.seqs, a.C = p.C, a.L = p.L, a.chunk = p.chunk, a.chunks = p.chunks;
+    a.seqs = p.seqs, a.C = p.C, a.L = p.L, a.chunk = p.chunk, a.chunks = p.chunks, a.parts = lm_parts(p);
+    a.slots = lm_slots(p);
+    if (p.chunks == 1) a.chunk = int64_t(1) << 62;   // whole sequences, also longer ones than expected
     a.state_rows = p.t[LM_STATE_OUT].sizes[0];
     a.silu = (p.args.flags & LM_SILU) != 0;
     a.w_dense = a.ws_c == p.K && (a.ws_k == 1 || p.K == 1);
@@ -390,7 +419,7 @@ ConvP base(const lm_plan_t &p, lm_ptrs q)
 int blocks_of(ConvP &a, int V)
 {
     a.cvs = lm_cdiv(a.C, V);
-    return (int)lm_cdiv(a.cvs * a.chunks * a.seqs, 256);
+    return (int)lm_cdiv(a.cvs * a.parts, 256);
 }
 
 // f(k) for the tap count as a constant.
@@ -458,7 +487,7 @@ template <typename T> void bwd(const lm_plan_t &p, ConvP a, lm_ptrs q, hipStream
     if (q[LM_DW] || q[LM_DBIAS]) {
         const conv_tensor &w = p.t[LM_DW], &b = p.t[LM_DBIAS];
         conv_bwd_sums<T><<<(int)lm_cdiv(p.C * (p.K + 1), 64), 1024, 0, s>>>(
-            a.part, p.seqs * p.chunks, p.C, (int)p.K, static_cast<T *>(q[LM_DW]), w.strides[0], w.strides[1],
+            a.part, a.parts, p.C, (int)p.K, static_cast<T *>(q[LM_DW]), w.strides[0], w.strides[1],
             static_cast<T *>(q[LM_DBIAS]), b.strides[0]);
     }
 }

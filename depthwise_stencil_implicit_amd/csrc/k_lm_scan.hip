@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256 * QW + kStage, DENSE && QW == 1 ? 4 : QW + 1) v
 {
     constexpr int W = 4 * QW * NS, CK = ScanShape{NS, QW}.save_steps();
     __shared__ FwdLds<NS, QW, PRE> sh;
-    const ScanAt at = scan_at(p, PRE ? p.chunks - 1 : p.chunks);
+    const ScanAt at = scan_at(p, PRE ? p.chunks - 1 : p.chunks, p.chunks - 1);
     if (PRE ? at.t0 + p.chunk >= at.sp.len : (at.t0 >= at.sp.len && at.ch > 0)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= 4 * QW) {
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256 * QW + kStage, DENSE && QW == 1 ? 4 : QW + 1) v
         A2[i] = real && q * NS + i < p.S ? rate(p.A[cc * p.A_c + (q * NS + i) * p.A_s]) : 0.f, h[i] = 0.f;
     if (!PRE && real) {
         if (p.s0) get_states<NS>(p.s0, p.s0s, at.seq, cc, q * NS, p.S, h);
-        fold_chunks<NS, W>(p, at.seq * (p.chunks - 1), 1, at.ch, cc, q * NS, A2, h);
+        fold_chunks<NS, W>(p, at.first, 1, at.ch, cc, q * NS, A2, h);
     }
     float *saved = !PRE && p.saved && real
                        ? p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * W + q * NS : nullptr;
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256 * QW + kStage, DENSE && QW == 1 ? 4 : QW + 1) v
     }
     if (!real) return;
     if (PRE) {
-        const int64_t k = (at.seq * (p.chunks - 1) + at.ch) * p.C + cc;
+        const int64_t k = (at.first + at.ch) * p.C + cc;
 #pragma unroll
         for (int i = 0; i < NS; ++i) p.carry_h[k * W + q * NS + i] = h[i];
         if (q == 0) p.carry_d[k] = sum_d;
@@ -270,8 +270,8 @@ int launch_lm_scan(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     if (a.seqs == 0) return CONV_OK;
     const bool dense = scan_dense(p, a, 8, scan_shape(p.S).width() / 4);
     a.carry_d = static_cast<float *>(ws);
-    a.carry_h = a.carry_d + lm_cdiv(a.seqs * (a.chunks - 1) * a.C, 4) * 4;
-    const int pre = (int)(a.seqs * (a.chunks - 1) * a.blocks), grid = (int)(a.seqs * a.chunks * a.blocks);
+    a.carry_h = a.carry_d + lm_cdiv(scan_carries(p) * a.C, 4) * 4;
+    const int pre = (int)(scan_carries(p) * a.blocks), grid = (int)(lm_parts(p) * a.blocks);
     with_type(p.dtype, [&](auto t) {
         with_ns(p.S, [&](auto n, auto w) {
             typedef decltype(t) T;

@@ -188,7 +188,7 @@ __device__ __forceinline__ void bwd_stage(const ScanP &p, const ScanAt &at, BwdL
     if constexpr (!PRE) {
         // Sums of D's and the bias's gradients over the rows of the staging waves.
         float(*sum)[kRow] = sh.o[0][0][0];
-        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (W + 2);
+        float *pc = p.part_c + (at.part * p.C + at.c0) * (W + 2);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             lds_sync();
@@ -211,8 +211,12 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
 {
     constexpr int W = 4 * QW * NS, CK = ScanShape{NS, QW}.save_steps(), TB = bwd_tile(W), PARTS = TB / CK;
     __shared__ BwdLds<NS, QW, PRE> sh;
-    const ScanAt at = scan_at(p, p.chunks);
-    if (at.t0 >= at.sp.len && at.ch > 0) return;
+    const ScanAt at = scan_at(p, p.chunks, p.chunks);
+    if (at.t0 >= at.sp.len && at.ch > 0) {
+        if (!PRE)   // a place without a chunk adds nothing to the sums
+            for (int e = threadIdx.x; e < at.nc * (W + 2); e += blockDim.x) p.part_c[(at.part * p.C + at.c0) * (W + 2) + e] = 0.f;
+        return;
+    }
     if (PRE && at.ch == 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= 4 * QW) {
@@ -230,9 +234,8 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
         A2[i] = real && q * NS + i < p.S ? rate(p.A[cc * p.A_c + (q * NS + i) * p.A_s]) : 0.f;
     if (!PRE && real) {
         if (p.gs) get_states<NS>(p.gs, p.gss, at.seq, cc, q * NS, p.S, r);
-        int64_t rest, last = at.sp.len > 0 ? divide(at.sp.len - 1, p.chunk, rest) : 0;
-        if (last > p.chunks - 1) last = p.chunks - 1;
-        if (last > at.ch) fold_chunks<NS, W>(p, at.seq * p.chunks + last, -1, last - at.ch, cc, q * NS, A2, r);
+        const int64_t last = p.chunks == 1 ? 0 : chunks_of(at.sp.len, p.chunk) - 1;
+        if (last > at.ch) fold_chunks<NS, W>(p, at.first + last, -1, last - at.ch, cc, q * NS, A2, r);
     }
     const float *saved = p.saved + ((saved_at<CK>(p, at) + at.t0 / CK) * p.C + cc) * W + q * NS;
     float sum_d = 0.f;
@@ -359,7 +362,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
     }
     if constexpr (PRE) {
         if (!real) return;
-        const int64_t k = (at.seq * p.chunks + at.ch) * p.C + cc;
+        const int64_t k = (at.first + at.ch) * p.C + cc;
 #pragma unroll
         for (int i = 0; i < NS; ++i) p.carry_h[k * W + q * NS + i] = r[i];
         if (q == 0) p.carry_d[k] = sum_d;
@@ -369,7 +372,7 @@ __global__ __launch_bounds__(256 * QW + kStage) void scan_bwd(const ScanP p)
         if (!real) return;
         if (p.ds && at.ch == 0) put_states<NS>(p.ds, p.dss, at.seq, cc, q * NS, p.S, r);
         // Parts of dA (4 NS per channel), dD and the bias, laid out [part][channel][4 NS + 2].
-        float *pc = p.part_c + ((at.seq * p.chunks + at.ch) * p.C + at.c0) * (W + 2);
+        float *pc = p.part_c + (at.part * p.C + at.c0) * (W + 2);
 #pragma unroll
         for (int i = 0; i < NS; ++i) pc[c * (W + 2) + q * NS + i] = dA[i];
     }
@@ -399,19 +402,14 @@ __global__ __launch_bounds__(256) void scan_bwd_bc(const float *part, int64_t ro
     else dC[n * cs.n + g * cs.g + s * cs.s + l * cs.l] = v;
 }
 
-// dA, dD and the bias's gradient: the parts of all sequences and chunks.  A
-// part of an empty chunk was never written and is left out.
+// dA, dD and the bias's gradient: the parts of all sequences and chunks.
 __global__ __launch_bounds__(256) void scan_bwd_c(const ScanP p, int W, float *dA, int64_t a_c, int64_t a_s, float *dD,
                                                   int64_t d_s, float *db, int64_t b_s)
 {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, n = p.C * (W + 2);
     if (e >= n) return;
     float v = 0.f;
-    for (int64_t seq = 0; seq < p.seqs; ++seq) {
-        const SeqSpan sp = seq_span(p.off, seq, p.L);
-        for (int64_t ch = 0; ch < p.chunks && (ch == 0 || ch * p.chunk < sp.len); ++ch)
-            v += p.part_c[(seq * p.chunks + ch) * n + e];
-    }
+    for (int64_t k = 0; k < p.parts; ++k) v += p.part_c[k * n + e];
     int64_t j;
     const int64_t c = divide(e, W + 2, j);
     if (j < p.S) dA[c * a_c + j * a_s] = v;
@@ -427,11 +425,11 @@ int launch_lm_scan_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     const int W = scan_shape(p.S).width(), TB = bwd_tile(W);
     float *f = static_cast<float *>(ws);
     a.part_bc = f, f += a.blocks * a.rows_total * 2 * W;
-    a.part_c = f, f += lm_cdiv(a.seqs * a.chunks * a.C * (W + 2), 4) * 4;
-    a.carry_d = f, f += lm_cdiv(a.seqs * a.chunks * a.C, 4) * 4;
+    a.part_c = f, f += lm_cdiv(lm_parts(p) * a.C * (W + 2), 4) * 4;
+    a.carry_d = f, f += lm_cdiv(lm_parts(p) * a.C, 4) * 4;
     a.carry_h = f;
     const bool dense = scan_dense(p, a, TB / 4, TB * W / 128);
-    const int grid = (int)(a.seqs * a.chunks * a.blocks);
+    const int grid = (int)(lm_parts(p) * a.blocks);
     with_type(p.dtype, [&](auto t) {
         typedef decltype(t) T;
         with_ns(p.S, [&](auto n, auto w) {

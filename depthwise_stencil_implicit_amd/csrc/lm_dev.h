@@ -31,6 +31,43 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t &rest)
     return q;
 }
 
+// The sequence whose chunks, numbered start / chunk + sequence on, reach
+// `slot` -- the last one with start < (slot - seq + 1) chunk -- and its rows; the
+// first one where none does.  first: the number of its first chunk.  For a whole
+// wave and one slot.  64 sequences are tested at a time and the found one's rows
+// taken from the lane that tested it, so up to 64 sequences cost the one load
+// that its rows alone would.  All numbers are below 2^31 here, and a wave that
+// starts waits for each of these operations.
+__device__ __forceinline__ SeqSpan seq_of_slot(const int32_t *offsets, int seqs, int L, uint32_t chunk, int slot, int &seq,
+                                               int &first)
+{
+    const int lane = threadIdx.x & 63;
+    const auto row = [&](int v) { return v < 0 ? 0 : (v > L ? L : v); };
+    seq = 0;
+    for (int n = seqs;;) {
+        const int by = (n + 63) >> 6, k = lane * by, s = seq + k;
+        int a = 0, b = 0;
+        bool in = k < n;
+        if (in) a = offsets[s], b = offsets[s + 1];
+        in = in && s <= slot && (uint64_t)(uint32_t)(slot - s + 1) * chunk > (uint32_t)row(a);
+        const uint64_t all = __ballot(in);
+        const int last = all ? __builtin_popcountll(all) - 1 : 0;
+        seq += last * by, n -= last * by;
+        if (by <= 1 || !all) {
+            const int start = row(__builtin_amdgcn_readlane(a, last)), end = row(__builtin_amdgcn_readlane(b, last));
+            first = (int)((uint32_t)start / chunk) + seq;
+            return {0, start, end > start ? end - start : 0};
+        }
+        if (n > by) n = by;
+    }
+}
+// Chunks of a sequence of this length; one, to take the state on, of an empty one.
+__device__ __forceinline__ int64_t chunks_of(int64_t len, int64_t chunk)
+{
+    int64_t rest;
+    return len > 0 ? divide(len - 1, chunk, rest) + 1 : 1;
+}
+
 // exp2, log2 and reciprocal of the hardware (1 ulp).  The compiler's exp2f
 // would add a rescaling for subnormal results, which here are factors that
 // vanish against the rest of a sum.

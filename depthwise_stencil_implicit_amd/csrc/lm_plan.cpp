@@ -302,7 +302,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
     if (conv) {
         if (!step) conv_chunks(p, max_len, bwd ? 2 : 16 / e, bwd ? 32 : 8);
         else p.chunk = p.chunks = 1;
-        if (bwd && (k.has(LM_DW) || k.has(LM_DBIAS))) p.workspace_bytes = p.seqs * p.chunks * p.C * (p.K + 1) * 4;
+        if (bwd && (k.has(LM_DW) || k.has(LM_DBIAS))) p.workspace_bytes = lm_parts(p) * p.C * (p.K + 1) * 4;
         const int64_t st = p.seqs * p.C * (p.K - 1) * e * ((k.has(LM_STATE_IN) || step) + k.has(LM_STATE_OUT) + k.has(LM_GSTATE) + k.has(LM_DSTATE));
         const int64_t act = args->flags & LM_SILU ? 4 : 0;
         p.bytes = cells * e * (bwd ? 2 + k.has(LM_DX) : 2) + st + (bwd ? 2 : 1) * p.C * (p.K + k.has(LM_BIAS)) * e;
@@ -316,17 +316,18 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
         if (k.status == CONV_OK && k.has(LM_SAVED) && t[LM_SAVED].strides[0] != 1 && p.saved_floats > 1) k.fail(CONV_EINVAL, "saved has to be contiguous");
         if (k.status != CONV_OK) return k.status;
         const int64_t blocks = p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH);
-        if (op == LM_SCAN) p.workspace_bytes = 4 * (lm_cdiv(p.seqs * (p.chunks - 1) * p.C, 4) * 4 + p.seqs * (p.chunks - 1) * p.C * W);
+        const int64_t parts = lm_parts(p), carries = scan_carries(p);
+        if (op == LM_SCAN) p.workspace_bytes = 4 * (lm_cdiv(carries * p.C, 4) * 4 + carries * p.C * W);
         if (op == LM_SCAN_BWD)
-            p.workspace_bytes = 4 * (blocks * N * p.L * 2 * W + lm_cdiv(p.seqs * p.chunks * p.C * (W + 2), 4) * 4 +
-                                     lm_cdiv(p.seqs * p.chunks * p.C, 4) * 4 + p.seqs * p.chunks * p.C * W);
+            p.workspace_bytes = 4 * (blocks * N * p.L * 2 * W + lm_cdiv(parts * p.C * (W + 2), 4) * 4 + lm_cdiv(parts * p.C, 4) * 4 +
+                                     parts * p.C * W);
         const int64_t io = 3 + k.has(LM_Z), bc = 2 * p.G * p.S * rows * e;
         p.bytes = cells * e * (bwd ? 2 * io : io) + (bwd ? 2 : 1) * (bc + p.C * (p.S + k.has(LM_D) + k.has(LM_DT_BIAS)) * 4) +
                   p.seqs * p.C * p.S * 4 * (k.has(LM_STATE_IN) + (step ? 2 : k.has(LM_STATE_OUT)) + k.has(LM_GSTATE) + k.has(LM_DSTATE));
         p.flops = cells * (bwd ? 20 * p.S + 40 : 7 * p.S + 16);
     }
     // Every launch has at most 2^31 - 1 workgroups.
-    const int64_t units = std::max<int64_t>(p.seqs, 1) * std::max<int64_t>(p.chunks, 1);
+    const int64_t units = std::max<int64_t>(lm_parts(p), 1);
     const int64_t per = conv ? lm_cdiv(p.C, 64) : std::max<int64_t>(p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH), lm_cdiv(p.C, 64));
     if (units > 0x7fffffff / std::max<int64_t>(per, 1) || (!conv && rows > 0x7fffffffll * 256 / (8 * LM_MAX_STATES * p.G))) {
         k.fail(CONV_EUNSUPPORTED, "too many rows for one launch");

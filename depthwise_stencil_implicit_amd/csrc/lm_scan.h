@@ -36,15 +36,15 @@ struct ScanP {
     const float *A, *D, *bias, *s0, *gs;
     void *y, *dx, *ddt, *dz;
     float *s1, *saved, *ds;
-    float *carry_h, *carry_d;        // per (sequence, chunk): state or gradient leaving it, sum of d
+    float *carry_h, *carry_d;        // per chunk: state or gradient leaving it, sum of d
     float *part_bc, *part_c;         // backward sums of a workgroup
     const int32_t *off, *rows;
     S3 xs, dts, zs, ys, gys, dxs, ddts, dzs;
     S4 Bs, Cs;
     S3 s0s, s1s, gss, dss;           // (sequence, channel, state)
     int64_t A_c, A_s, D_s, bias_s;
-    int64_t seqs, C, L, S, chunk, chunks, Cg, blocks_g, blocks, rows_total, state_rows;
-    int softplus, dense;
+    int64_t seqs, C, L, S, chunk, chunks, Cg, blocks_g, blocks, rows_total, parts, state_rows;
+    int softplus, dense, slots;
 };
 
 constexpr int kCH = LM_SCAN_CH;
@@ -114,24 +114,36 @@ template <int V> __device__ __forceinline__ void get_param(const float *p, int64
 // Where a workgroup stands.
 struct ScanAt {
     int64_t seq, ch, c0;     // sequence, chunk, first channel
+    int64_t first, part;     // numbers of the sequence's first chunk and of this one among all
     int g, nc;               // group, channels of this workgroup
     SeqSpan sp;
     int64_t t0, t1;          // its steps of the sequence
 };
-__device__ __forceinline__ ScanAt scan_at(const ScanP &p, int64_t chunks)
+// chunks: a sequence's workgroups of this launch per channel block; numbered: how
+// many of its chunks have a number.  A place between packed sequences gets a
+// chunk past its sequence's end.
+__device__ __forceinline__ ScanAt scan_at(const ScanP &p, int64_t chunks, int64_t numbered)
 {
     ScanAt a;
     // All of these are below 2^31.
     const uint32_t b = blockIdx.x, r = b / (uint32_t)p.blocks, cb = b - r * (uint32_t)p.blocks;
-    const uint32_t seq = r / (uint32_t)chunks;
-    a.seq = seq, a.ch = r - seq * (uint32_t)chunks;
+    a.part = r;
+    if (__builtin_expect(p.slots, 0)) {
+        int seq, first;
+        a.sp = seq_of_slot(p.off, (int)p.seqs, (int)p.L, (uint32_t)p.chunk, (int)r, seq, first);
+        a.seq = seq, a.first = first, a.ch = (int)r - first;
+        if (a.ch < 0) a.sp.len = 0, a.ch = 1;   // in front of the first sequence
+    } else {
+        const uint32_t seq = r / (uint32_t)chunks;
+        a.seq = seq, a.ch = r - seq * (uint32_t)chunks, a.first = seq * numbered;
+        a.sp = seq_span(p.off, a.seq, p.L);
+    }
     a.g = (int)(cb / (uint32_t)p.blocks_g);
     const int64_t in_g = (int64_t)(cb - a.g * (uint32_t)p.blocks_g) * kCH;
     a.c0 = a.g * p.Cg + in_g;
     a.nc = (int)(p.Cg - in_g < kCH ? p.Cg - in_g : kCH);
-    a.sp = seq_span(p.off, a.seq, p.L);
     a.t0 = a.ch * p.chunk;
-    a.t1 = a.ch == p.chunks - 1 || a.t0 + p.chunk > a.sp.len ? a.sp.len : a.t0 + p.chunk;
+    a.t1 = p.chunks == 1 || a.t0 + p.chunk > a.sp.len ? a.sp.len : a.t0 + p.chunk;
     return a;
 }
 
@@ -401,6 +413,7 @@ inline ScanP scan_params(const lm_plan_t &p, lm_ptrs q)
     a.blocks = a.blocks_g * p.G;
     a.rows_total = p.t[LM_X].sizes[0] * p.L;
     a.state_rows = p.t[LM_STATE_OUT].sizes[0];
+    a.parts = lm_parts(p), a.slots = lm_slots(p);
     a.softplus = (p.args.flags & LM_SOFTPLUS) != 0;
     return a;
 }

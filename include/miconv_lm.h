@@ -104,7 +104,8 @@ typedef struct lm_args {
     int32_t flags;
     int32_t reserved;
     int64_t max_len;   /* packed calls: a length that few sequences pass (0: T); it only
-                          decides how the work is split, results hold for any value */
+                          decides how the work is split, results hold for any value and the
+                          workspace follows T and the number of sequences */
     int64_t chunk;     /* 0: chosen; else rows per chunk of the long axis (rounded up as the kernel needs) */
 } lm_args;
 
@@ -116,7 +117,7 @@ typedef struct lm_plan_t {
     int64_t C, L;      /* channels (MV4: outputs), rows of one x row */
     int64_t K;         /* taps; MV4: columns */
     int64_t S, G;      /* states, groups; MV4: G = columns per scale */
-    int64_t chunk, chunks;       /* rows per chunk, chunks per sequence */
+    int64_t chunk, chunks;       /* rows per chunk, chunks per sequence (packed: of max_len rows) */
     int64_t saved_floats;        /* SCAN*: elements of LM_SAVED */
     int64_t workspace_bytes;
     int64_t flops, bytes;        /* algorithmic work of one call (packed calls: of T rows) */

@@ -136,3 +136,72 @@ def test_scan_gradients_without_channels(lens):
     assert got.dx.shape == x.shape and bool((got.dB == 0).all()) and bool((got.dC == 0).all())
     out = lm.selective_scan(x, x, rate, B, B, offsets=off, return_state=True)
     assert out.y.shape == x.shape and out.state.shape == (len(lens) if lens else N, 0, S)
+
+
+def lengths(g, n, total, most_empty=False):
+    """n lengths that add up to total, many of them zero with most_empty."""
+    cuts = torch.randint(0, total + 1, (n - 1,), generator=g).sort().values
+    if most_empty:
+        cuts = cuts[torch.randint(0, 4, (n - 1,), generator=g).sort().values] if n > 4 else cuts
+    return torch.cat([torch.zeros(1, dtype=torch.int64), cuts, torch.tensor([total])]).to(torch.int32)
+
+
+PACKED = [
+    # dtype, sequences, rows, channels, chunk, max_len, most of them empty
+    (F, 5, 130, 24, 32, None, False),
+    (BF, 13, 300, 1, 32, None, False),       # a wave spans many chunks
+    (F, 70, 400, 3, 32, None, True),         # more than one wave of sequences
+    (HF, 200, 260, 66, 32, 7, False),        # max_len far below the longest
+    (F, 4200, 4500, 2, 32, None, False),     # more than a wave of waves
+    (BF, 1, 200, 130, 64, None, False),
+    (F, 3, 96, 40, 32, 1, True),
+]
+
+
+def packed_case(i):
+    dt, n, t, c, chunk, max_len, empty = PACKED[i]
+    g = gen(700 + i)
+    off = lengths(g, n, t, empty)
+    rows = lambda *s: rnd(g, t, *s, dtype=dt).movedim(0, -1)[None]  # noqa: E731
+    return g, dt, n, t, c, off.cuda(), dict(offsets=off.cuda(), chunk=chunk, max_len=max_len), rows
+
+
+@pytest.mark.parametrize("i", range(len(PACKED)))
+def test_packed_convolutions_of_any_lengths(i):
+    """Chunks of unlike sequences beside each other, in one piece and in many;
+    every sequence, the empty ones too, hands its state on."""
+    g, dt, n, t, c, off, kw, rows = packed_case(i)
+    print(f"packed conv {PACKED[i]}", flush=True)
+    K = 4
+    x, gy, w, b = rows(c), rows(c), rnd(g, c, K, dtype=dt, scale=0.6), rnd(g, c, dtype=dt)
+    st, gs = rnd(g, n, c, K - 1, dtype=dt), rnd(g, n, c, K - 1, dtype=dt)
+    args = (x, w, b, "silu", st, off)
+    (y, last), (yb, _) = R.conv(*args), R.conv(*args, bound=True)
+    ref, bound = R.conv(*args, gy, gs), R.conv(*args, gy, gs, bound=True)
+    for chunk in (kw["chunk"], 3, None):
+        kw["chunk"] = chunk
+        got = lm.causal_conv(x, w, b, activation="silu", state=st, return_state=True, **kw)
+        back = lm.causal_conv_backward(gy, x, w, b, activation="silu", state=st, gstate=gs, **kw)
+        R.assert_close(got.y, y, yb, 2 * K + 64, "y")
+        assert torch.equal(got.state.cpu().double(), last)
+        for name, v, r, e in zip(("dx", "dw", "db", "dstate"), back, ref, bound):
+            R.assert_close(v, r, e, (t if name in ("dw", "db") else 0) + 4 * K + 64, name)
+
+
+@pytest.mark.parametrize("i", range(len(PACKED)))
+def test_packed_scans_of_any_lengths(i):
+    g, dt, n, t, c, off, kw, rows = packed_case(i)
+    print(f"packed scan {PACKED[i]}", flush=True)
+    S = 6
+    x, d, z, gy, B, Cm = rows(c), rows(c), rows(c), rows(c), rows(1, S), rows(1, S)
+    A, D, st, gs = -torch.exp(rnd(g, c, S, scale=0.5)), rnd(g, c), rnd(g, n, c, S), rnd(g, n, c, S)
+    par = dict(D=D, z=z, state=st)
+    got = lm.selective_scan(x, d, A, B, Cm, dt_softplus=True, return_state=True, **par, **kw)
+    o, b = (R.scan(x, d, A, B, Cm, softplus_dt=True, offsets=off, **par, bound=k) for k in (False, True))
+    n_f = 4 * t + 2 * S + 64
+    R.assert_close(got.state, o["state"], b["state"], n_f, "state")
+    R.assert_close(got.y, o["y"], b["y"], n_f, "y")
+    back = lm.selective_scan_backward(gy, x, d, A, B, Cm, dt_softplus=True, gstate=gs, **par, **kw)
+    o, b = (R.scan(x, d, A, B, Cm, softplus_dt=True, offsets=off, **par, gy=gy, gstate=gs, bound=k) for k in (False, True))
+    for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dstate"):
+        R.assert_close(getattr(back, k), o[k], b[k], 2 * n_f + (t if k in ("dA", "dD") else c), k)

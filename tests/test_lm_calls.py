@@ -143,3 +143,33 @@ def test_steps_by_name_refuse(calls):
     with pytest.raises(lm.ConvError, match="groups"):
         lm.matvec4(torch.zeros(1, 64), torch.zeros(5, 32, dtype=torch.uint8), torch.zeros(5, 3))
     assert not calls
+
+
+def packed(op, seqs, t, c, s=16, max_len=0):
+    """The plan of a packed call of bf16 rows, with nothing behind its descriptors."""
+    rows = lambda *v, d=BF: torch.empty(v, dtype=d, device="meta")  # noqa: E731
+    x, off = rows(1, c, t), rows(seqs + 1, d=torch.int32)
+    if op == A.LM_CONV_BWD:
+        w = rows(c, 4)
+        return lm._make_plan(op, {lm._X: x, lm._GY: x, lm._W: w, lm._BIAS: rows(c), lm._OFF: off, lm._DX: x, lm._DW: w, lm._DBIAS: rows(c)},
+                             max_len=max_len)
+    bc, a = rows(1, 1, s, t), rows(c, s, d=F)
+    ins = {lm._X: x, lm._DT: x, lm._A: a, lm._B: bc, lm._C: bc, lm._OFF: off}
+    if op == A.LM_SCAN:
+        return lm._make_plan(op, {**ins, lm._Y: x}, max_len=max_len)
+    ck, w = (16, 16) if s <= 16 else (8, 32)
+    saved = rows((t // ck + seqs + 1) * c * w, d=F)
+    return lm._make_plan(op, {**ins, lm._GY: x, lm._DX: x, lm._DDT: x, lm._DA: a, lm._DB: bc, lm._DC: bc, lm._SAVED: saved}, max_len=max_len)
+
+
+@pytest.mark.parametrize("op,seqs,t,c,max_len", [
+    (A.LM_CONV_BWD, 256, 16384, 4096, 0), (A.LM_CONV_BWD, 64, 65536, 4096, 32768), (A.LM_CONV_BWD, 1000, 65536, 1024, 65536),
+    (A.LM_SCAN, 256, 16384, 1024, 0), (A.LM_SCAN, 2000, 32768, 512, 30000), (A.LM_SCAN_BWD, 256, 16384, 1024, 0)])
+def test_packed_workspace_follows_the_rows(op, seqs, t, c, max_len):
+    """However long the longest sequence may be, all of them have at most
+    t / chunk + seqs chunks, and the workspace holds one part for each."""
+    p = packed(op, seqs, t, c, max_len=max_len)
+    places = t // p.chunk + seqs
+    per = {A.LM_CONV_BWD: 5, A.LM_SCAN: 17, A.LM_SCAN_BWD: 18 + 17}[op] * c * 4
+    whole = 4 * -(-c // 64) * t * 2 * 16 if op == A.LM_SCAN_BWD else 0   # dB and dC of each 64 channels
+    assert p.workspace_bytes <= whole + places * per + 64
