@@ -125,7 +125,7 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
 
 def _run(p: A.LmPlan, q, dev: int) -> None:
     """Launch on the device's current stream, which the workspace belongs to."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _run(p, q, dev)
     n = p.workspace_bytes
@@ -140,6 +140,11 @@ def _on_gpu(*tensors) -> None:
     for t in tensors:
         if not t.is_cuda:
             raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
+
+
+def _new(t) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _rows_like(n, c, l, ref):
@@ -190,12 +195,12 @@ def causal_conv_backward(gy, x, w, b=None, *, activation=None, state=None, offse
     shape, w = w.shape, _taps(w)
     _on_gpu(x)
     dx = torch.empty_like(x) if need_dx else None
-    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if need_dw else None
-    db = torch.empty(b.shape, dtype=b.dtype, device=b.device) if need_dw and b is not None else None
+    dw = _new(w) if need_dw else None
+    db = _new(b) if need_dw and b is not None else None
     ds = torch.empty_like(state) if state is not None else None
     _call(A.LM_CONV_BWD, [(_GY, gy), (_X, x), (_W, w), (_BIAS, b), (_S0, state), (_OFF, offsets), (_GS, gstate)],
           [(_DX, dx), (_DW, dw), (_DBIAS, db), (_DS, ds)], _act(activation), max_len, chunk)
-    return ConvGrads(dx, dw.view(shape) if dw is not None else None, db, ds)
+    return ConvGrads(dx, dw.view(shape) if dw is not None and len(shape) == 3 else dw, db, ds)
 
 
 class _Step:
@@ -252,7 +257,7 @@ def causal_conv_step(x, w, b, state, *, activation=None, rows=None) -> torch.Ten
     """One token: x [N, C], state [N, C, K-1] updated in place.  With ``rows``
     (int32 [N], distinct) batch row n uses state row rows[n]; a row outside
     the state is left out and its y is zero."""
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _new(x)
     _call(A.LM_CONV_STEP, [(_X, x), (_W, _taps(w)), (_BIAS, b), (_S1, state), (_ROWS, rows)], [(_Y, y)], _act(activation))
     return y
 
@@ -278,8 +283,7 @@ def selective_scan(x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus
     _on_gpu(x)
     y = torch.empty_like(x) if want_y else None
     # Their type is said: without it they would have torch's default one.
-    last = (torch.empty((_seqs(x, offsets), x.shape[1], A_.shape[-1]), dtype=torch.float32, device=x.device)
-            if return_state else None)
+    last = x.new_empty((_seqs(x, offsets), x.shape[1], A_.shape[-1]), dtype=torch.float32) if return_state else None
     saved = _new_saved(x, A_, offsets) if save else None
     _call(A.LM_SCAN,
           [(_X, x), (_DT, dt), (_A, A_), (_B, B), (_C, C), (_D, D), (_Z, z), (_DTB, dt_bias), (_S0, state), (_OFF, offsets)],
@@ -317,7 +321,8 @@ def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None
            (_GS, gstate), (_SAVED, saved)],
           [(_DX, dx), (_DDT, ddt), (_DA, dA), (_DB, dB), (_DC, dC), (_DD, dD), (_DZ, dz), (_DDTB, db), (_DS, ds)],
           A.LM_SOFTPLUS if dt_softplus else 0, max_len, chunk)
-    return ScanGrads(dx, ddt, dA, dB.view(b_shape), dC.view(c_shape), dD, dz, db, ds)
+    return ScanGrads(dx, ddt, dA, dB if len(b_shape) == 4 else dB.view(b_shape), dC if len(c_shape) == 4 else dC.view(c_shape), dD,
+                     dz, db, ds)
 
 
 class PreparedSelectiveScanStep(_Step):
@@ -348,7 +353,7 @@ def selective_scan_step(x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None,
                         rows=None) -> torch.Tensor:
     """One token: x, dt, z [N, C], B and C [N, G, S] (or [N, S]), state f32
     [N, C, S] updated in place; ``rows`` as in ``causal_conv_step``."""
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _new(x)
     _call(A.LM_SCAN_STEP, [(_X, x), (_DT, dt), (_A, A_), (_B, _grouped(B, 3)), (_C, _grouped(C, 3)), (_S1, state), (_D, D),
                            (_Z, z), (_DTB, dt_bias), (_ROWS, rows)], [(_Y, y)], A.LM_SOFTPLUS if dt_softplus else 0)
     return y
@@ -382,7 +387,7 @@ def matvec4(x, packed, scales, zeros=None, bias=None) -> torch.Tensor:
     few rows: 16 cost about what one does, more repeat the weights' pass.  A
     row whose sums pass f32's range at 256 times x gives infinities or NaN."""
     x2 = x.reshape(-1, x.shape[-1])
-    y = torch.empty((x2.shape[0], packed.shape[0]), dtype=x.dtype, device=x.device)
+    y = x2.new_empty((x2.shape[0], packed.shape[0]))
     _call(A.LM_MV4, [(_X, x2), (_W, packed), (_SCALES, scales), (_ZEROS, zeros), (_BIAS, bias)], [(_Y, y)])
     return y.view(x.shape[:-1] + (packed.shape[0],))
 
