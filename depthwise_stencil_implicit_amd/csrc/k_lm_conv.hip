@@ -440,7 +440,7 @@ template <typename F> void with_taps(int64_t K, F f)
 template <typename T> void fwd(const lm_plan_t &p, ConvP a, hipStream_t s)
 {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.xs.c == 1 && a.ys.c == 1 && a.C >= V;
+    const bool vec = conv_width(p) == V;
     with_taps(p.K, [&](auto k) {
         constexpr int K = decltype(k)::value;
         if (vec) {
@@ -457,10 +457,7 @@ template <typename T> void step(const lm_plan_t &p, ConvP a, hipStream_t s)
 {
     with_taps(p.K, [&](auto k) {
         constexpr int K = decltype(k)::value;
-        // Two channels per thread: enough threads for small batches.  An odd C
-        // takes one: the state moves in place, so no two threads may share a
-        // channel.
-        if (a.C % 2 == 0) {
+        if (conv_width(p) == 2) {
             const int g = blocks_of(a, 2);
             if (g) conv_step<T, K, 2><<<g, 256, 0, s>>>(a);
         } else {
@@ -473,7 +470,7 @@ template <typename T> void step(const lm_plan_t &p, ConvP a, hipStream_t s)
 template <typename T> void bwd(const lm_plan_t &p, ConvP a, lm_ptrs q, hipStream_t s)
 {
     constexpr int V = 2;
-    const bool vec = a.xs.c == 1 && a.gys.c == 1 && (!a.dx || a.dxs.c == 1) && a.C >= V;
+    const bool vec = conv_width(p) == V;
     with_taps(p.K, [&](auto k) {
         constexpr int K = decltype(k)::value;
         if (vec) {

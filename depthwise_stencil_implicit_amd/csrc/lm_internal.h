@@ -43,6 +43,18 @@ inline int64_t lm_parts(const lm_plan_t &p)
 {
     return lm_slots(p) ? (p.seqs > 0 ? p.L / p.chunk + p.seqs : 0) : p.seqs * p.chunks;
 }
+// Channels of a convolution's thread: 16 bytes of contiguous ones, or one.  The
+// backward walk's registers hold two.  A step takes two, enough threads for
+// small batches, but one of an odd number: the state moves in place, so no two
+// threads may share a channel.
+inline int conv_width(const lm_plan_t &p)
+{
+    if (p.op == LM_CONV_STEP) return p.C % 2 ? 1 : 2;
+    const int V = p.op == LM_CONV_BWD ? 2 : p.dtype == CONV_F32 ? 4 : 8;
+    for (int s : {LM_X, LM_Y, LM_GY, LM_DX})
+        if (p.t[s].rank && p.t[s].strides[1] != 1) return 1;
+    return p.C >= V ? V : 1;
+}
 // States (gradients) between the scan's chunks: the forward pass needs none of
 // a sequence's last one.
 inline int64_t scan_carries(const lm_plan_t &p)

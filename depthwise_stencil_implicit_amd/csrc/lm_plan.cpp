@@ -109,6 +109,37 @@ uint64_t allowed(int op)
     }
 }
 
+// A grid has fewer than 2^32 threads in each dimension.  The largest launch of
+// the call is looked at (in double: sizes may be any).
+bool one_launch(const lm_plan_t &p)
+{
+    const double C = (double)p.C, parts = (double)lm_parts(p);
+    double threads = 0;
+    const auto add = [&](double groups, double size) { threads = std::max(threads, std::ceil(groups) * size); };
+    switch (p.op) {
+    case LM_CONV: case LM_CONV_BWD: case LM_CONV_STEP:
+        add(std::ceil(C / conv_width(p)) * parts / 256, 256);
+        if (p.op == LM_CONV_BWD) add(C * (double)(p.K + 1) / 64, 1024);
+        break;
+    case LM_SCAN: case LM_SCAN_BWD: {
+        const ScanShape shape = scan_shape(p.S);
+        add(parts * (double)p.G * std::ceil(C / (double)p.G / LM_SCAN_CH), 256 * (shape.qw + 1));
+        if (p.op == LM_SCAN_BWD) {
+            add((double)p.t[LM_X].sizes[0] * (double)p.L * 2 * shape.width() * (double)p.G / 256, 256);
+            add(C * (shape.width() + 2) / 256, 256);
+        }
+        break;
+    }
+    case LM_SCAN_STEP: add((double)p.seqs * C * 4 / 256, 256); break;
+    case LM_MV4:
+        if (mv4_parts(p) == 0) add(C / 16, 512);
+        add(C / 256, 256), add((double)p.K / 256, 256);
+        if (lm_cdiv(p.seqs, 16) > 65535) return false;   // rows of x lie along the second dimension
+        break;
+    }
+    return threads < 4294967296.0 && parts < 2147483648.0;
+}
+
 // Rows per chunk and chunks per sequence of a convolution: the kernel's
 // threads own a few channels each, and 2^18 of them (four waves on every
 // SIMD) hide the memory's latency.  A chunk reads K-1 rows of its neighbour
@@ -218,8 +249,8 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
             k.fail(CONV_EUNSUPPORTED, "w needs contiguous rows a multiple of 16 bytes apart");
             return k.status;
         }
-        if (p.K > 0x7fffff00 || lm_cdiv(p.seqs, 16) > 65535 || lm_cdiv(p.C, 16) > 0x7fffffff) {
-            k.fail(CONV_EUNSUPPORTED, "too many rows");
+        if (p.K > 0x7fffff00 || !one_launch(p)) {
+            k.fail(CONV_EUNSUPPORTED, "too many rows for one launch");
             return k.status;
         }
         p.workspace_bytes = mv4_rows_bytes(p) + (mv4_parts(p) > 1 ? mv4_parts(p) * p.seqs * p.C * 4 : 0);
@@ -326,10 +357,7 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
                   p.seqs * p.C * p.S * 4 * (k.has(LM_STATE_IN) + (step ? 2 : k.has(LM_STATE_OUT)) + k.has(LM_GSTATE) + k.has(LM_DSTATE));
         p.flops = cells * (bwd ? 20 * p.S + 40 : 7 * p.S + 16);
     }
-    // Every launch has at most 2^31 - 1 workgroups.
-    const int64_t units = std::max<int64_t>(lm_parts(p), 1);
-    const int64_t per = conv ? lm_cdiv(p.C, 64) : std::max<int64_t>(p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH), lm_cdiv(p.C, 64));
-    if (units > 0x7fffffff / std::max<int64_t>(per, 1) || (!conv && rows > 0x7fffffffll * 256 / (8 * LM_MAX_STATES * p.G))) {
+    if (!one_launch(p)) {
         k.fail(CONV_EUNSUPPORTED, "too many rows for one launch");
         return k.status;
     }

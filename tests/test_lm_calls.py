@@ -173,3 +173,35 @@ def test_packed_workspace_follows_the_rows(op, seqs, t, c, max_len):
     per = {A.LM_CONV_BWD: 5, A.LM_SCAN: 17, A.LM_SCAN_BWD: 18 + 17}[op] * c * 4
     whole = 4 * -(-c // 64) * t * 2 * 16 if op == A.LM_SCAN_BWD else 0   # dB and dC of each 64 channels
     assert p.workspace_bytes <= whole + places * per + 64
+
+
+@pytest.mark.parametrize("op,shape", [
+    # Rows x what each of them gets threads for, 2^32 of them or more in one dimension of a grid.
+    ("scan", (1 << 17, 4096, 1, 16, 1)), ("scan", (1 << 23, 64, 1, 16, 1)), ("scan_bwd", (1 << 18, 64, 64, 64, 2)),
+    ("scan_bwd", (1 << 17, 4096, 1, 16, 1)), ("scan_step", (1 << 20, 1024, 1, 16, 1)), ("conv_step", (1 << 20, 8192)),
+    ("conv", (1 << 24, 16384, 1)), ("conv_bwd", (1 << 20, 8192, 1)), ("mv4", (1, 64, 1 << 28))])
+def test_refuses_what_one_launch_cannot_hold(op, shape):
+    """A grid counts its threads in 32 bits: such calls are refused when they
+    are planned, before any kernel of theirs runs."""
+    e = lambda *v, d=BF: torch.empty(v, dtype=d, device="meta")  # noqa: E731
+    if op == "mv4":
+        m, k, n = shape
+        code, t = A.LM_MV4, {lm._X: e(m, k), lm._W: e(n, k // 2, d=torch.uint8), lm._SCALES: e(n, 2), lm._Y: e(m, n)}
+    elif op.startswith("conv"):
+        x, (n, c) = e(*shape), shape[:2]
+        w = e(c, 4)
+        code, t = {"conv": (A.LM_CONV, {lm._Y: x}), "conv_step": (A.LM_CONV_STEP, {lm._Y: x, lm._S1: e(n, c, 3)}),
+                   "conv_bwd": (A.LM_CONV_BWD, {lm._GY: x, lm._DX: x, lm._DW: w})}[op]
+        t |= {lm._X: x, lm._W: w}
+    else:
+        n, c, l, s, g = shape
+        x = e(n, c) if op == "scan_step" else e(n, c, l)
+        bc, a = e(n, g, s) if op == "scan_step" else e(n, g, s, l), e(c, s, d=F)
+        code, t = {"scan": (A.LM_SCAN, {lm._Y: x}), "scan_step": (A.LM_SCAN_STEP, {lm._Y: x, lm._S1: e(n, c, s, d=F)}),
+                   "scan_bwd": (A.LM_SCAN_BWD, {lm._GY: x, lm._DX: x, lm._DDT: x, lm._DA: a, lm._DB: bc, lm._DC: bc})}[op]
+        t |= {lm._X: x, lm._DT: x, lm._A: a, lm._B: bc, lm._C: bc}
+        if op == "scan_bwd":
+            t[lm._SAVED] = e(n * -(-l // (16 if s <= 16 else 4)) * c * (16 if s <= 16 else 64), d=F)
+    with pytest.raises(lm.ConvError, match="one launch") as r:
+        lm._make_plan(code, t)
+    assert r.value.status == A.EUNSUPPORTED
