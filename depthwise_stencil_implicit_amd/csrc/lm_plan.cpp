@@ -140,13 +140,19 @@ bool one_launch(const lm_plan_t &p)
     return threads < 4294967296.0 && parts < 2147483648.0;
 }
 
+// Rows per chunk that the caller asks for (0: none), no more than there are.
+int64_t forced_rows(const lm_plan_t &p, int64_t max_len)
+{
+    return std::min(p.args.chunk, std::max<int64_t>(max_len, 1));
+}
+
 // Rows per chunk and chunks per sequence of a convolution: the kernel's
 // threads own a few channels each, and 2^18 of them (four waves on every
 // SIMD) hide the memory's latency.  A chunk reads K-1 rows of its neighbour
 // again, so it is never shorter than min_rows.
 void conv_chunks(lm_plan_t &p, int64_t max_len, int64_t per_thread, int64_t min_rows)
 {
-    int64_t rows = p.args.chunk;
+    int64_t rows = forced_rows(p, max_len);
     if (rows <= 0) {
         const int64_t total = p.t[LM_OFFSETS].rank ? p.L : p.seqs * p.L;
         rows = total * lm_cdiv(p.C, per_thread) / (1 << 18);
@@ -168,7 +174,7 @@ void scan_chunks(lm_plan_t &p, int64_t max_len)
     const int64_t blocks = p.G * lm_cdiv(p.C / p.G, LM_SCAN_CH);
     const bool packed = p.t[LM_OFFSETS].rank > 0;
     const double pair = p.op == LM_SCAN && p.S <= 16 ? 1.5 : 2.0;
-    int64_t rows = p.args.chunk;
+    int64_t rows = forced_rows(p, max_len);
     if (rows <= 0) {
         const int64_t len = std::max<int64_t>(max_len, 1);
         double best = 0;

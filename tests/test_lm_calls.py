@@ -205,3 +205,23 @@ def test_refuses_what_one_launch_cannot_hold(op, shape):
     with pytest.raises(lm.ConvError, match="one launch") as r:
         lm._make_plan(code, t)
     assert r.value.status == A.EUNSUPPORTED
+
+
+def conv_and_scan(n=2, c=8, l=100, s=16, offsets=None):
+    x, w = torch.zeros(n, c, l), torch.zeros(c, 4)
+    bc, a = torch.zeros(n, 1, s, l), torch.zeros(c, s)
+    return ((A.LM_CONV, {lm._X: x, lm._W: w, lm._Y: x, lm._OFF: offsets}),
+            (A.LM_CONV_BWD, {lm._X: x, lm._GY: x, lm._W: w, lm._DX: x, lm._DW: w, lm._OFF: offsets}),
+            (A.LM_SCAN, {lm._X: x, lm._DT: x, lm._A: a, lm._B: bc, lm._C: bc, lm._Y: x, lm._OFF: offsets}))
+
+
+@pytest.mark.parametrize("chunk", [101, 1 << 40, (1 << 63) - 40, (1 << 63) - 1])
+@pytest.mark.parametrize("offsets", [None, torch.zeros(4, dtype=torch.int32)])
+def test_a_chunk_longer_than_the_axis(chunk, offsets):
+    """One piece per sequence, whatever the forced length: none of the plan's
+    numbers overflows."""
+    for op, t in conv_and_scan(n=1 if offsets is not None else 2, offsets=offsets):
+        p = lm._make_plan(op, t, chunk=chunk)
+        assert p.chunks == 1 and 100 <= p.chunk <= 128 and 0 <= p.workspace_bytes < 4096
+    for op, t in conv_and_scan(n=1, l=0):
+        assert lm._make_plan(op, t, chunk=chunk).chunks == 1
