@@ -397,9 +397,9 @@ def quantize4(w: torch.Tensor, group: int = 128, symmetric: bool = True, dtype: 
     scale per group of columns, around 8 (zeros is None) or, not symmetric,
     around the group's own zero point."""
     n, k = w.shape
-    if k % group:
-        raise ValueError(f"{k} columns do not make groups of {group}")
-    g = w.float().view(n, k // group, group)
+    if group < 1 or k % group or k % 2:
+        raise ValueError(f"{k} columns do not make pairs and groups of {group}")
+    g = w.float().reshape(n, k // group, group)
     if symmetric:
         scales = (g.abs().amax(2) / 7).to(dtype)
         scales[scales == 0] = 1  # a group of zeros

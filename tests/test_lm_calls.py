@@ -225,3 +225,18 @@ def test_a_chunk_longer_than_the_axis(chunk, offsets):
         assert p.chunks == 1 and 100 <= p.chunk <= 128 and 0 <= p.workspace_bytes < 4096
     for op, t in conv_and_scan(n=1, l=0):
         assert lm._make_plan(op, t, chunk=chunk).chunks == 1
+
+
+def test_quantize4_takes_any_weight(calls):
+    """Transposed and sliced weights of every type; columns that do not make
+    pairs or groups are refused."""
+    g = torch.Generator().manual_seed(1)
+    w = torch.randn(64, 12, generator=g)
+    wide = torch.randn(12, 100, generator=g)
+    for v in (w.t(), wide[:, 10:74], w.t().to(BF), wide.to(HF)[:, ::1][:, 36:]):
+        for symmetric in (True, False):
+            got, want = (lm.quantize4(u, 32, symmetric=symmetric, dtype=F) for u in (v, v.contiguous()))
+            assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+    for columns, group in ((21, 1), (21, 3), (21, 7), (21, 32), (64, 0), (64, -32), (64, 48), (64, 128)):
+        with pytest.raises(ValueError, match=f"{columns} columns"):
+            lm.quantize4(torch.zeros(4, columns), group)
