@@ -205,3 +205,26 @@ def test_packed_scans_of_any_lengths(i):
     o, b = (R.scan(x, d, A, B, Cm, softplus_dt=True, offsets=off, **par, gy=gy, gstate=gs, bound=k) for k in (False, True))
     for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dstate"):
         R.assert_close(getattr(back, k), o[k], b[k], 2 * n_f + (t if k in ("dA", "dD") else c), k)
+
+
+@pytest.mark.parametrize("dt", [BF, HF, F])
+@pytest.mark.parametrize("K,group,zeros", [
+    (192, 64, True), (224, 32, False), (160, 32, True), (1120, 224, True), (1152, 96, False), (2080, 32, True), (4160, 64, False),
+    (8224, 32, True), (9088, 32, False), (8320, 128, False), (16384, 64, True), (10240, 2560, True)])
+def test_matvec4_weighs_every_group_exactly(dt, K, group, zeros):
+    """Rows with one power of two each, one in every 32 columns and in each of
+    the last 64: rows cut short, split rows and every size of group leave no
+    column out, take its own scale and zero, and round nothing."""
+    g = gen(K)
+    N = 21
+    cols = sorted({c + (7 * c // 32) % 32 for c in range(0, K, 32)} | set(range(K - 64, K)))
+    x = torch.zeros(len(cols), K, dtype=torch.float64)
+    x[range(len(cols)), cols] = 2.0 ** (torch.arange(len(cols)) % 5 - 2).double()
+    packed = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    scales = 2.0 ** torch.randint(-4, 3, (N, K // group), generator=g).double()
+    zz = torch.randint(0, 16, (N, K // group), generator=g).double() if zeros else None
+    q = torch.stack([packed & 15, packed >> 4], 2).reshape(N, K).double()
+    w = scales.repeat_interleave(group, 1) * (q - (zz.repeat_interleave(group, 1) if zeros else 8))
+    on = lambda v: v.to(dt).cuda() if v is not None else None  # noqa: E731
+    y = lm.matvec4(on(x), packed.cuda(), on(scales), on(zz))
+    assert torch.equal(y.cpu().double(), x @ w.t())
