@@ -209,6 +209,12 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
             k.fail(CONV_EINVAL, "%s is not a tensor of this operator", kNames[s]);
             return k.status;
         }
+    for (int s = 0; s < LM_NSLOT; ++s)
+        for (int i = 0; i < t[s].rank; ++i)
+            if (t[s].sizes[i] < 0) {
+                k.fail(CONV_EINVAL, "%s has a negative size", kNames[s]);
+                return k.status;
+            }
     const bool step = op == LM_CONV_STEP || op == LM_SCAN_STEP, conv = op <= LM_CONV_STEP, mv = op == LM_MV4;
     const bool bwd = op == LM_CONV_BWD || op == LM_SCAN_BWD;
     const conv_tensor &x = t[LM_X];

@@ -2,6 +2,7 @@
 the outputs it allocates and the plans it keeps.  ``calls`` stands in for the
 launch and records each call's plan and tensors."""
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -240,3 +241,15 @@ def test_quantize4_takes_any_weight(calls):
     for columns, group in ((21, 1), (21, 3), (21, 7), (21, 32), (64, 0), (64, -32), (64, 48), (64, 128)):
         with pytest.raises(ValueError, match=f"{columns} columns"):
             lm.quantize4(torch.zeros(4, columns), group)
+
+
+def test_refuses_negative_sizes():
+    """Through the C entry, where any descriptor may come."""
+    d = (A.ConvTensor * A.LM_NSLOT)()
+    for place, sizes in ((lm._X, (-2, 8, 10)), (lm._Y, (-2, 8, 10)), (lm._W, (8, 4))):
+        d[place].rank, d[place].dtype = len(sizes), A.F32
+        for i, s in enumerate(sizes):
+            d[place].sizes[i], d[place].strides[i] = s, 1
+    p, err = A.LmPlan(), ctypes.create_string_buffer(256)
+    assert A.lib().lm_plan(A.LM_CONV, d, ctypes.byref(A.LmArgs()), ctypes.byref(p), err, len(err)) == A.EINVAL
+    assert b"negative size" in err.value
