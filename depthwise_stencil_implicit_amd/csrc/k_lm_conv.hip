@@ -13,7 +13,9 @@
 // Measured, bf16, K = 4: 4 x 2048 x 4096 in 28 us (4.9 TB/s; a large copy
 // reaches 5.1); output and gradients of 8 x 2048 x 2048 in 88 us, of which the
 // backward walk takes 55 (2 channels per thread and 64-row chunks; 4 channels
-// and 32 rows read a seventh more and took 64).
+// and 32 rows read a seventh more and took 64).  In f32 the prompt takes 58 us
+// (4.6 TB/s), with positions contiguous 240 and in bf16 234: lanes L elements
+// apart use a word of each line they fetch.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -51,6 +53,8 @@ template <int V> __device__ __forceinline__ bool conv_item(const ConvP &p, ConvA
     const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     a.part = divide(item, p.cvs, a.c);
     if (!p.slots && a.part >= p.parts) return false;
+    // Out of the straight path, whose start would be half a us longer (prompt of
+    // 4 x 2048 x 4096: 28.3 for 27.8).
     if (__builtin_expect(p.slots, 0)) {
         // The first lane's sequence by the whole wave, then on to the lane's own.
         const int part = (int)a.part;

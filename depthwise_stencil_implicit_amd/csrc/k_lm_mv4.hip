@@ -13,6 +13,12 @@
 // pair of weights, exactly.  f32 rows are split into three bf16 terms, which
 // hold all 24 bits, against exact weights.
 //
+// What that costs in bits: the bf16 sums are about 30 times what is wanted of
+// them, so where they are taken apart 5 of f32's 24 bits are gone, 11 more than
+// the result's own rounding keeps.  It shows only where the terms of a row
+// cancel to 2^-11 of their size.  An infinity in a row of x makes its products
+// NaN (infinity less infinity), where a sum of products could be infinite.
+//
 // A workgroup works on tiles of 16 outputs; its waves take blocks of 128
 // columns in turn (each lane 16 bytes = 32 weights of one output) and join
 // through LDS.  mv4_tiles keeps the rows of x in registers over many tiles, so

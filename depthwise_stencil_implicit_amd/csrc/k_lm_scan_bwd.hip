@@ -6,9 +6,11 @@
 // and dz = gy (sum_s C h + D x) silu'(z), ddt = dd softplus'.
 //
 // States come from the saved ones: CK steps are run forward again from a saved
-// state, a and h[t-1] stay in registers (2 CK NS = 128 values per lane, 64 above 16 states), then
-// the same steps are run in reverse.  Running the recurrence backwards instead
-// (h[t-1] = (h[t] - d x B) / a) would divide by factors near zero.
+// state, a and h[t-1] stay in registers (2 CK NS = 128 values per lane, 64 above
+// 16 states), then the same steps are run in reverse.  Running the recurrence
+// backwards instead (h[t-1] = (h[t] - d x B) / a) would divide by factors near
+// zero.  Above 32 states 52 of a lane's registers do not fit and spill, in the
+// kernels for other layouts 6 to 58 (f32 and up to 16 states most).
 //
 // Sums over states cross the four rows of a wave; sums over channels (dB, dC)
 // cross a row's sixteen channels by halving exchanges, then the four waves
@@ -16,8 +18,11 @@
 // fixed order, as scan_bwd_c does for dA, dD and the bias over the sequences.
 //
 // Bound by vector issue, 73 instructions per step and wave (20 for the forward
-// steps, 36 for the reverse ones, 17 for the exchanges).  Measured, bf16, 8 x
-// 2048 x 2048 channels of 16 states: 450 us, and 14 for scan_bwd_bc.
+// steps, 36 for the reverse ones, 17 for the exchanges), and some 85 scalar
+// registers kept in vector lanes.  Measured, bf16, 8 x 2048 x 2048 channels of 16
+// states: 447 us, and 13 for scan_bwd_bc.  8 x 1024 x 2048 with its forward call:
+// 16 states 314 us (f32 329, positions contiguous 418 and 605), 32 states 489, 64
+// states 1890.
 #include <hip/hip_runtime.h>
 
 #include "lm_scan.h"

@@ -147,9 +147,10 @@ int64_t forced_rows(const lm_plan_t &p, int64_t max_len)
 }
 
 // Rows per chunk and chunks per sequence of a convolution: the kernel's
-// threads own a few channels each, and 2^18 of them (four waves on every
-// SIMD) hide the memory's latency.  A chunk reads K-1 rows of its neighbour
-// again, so it is never shorter than min_rows.
+// threads own a few channels each, and 2^18 of them are four waves for every
+// SIMD, which hide the memory's latency (the forward kernel's registers let two
+// or three of them run at a time, the backward one's four).  A chunk reads K-1
+// rows of its neighbour again, so it is never shorter than min_rows.
 void conv_chunks(lm_plan_t &p, int64_t max_len, int64_t per_thread, int64_t min_rows)
 {
     int64_t rows = forced_rows(p, max_len);

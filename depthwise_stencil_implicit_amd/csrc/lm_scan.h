@@ -128,6 +128,7 @@ __device__ __forceinline__ ScanAt scan_at(const ScanP &p, int64_t chunks, int64_
     // All of these are below 2^31.
     const uint32_t b = blockIdx.x, r = b / (uint32_t)p.blocks, cb = b - r * (uint32_t)p.blocks;
     a.part = r;
+    // Out of the straight path (prompt of 8 x 1024 x 2048 x 16: 76.7 us in it, 75.7 out of it).
     if (__builtin_expect(p.slots, 0)) {
         int seq, first;
         a.sp = seq_of_slot(p.off, (int)p.seqs, (int)p.L, (uint32_t)p.chunk, (int)r, seq, first);

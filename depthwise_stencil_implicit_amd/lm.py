@@ -5,15 +5,17 @@ scan, and products with 4-bit weights.
 Activations are logical [N, C, L] with any strides, like the convolution's;
 channels-last storage (L rows of C channels) is the fast order.  A packed batch
 is [1, C, T] with ``offsets`` (int32 on the device, ascending from 0 to T):
-sequence s is the rows offsets[s] .. offsets[s+1]-1.  Give ``max_len`` with it,
-a length that few sequences pass: it decides how the work is split and nothing
-else.
+sequence s is the rows offsets[s] .. offsets[s+1]-1.  ``max_len`` with it, a
+length that few sequences pass, helps to choose how the work is split (without
+it they may be as long as T); results and the size of the workspace hold for any
+value.
 
 Each operator exists for prompts (``causal_conv``, ``selective_scan``), as its
 gradients (``*_backward``) and for single tokens (``*_step``, which update the
 state in place).  ``Prepared*`` objects keep the plan of fixed shapes, strides
 and types for loops where a call's latency counts; like ``Prepared`` of the
-convolution they take tensors of those descriptors and check no more.
+convolution they take tensors of those descriptors and check no more.  Calls by
+name keep their plans by the descriptors of all their tensors.
 
 torch provides device memory and the current stream; all arithmetic is in the
 library's kernels.  Nothing here records autograd history.

@@ -46,7 +46,8 @@
  *   y[m,n] = bias[n] + sum_k x[m,k] scales[n,k/group] (q[n,k] - zeros[n,k/group])
  *   q: uint8 [N, K/2], the low four bits the even k; zeros default to 8;
  *   scales and zeros [N, K/group] in x's dtype.  group = K / (columns of
- *   scales), a multiple of 32.
+ *   scales), a multiple of 32.  A row of x whose sums pass f32's range at 256
+ *   times x (one with an infinity does) gives infinities or NaN.
  */
 #ifndef MICONV_LM_H
 #define MICONV_LM_H
@@ -115,8 +116,8 @@ typedef struct lm_plan_t {
     conv_tensor t[LM_NSLOT];
     int64_t seqs;      /* sequences (batch rows of a *_STEP, products' rows of x for MV4) */
     int64_t C, L;      /* channels (MV4: outputs), rows of one x row */
-    int64_t K;         /* taps; MV4: columns */
-    int64_t S, G;      /* states, groups; MV4: G = columns per scale */
+    int64_t K;         /* taps; MV4: columns of x */
+    int64_t S, G;      /* states, groups; MV4: G = groups of columns (K / G columns each) */
     int64_t chunk, chunks;       /* rows per chunk, chunks per sequence (packed: of max_len rows) */
     int64_t saved_floats;        /* SCAN*: elements of LM_SAVED */
     int64_t workspace_bytes;
@@ -128,7 +129,8 @@ typedef struct lm_plan_t {
  *   tensors  LM_NSLOT descriptors.
  *   err, err_len  optional buffer for a message on failure.
  * Returns CONV_OK, CONV_EINVAL (shapes, types, missing or surplus tensors), or
- * CONV_EUNSUPPORTED (K, S or group outside the kernels' range).
+ * CONV_EUNSUPPORTED (K, S or group outside the kernels' range, or a call of 2^32
+ * or more threads in one launch).
  */
 MICONV_API int lm_plan(int32_t op, const conv_tensor *tensors, const lm_args *args, lm_plan_t *out, char *err,
                        size_t err_len);
