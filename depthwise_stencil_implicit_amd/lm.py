@@ -101,7 +101,7 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
     of them follow from the inputs (dstate from a state that the call does not
     read), and lm_run sees pointers only."""
     key = [op, flags, max_len, chunk]
-    dev, q, tensors = -1, _Ptrs(), ins + outs
+    dev, q, tensors = None, _Ptrs(), ins + outs
     for slot, t in tensors:
         if t is None:
             key.append(None)
@@ -110,7 +110,7 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
         if d != dev:
             if d < 0:
                 raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
-            if dev >= 0:
+            if dev is not None:
                 raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
             dev = d
         key += (t.shape, t.stride(), t.dtype)
@@ -135,13 +135,6 @@ def _run(p: A.LmPlan, q, dev: int) -> None:
     st = A.lib().lm_run(ctypes.byref(p), q, ws.data_ptr() if n else None, n, torch._C._cuda_getCurrentRawStream(dev))
     if st != A.OK:
         raise ConvError(st)
-
-
-def _on_gpu(*tensors) -> None:
-    """Before outputs are allocated: a clear refusal of CPU tensors."""
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
 
 
 def _new(t) -> torch.Tensor:
@@ -181,7 +174,6 @@ def causal_conv(x, w, b=None, *, activation=None, state=None, offsets=None, max_
     sequence (zeros without it); ``return_state`` gives those in front of what
     follows it.  ``chunk`` forces the rows one thread walks."""
     w = _taps(w)
-    _on_gpu(x)
     y = torch.empty_like(x)
     last = _rows_like(_seqs(x, offsets), x.shape[1], w.shape[-1] - 1, x) if return_state else None
     _call(A.LM_CONV, [(_X, x), (_W, w), (_BIAS, b), (_S0, state), (_OFF, offsets)], [(_Y, y), (_S1, last)], _act(activation),
@@ -195,7 +187,6 @@ def causal_conv_backward(gy, x, w, b=None, *, activation=None, state=None, offse
     that of the returned state.  db comes with a bias, dstate with a state;
     ``need_dw`` covers dw and db."""
     shape, w = w.shape, _taps(w)
-    _on_gpu(x)
     dx = torch.empty_like(x) if need_dx else None
     dw = _new(w) if need_dw else None
     db = _new(b) if need_dw and b is not None else None
@@ -213,8 +204,9 @@ class _Step:
     current one for the call."""
 
     def __init__(self, op, tensors, shape, ref, flags=0):
-        _on_gpu(*[t for t in tensors.values() if t is not None])
         self.device = ref.device
+        if any(t is not None and not t.is_cuda for t in tensors.values()):
+            raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
         if any(t is not None and t.device != ref.device for t in tensors.values()):
             raise ValueError("tensors on several devices")
         self.shape, self.dtype = shape, ref.dtype
@@ -282,7 +274,6 @@ def selective_scan(x, dt, A_, B, C, *, D=None, z=None, dt_bias=None, dt_softplus
     state f32 [sequences, C, S].  ``save`` returns what ``selective_scan_backward``
     takes as ``saved``.  ``chunk`` forces how many steps run in one piece."""
     B, C = _grouped(B, 4), _grouped(C, 4)
-    _on_gpu(x)
     y = torch.empty_like(x) if want_y else None
     # Their type is said: without it they would have torch's default one.
     last = x.new_empty((_seqs(x, offsets), x.shape[1], A_.shape[-1]), dtype=torch.float32) if return_state else None
@@ -310,7 +301,6 @@ def selective_scan_backward(gy, x, dt, A_, B, C, *, D=None, z=None, dt_bias=None
     ``gstate``, that of the returned state.  ``saved`` comes from the forward
     call (``save=True``) on the same tensors; without it the states are computed
     again.  dD, dz, ddt_bias and dstate come with D, z, dt_bias and state."""
-    _on_gpu(x)
     if saved is None:
         saved = selective_scan(x, dt, A_, B, C, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, state=state,
                                offsets=offsets, max_len=max_len, save=True, want_y=False, chunk=chunk).saved

@@ -19,7 +19,6 @@ def calls(monkeypatch):
     count as ones of device 0."""
     made = []
     monkeypatch.setattr(lm, "_plans", {})
-    monkeypatch.setattr(lm, "_on_gpu", lambda *t: None)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
     monkeypatch.setattr(lm, "_run", lambda p, q, *rest: made.append((p, {i: v for i, v in enumerate(q) if v})))
     return made
@@ -115,7 +114,6 @@ def test_steps_by_name_plan_once(calls, monkeypatch):
     of a shape checks and plans."""
     plans, make = [], lm._make_plan
     monkeypatch.setattr(lm, "_make_plan", lambda *a, **k: plans.append(a) or make(*a, **k))
-    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
     x, w, st = torch.zeros(3, 8), torch.zeros(8, 4), torch.zeros(3, 8, 3)
     dt, a, bc, h = torch.zeros(3, 8), torch.zeros(8, 16), torch.zeros(3, 16), torch.zeros(3, 8, 16)
     packed, scales, wide = torch.zeros(5, 32, dtype=torch.uint8), torch.zeros(5, 2), torch.zeros(2, 3, 64)
@@ -253,3 +251,19 @@ def test_refuses_negative_sizes():
     p, err = A.LmPlan(), ctypes.create_string_buffer(256)
     assert A.lib().lm_plan(A.LM_CONV, d, ctypes.byref(A.LmArgs()), ctypes.byref(p), err, len(err)) == A.EINVAL
     assert b"negative size" in err.value
+
+
+def test_every_call_refuses_host_memory():
+    """All tensors on the host, before a pointer of theirs goes anywhere."""
+    x, w, st = torch.zeros(2, 8, 5), torch.zeros(8, 4), torch.zeros(2, 8, 3)
+    dt, a, bc = torch.zeros(2, 8, 5), torch.zeros(8, 16), torch.zeros(2, 16, 5)
+    packed, scales = torch.zeros(5, 32, dtype=torch.uint8), torch.zeros(5, 2)
+    one = (x[:, :, 0], dt[:, :, 0], a, bc[..., 0], bc[..., 0], torch.zeros(2, 8, 16))
+    for call in (lambda: lm.causal_conv(x, w, state=st, return_state=True), lambda: lm.causal_conv_backward(x, x, w, state=st),
+                 lambda: lm.causal_conv_step(x[:, :, 0], w, None, st), lambda: lm.selective_scan(x, dt, a, bc, bc, save=True),
+                 lambda: lm.selective_scan_backward(x, x, dt, a, bc, bc), lambda: lm.selective_scan_step(*one),
+                 lambda: lm.matvec4(torch.zeros(2, 64), packed, scales),
+                 lambda: lm.PreparedCausalConvStep(x[:, :, 0], w, None, st), lambda: lm.PreparedSelectiveScanStep(*one),
+                 lambda: lm.PreparedMatvec4(torch.zeros(2, 64), packed, scales)):
+        with pytest.raises(ValueError, match="GPU only"):
+            call()
