@@ -248,11 +248,12 @@ template <typename T, int NS> __global__ __launch_bounds__(256) void scan_step(c
     float d = to_f32(static_cast<const T *>(p.dt)[n * p.dts.n + c * p.dts.c]);
     if (p.bias) d += p.bias[c * p.bias_s];
     if (p.softplus) d = softplus(d);
-    const float dx = d * x;
+    const float dx = d * x, d2 = d * kLog2e;
     float o = 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        h[i] = __builtin_fmaf(hw_exp2(d * rate(A[i])), h[i], dx * b[i]);
+        // d = 0 leaves the state also where A is infinite (as rate() does).
+        h[i] = __builtin_fmaf(hw_exp2(d2 != 0.f ? d2 * A[i] : 0.f), h[i], dx * b[i]);
         o = __builtin_fmaf(cv[i], h[i], o);
     }
     if (p.dense) store_f32<float, NS>(ph, h);

@@ -228,3 +228,22 @@ def test_matvec4_weighs_every_group_exactly(dt, K, group, zeros):
     on = lambda v: v.to(dt).cuda() if v is not None else None  # noqa: E731
     y = lm.matvec4(on(x), packed.cuda(), on(scales), on(zz))
     assert torch.equal(y.cpu().double(), x @ w.t())
+
+
+def test_steps_of_zero_keep_the_state():
+    """dt of the type's lowest value under softplus is d = 0: prompt and step
+    leave the state bit for bit, whatever A is, and a NaN in A stays one."""
+    g = gen(77)
+    C, S, L = 12, 16, 5
+    x, B = rnd(g, 1, C, L), rnd(g, 1, 1, S, L)
+    d = torch.full_like(x, torch.finfo(F).min)
+    A, st = -torch.exp(rnd(g, C, S)), rnd(g, 1, C, S)
+    A[::2, ::3], A[1, 1] = -torch.inf, torch.inf
+    got = lm.selective_scan(x, d, A, B, B, dt_softplus=True, state=st, return_state=True)
+    assert torch.equal(got.state, st)
+    h = st.clone()
+    lm.selective_scan_step(x[:, :, 0], d[:, :, 0], A, B[..., 0], B[..., 0], h, dt_softplus=True)
+    assert torch.equal(h, st)
+    A[3, 4] = torch.nan
+    got = lm.selective_scan(x, x, A, B, B, dt_softplus=True, state=st, return_state=True)
+    assert torch.equal(torch.isnan(got.state).nonzero().cpu(), torch.tensor([[0, 3, 4]]))
