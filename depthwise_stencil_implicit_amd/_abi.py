@@ -71,8 +71,9 @@ class ConvPlanOpts(ctypes.Structure):
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmiconv.so")
 
 # The sequence operators (include/miconv_lm.h).
-LM_I32, LM_U8 = 16, 17
-LM_CONV, LM_CONV_BWD, LM_CONV_STEP, LM_SCAN, LM_SCAN_BWD, LM_SCAN_STEP, LM_MV4 = range(7)
+LM_I32, LM_U8, LM_F8 = 16, 17, 18
+(LM_CONV, LM_CONV_BWD, LM_CONV_STEP, LM_SCAN, LM_SCAN_BWD, LM_SCAN_STEP, LM_MV4, LM_GATED, LM_GATED_BWD, LM_GATED_STEP,
+ LM_NORM, LM_NORM_BWD, LM_ADAPTERS) = range(13)
 LM_SLOTS = ("X", "W", "BIAS", "Y", "STATE_IN", "STATE_OUT", "OFFSETS", "GY", "GSTATE", "DX", "DW", "DBIAS", "DSTATE",
             "DT", "A", "B", "C", "D", "Z", "DT_BIAS", "DDT", "DA", "DB", "DC", "DD", "DZ", "DDT_BIAS", "SAVED", "ROWS",
             "SCALES", "ZEROS")
@@ -81,7 +82,7 @@ LM_SILU, LM_SOFTPLUS = 1, 2
 
 
 class LmArgs(ctypes.Structure):
-    _fields_ = [("flags", _i32), ("reserved", _i32), ("max_len", _i64), ("chunk", _i64)]
+    _fields_ = [("flags", _i32), ("value", ctypes.c_float), ("max_len", _i64), ("chunk", _i64)]
 
 
 class LmPlan(ctypes.Structure):

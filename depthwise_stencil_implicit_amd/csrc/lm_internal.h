@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/miconv_lm.h"
@@ -82,6 +83,48 @@ inline int mv4_parts(const lm_plan_t &p)
     return (int)lm_cdiv(blocks, p.dtype == CONV_F32 ? 16 : p.K % 128 ? 32 : 64);
 }
 
+// The recurrence: rows of a workgroup's tile, steps between saved states,
+// channels of a thread (two of 16 bits make a word; other memory orders take
+// one, as do single channels).
+constexpr int LM_GATED_TILE = 128, LM_GATED_SAVE = 64;
+inline int gated_width(const lm_plan_t &p)
+{
+    if (p.dtype == CONV_F32 || p.C < 2) return 1;
+    for (int s : {LM_X, LM_A, LM_B, LM_Y, LM_GY, LM_DX, LM_DA, LM_DB})
+        if (p.t[s].rank && p.t[s].strides[1] != 1) return 1;
+    return 2;
+}
+
+// The norm: channels that a workgroup's registers hold, workgroups of the
+// gradients, each of which leaves one row of dw's sums.
+constexpr int LM_NORM_MAX = 65536;
+inline int norm_threads(int64_t rows, int64_t C)   // threads of a row
+{
+    if (rows >= 2048) return C <= 2048 ? 64 : C <= 16384 ? 256 : 1024;
+    return C <= 512 ? 64 : C <= 4096 ? 256 : 1024;
+}
+inline int64_t norm_bwd_groups(const lm_plan_t &p)
+{
+    const int64_t rows = p.seqs * p.L, t = norm_threads(rows, p.C), per = t == 64 ? 4 : 1;
+    return std::max<int64_t>(1, std::min<int64_t>(lm_cdiv(rows, per), t == 1024 ? 256 : 1024));
+}
+
+// Adapters: rows of a tile, parts of the columns of x, adapters of a tile that
+// are worked on at a time, width of a row of inner sums.
+constexpr int LM_MAX_RANK = 256, LM_ADAPTER_N = 256;
+struct AdapterShape { int rows, parts, slots, width; };
+inline AdapterShape adapter_shape(const lm_plan_t &p)
+{
+    AdapterShape s;
+    s.rows = p.seqs >= 512 ? 64 : 16;
+    const int64_t tiles = lm_cdiv(p.seqs, s.rows);
+    s.slots = (int)std::min<int64_t>(s.rows == 64 ? 2 : 16, std::max<int64_t>(1, std::min(p.seqs, p.G)));
+    const int64_t want = lm_cdiv(512, std::max<int64_t>(1, tiles * (s.rows == 64 ? 1 : s.slots)));
+    s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({want, lm_cdiv(p.K, 256), 16}));
+    s.width = (int)lm_cdiv(p.S, 32) * 32;
+    return s;
+}
+
 typedef void *const *lm_ptrs;
 int launch_lm_conv(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
 int launch_lm_conv_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
@@ -89,6 +132,12 @@ int launch_lm_conv_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
 int launch_lm_scan(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 int launch_lm_scan_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 int launch_lm_scan_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
+int launch_lm_gated(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
+int launch_lm_gated_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
+int launch_lm_gated_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
+int launch_lm_norm(const lm_plan_t &p, lm_ptrs q, hipStream_t s);
+int launch_lm_norm_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
+int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 int launch_lm_mv4(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s);
 
 inline int lm_launch_status() { return hipGetLastError() == hipSuccess ? CONV_OK : CONV_EDEVICE; }

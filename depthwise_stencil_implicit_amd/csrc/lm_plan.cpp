@@ -2,88 +2,14 @@
 // how their long axis is split.  lm_run: checks of the pointers, dispatch.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 
 #include "internal.h"
-#include "lm_internal.h"
+#include "lm_check.h"
 
 namespace {
 
 using namespace miconv;
-
-const char *const kNames[LM_NSLOT] = {
-    "x",   "w", "bias", "y", "state_in", "state_out", "offsets", "gy",  "gstate",  "dx",     "dw",   "dbias",  "dstate", "dt",
-    "A",   "B", "C",    "D", "z",        "dt_bias",   "ddt",     "dA",  "dB",      "dC",     "dD",   "dz",     "ddt_bias",
-    "saved", "rows", "scales", "zeros"};
-
-int64_t elem(int32_t dtype)
-{
-    switch (dtype) {
-    case CONV_F32: case LM_I32: return 4;
-    case CONV_F16: case CONV_BF16: return 2;
-    case LM_U8: return 1;
-    default: return 0;
-    }
-}
-
-struct Checker {
-    const conv_tensor *t;
-    char *err;
-    size_t len;
-    int status = CONV_OK;
-
-    bool fail(int st, const char *fmt, ...) __attribute__((format(printf, 3, 4)))
-    {
-        if (status == CONV_OK) {
-            status = st;
-            if (err && len) {
-                va_list ap;
-                va_start(ap, fmt);
-                vsnprintf(err, len, fmt, ap);
-                va_end(ap);
-            }
-        }
-        return false;
-    }
-    bool has(int s) const { return t[s].rank > 0; }
-    // Tensor s with these sizes and type; present unless optional.
-    bool want(int s, int32_t dtype, std::initializer_list<int64_t> sizes, bool optional = false)
-    {
-        if (status != CONV_OK) return false;
-        const conv_tensor &d = t[s];
-        if (!has(s)) return optional ? true : fail(CONV_EINVAL, "%s is missing", kNames[s]);
-        if (d.rank != (int)sizes.size()) return fail(CONV_EINVAL, "%s has %d dims, %d expected", kNames[s], d.rank, (int)sizes.size());
-        if (d.dtype != dtype) return fail(CONV_EINVAL, "%s has another element type than the call needs", kNames[s]);
-        int i = 0;
-        for (int64_t v : sizes) {
-            if (d.sizes[i] != v)
-                return fail(CONV_EINVAL, "%s has size %lld in dim %d, %lld expected", kNames[s], (long long)d.sizes[i], i, (long long)v);
-            if (d.strides[i] < 0) return fail(CONV_EINVAL, "%s has a negative stride", kNames[s]);
-            ++i;
-        }
-        return true;
-    }
-    // An output has no two elements in one place.
-    bool output(int s)
-    {
-        if (status != CONV_OK || !has(s)) return status == CONV_OK;
-        const conv_tensor &d = t[s];
-        int order[CONV_MAX_RANK], n = 0;
-        for (int i = 0; i < d.rank; ++i) {
-            if (d.sizes[i] == 0) return true;
-            if (d.sizes[i] > 1) order[n++] = i;
-        }
-        std::sort(order, order + n, [&](int a, int b) { return d.strides[a] < d.strides[b]; });
-        int64_t span = 1;
-        for (int i = 0; i < n; ++i) {
-            if (d.strides[order[i]] < span) return fail(CONV_EINVAL, "output %s overlaps itself", kNames[s]);
-            span = (d.sizes[order[i]] - 1) * d.strides[order[i]] + span;
-        }
-        return true;
-    }
-};
 
 // Which tensors an operator may have.
 uint64_t allowed(int op)
@@ -105,6 +31,13 @@ uint64_t allowed(int op)
                   LM_DA, LM_DB, LM_DC, LM_DD, LM_DZ, LM_DDT_BIAS, LM_DSTATE});
     case LM_SCAN_STEP: return m({LM_X, LM_DT, LM_A, LM_B, LM_C, LM_D, LM_Z, LM_DT_BIAS, LM_Y, LM_STATE_OUT, LM_ROWS});
     case LM_MV4: return m({LM_X, LM_W, LM_BIAS, LM_Y, LM_SCALES, LM_ZEROS});
+    case LM_GATED: return m({LM_X, LM_A, LM_B, LM_D, LM_Y, LM_STATE_IN, LM_STATE_OUT, LM_OFFSETS, LM_SAVED});
+    case LM_GATED_BWD:
+        return m({LM_X, LM_A, LM_B, LM_D, LM_OFFSETS, LM_SAVED, LM_GY, LM_GSTATE, LM_DX, LM_DA, LM_DB, LM_DD, LM_DSTATE});
+    case LM_GATED_STEP: return m({LM_X, LM_A, LM_B, LM_D, LM_Y, LM_STATE_OUT, LM_ROWS});
+    case LM_NORM: return m({LM_X, LM_W, LM_Y, LM_STATE_IN, LM_STATE_OUT, LM_SCALES, LM_SAVED});
+    case LM_NORM_BWD: return m({LM_X, LM_W, LM_GY, LM_GSTATE, LM_SAVED, LM_DX, LM_DW});
+    case LM_ADAPTERS: return m({LM_X, LM_A, LM_B, LM_ROWS, LM_Z, LM_D, LM_SCALES, LM_Y});
     default: return 0;
     }
 }
@@ -138,12 +71,6 @@ bool one_launch(const lm_plan_t &p)
         break;
     }
     return threads < 4294967296.0 && parts < 2147483648.0;
-}
-
-// Rows per chunk that the caller asks for (0: none), no more than there are.
-int64_t forced_rows(const lm_plan_t &p, int64_t max_len)
-{
-    return std::min(p.args.chunk, std::max<int64_t>(max_len, 1));
 }
 
 // Rows per chunk and chunks per sequence of a convolution: the kernel's
@@ -216,6 +143,14 @@ extern "C" int lm_plan(int32_t op, const conv_tensor *t, const lm_args *args, lm
                 k.fail(CONV_EINVAL, "%s has a negative size", kNames[s]);
                 return k.status;
             }
+    if (op >= LM_GATED) {
+        lm_plan_t p;
+        memset(&p, 0, sizeof(p));
+        p.op = op, p.args = *args;
+        memcpy(p.t, t, sizeof(p.t));
+        if (lm_plan_layer(op, k, *args, p) == CONV_OK) *out = p;
+        return k.status;
+    }
     const bool step = op == LM_CONV_STEP || op == LM_SCAN_STEP, conv = op <= LM_CONV_STEP, mv = op == LM_MV4;
     const bool bwd = op == LM_CONV_BWD || op == LM_SCAN_BWD;
     const conv_tensor &x = t[LM_X];
@@ -397,7 +332,7 @@ extern "C" int lm_run(const lm_plan_t *p, void *const *q, void *workspace, size_
     }
     // Sums are written without their terms too, as zeros: those over sequences
     // (dw, dA ...) without sequences, those over channels (dB, dC) without channels.
-    if ((p->C == 0 && p->op != LM_SCAN_BWD) || (p->op == LM_MV4 && p->seqs == 0)) return CONV_OK;
+    if ((p->C == 0 && p->op != LM_SCAN_BWD) || ((p->op == LM_MV4 || p->op == LM_ADAPTERS) && p->seqs == 0)) return CONV_OK;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (p->op) {
     case LM_CONV: return launch_lm_conv(*p, q, s);
@@ -407,6 +342,12 @@ extern "C" int lm_run(const lm_plan_t *p, void *const *q, void *workspace, size_
     case LM_SCAN_BWD: return launch_lm_scan_bwd(*p, q, workspace, s);
     case LM_SCAN_STEP: return launch_lm_scan_step(*p, q, s);
     case LM_MV4: return launch_lm_mv4(*p, q, workspace, s);
+    case LM_GATED: return launch_lm_gated(*p, q, workspace, s);
+    case LM_GATED_BWD: return launch_lm_gated_bwd(*p, q, workspace, s);
+    case LM_GATED_STEP: return launch_lm_gated_step(*p, q, s);
+    case LM_NORM: return launch_lm_norm(*p, q, s);
+    case LM_NORM_BWD: return launch_lm_norm_bwd(*p, q, workspace, s);
+    case LM_ADAPTERS: return launch_lm_adapters(*p, q, workspace, s);
     default: return CONV_EINVAL;
     }
 }

@@ -1,6 +1,7 @@
 """Sequence operators of language models on the GPU (binding of
 include/miconv_lm.h): the short causal convolution, the selective state space
-scan, and products with 4-bit weights.
+scan, the gated linear recurrence, the RMS norm with the residual's addition,
+products with 4-bit weights, and low-rank adapters of many requests.
 
 Activations are logical [N, C, L] with any strides, like the convolution's;
 channels-last storage (L rows of C channels) is the fast order.  A packed batch
@@ -10,9 +11,10 @@ length that few sequences pass, helps to choose how the work is split (without
 it they may be as long as T); results and the size of the workspace hold for any
 value.
 
-Each operator exists for prompts (``causal_conv``, ``selective_scan``), as its
-gradients (``*_backward``) and for single tokens (``*_step``, which update the
-state in place).  ``Prepared*`` objects keep the plan of fixed shapes, strides
+The sequence operators exist for prompts (``causal_conv``, ``selective_scan``,
+``gated_recurrence``), as their gradients (``*_backward``) and for single tokens
+(``*_step``, which update the state in place).  ``rms_norm``, ``matvec4`` and
+``adapters`` work on rows, of prompts and of single tokens alike.  ``Prepared*`` objects keep the plan of fixed shapes, strides
 and types for loops where a call's latency counts; like ``Prepared`` of the
 convolution they take tensors of those descriptors and check no more.  Calls by
 name keep their plans by the descriptors of all their tensors.
@@ -32,7 +34,7 @@ from .api import ConvError, _TORCH_DT
 
 (_X, _W, _BIAS, _Y, _S0, _S1, _OFF, _GY, _GS, _DX, _DW, _DBIAS, _DS, _DT, _A, _B, _C, _D, _Z, _DTB, _DDT, _DA, _DB, _DC,
  _DD, _DZ, _DDTB, _SAVED, _ROWS, _SCALES, _ZEROS) = range(A.LM_NSLOT)
-_TYPES = {**_TORCH_DT, torch.int32: A.LM_I32, torch.uint8: A.LM_U8}
+_TYPES = {**_TORCH_DT, torch.int32: A.LM_I32, torch.uint8: A.LM_U8, torch.float8_e4m3fn: A.LM_F8}
 _Ptrs = ctypes.c_void_p * A.LM_NSLOT
 
 
@@ -66,9 +68,29 @@ class ScanGrads(NamedTuple):
     dstate: Optional[torch.Tensor]
 
 
+class GatedGrads(NamedTuple):
+    dx: torch.Tensor
+    dr: torch.Tensor
+    di: torch.Tensor
+    ddecay: torch.Tensor
+    dstate: Optional[torch.Tensor]
+
+
+class NormOut(NamedTuple):
+    y: torch.Tensor
+    residual: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
+
+class NormGrads(NamedTuple):
+    dx: Optional[torch.Tensor]
+    dw: Optional[torch.Tensor]
+
+
 # ------------------------------------------------------------------- plans --
 
-def _make_plan(op, tensors, flags=0, max_len=0, chunk=0) -> A.LmPlan:
+def _make_plan(op, tensors, flags=0, max_len=0, chunk=0, value=0.0) -> A.LmPlan:
     """lm_plan for {place: tensor} (None: absent)."""
     d = (A.ConvTensor * A.LM_NSLOT)()
     for slot, t in tensors.items():
@@ -82,7 +104,7 @@ def _make_plan(op, tensors, flags=0, max_len=0, chunk=0) -> A.LmPlan:
         e.rank, e.dtype = t.dim(), _TYPES[t.dtype]
         for i, (s, st) in enumerate(zip(t.shape, t.stride())):
             e.sizes[i], e.strides[i] = s, st
-    args = A.LmArgs(flags, 0, int(max_len or 0), int(chunk or 0))
+    args = A.LmArgs(flags, value, int(max_len or 0), int(chunk or 0))
     p = A.LmPlan()
     err = ctypes.create_string_buffer(256)
     st = A.lib().lm_plan(op, d, ctypes.byref(args), ctypes.byref(p), err, len(err))
@@ -95,12 +117,12 @@ def _make_plan(op, tensors, flags=0, max_len=0, chunk=0) -> A.LmPlan:
 _plans: dict = {}
 
 
-def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
+def _call(op, ins, outs, flags=0, max_len=None, chunk=None, value=0.0) -> None:
     """Plan (or its cached copy) and launch of a call on ``ins`` and ``outs``,
     lists of (place, tensor or None).  Outputs are part of the key too: not all
     of them follow from the inputs (dstate from a state that the call does not
     read), and lm_run sees pointers only."""
-    key = [op, flags, max_len, chunk]
+    key = [op, flags, max_len, chunk, value]
     dev, q, tensors = None, _Ptrs(), ins + outs
     for slot, t in tensors:
         if t is None:
@@ -118,7 +140,7 @@ def _call(op, ins, outs, flags=0, max_len=None, chunk=None) -> None:
     key = tuple(key)
     p = _plans.get(key)
     if p is None:
-        p = _make_plan(op, dict(tensors), flags, max_len, chunk)
+        p = _make_plan(op, dict(tensors), flags, max_len, chunk, value)
         if len(_plans) >= 512:
             _plans.clear()
         _plans[key] = p
@@ -203,14 +225,14 @@ class _Step:
     one).  A new output belongs to that stream, as if it had been made the
     current one for the call."""
 
-    def __init__(self, op, tensors, shape, ref, flags=0):
+    def __init__(self, op, tensors, shape, ref, flags=0, value=0.0, dtype=None):
         self.device = ref.device
         if any(t is not None and not t.is_cuda for t in tensors.values()):
             raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
         if any(t is not None and t.device != ref.device for t in tensors.values()):
             raise ValueError("tensors on several devices")
-        self.shape, self.dtype = shape, ref.dtype
-        self.plan = _make_plan(op, {**tensors, _Y: self.empty_output()}, flags)
+        self.shape, self.dtype = shape, dtype or ref.dtype
+        self.plan = _make_plan(op, {**tensors, _Y: self.empty_output()}, flags, value=value)
 
     def empty_output(self) -> torch.Tensor:
         return torch.empty(self.shape, dtype=self.dtype, device=self.device)
@@ -351,6 +373,149 @@ def selective_scan_step(x, dt, A_, B, C, state, *, D=None, z=None, dt_bias=None,
     return y
 
 
+# ------------------------------------------------ gated linear recurrence --
+
+def gated_recurrence(x, r, i, decay, *, sharpness: float = 8.0, state=None, offsets=None, max_len=None, return_state: bool = False,
+                     save: bool = False, want_y: bool = True, chunk=None) -> ScanOut:
+    """h <- a h + sqrt(1 - a^2) sigmoid(i) x,  y = h,
+    a = exp(-sharpness softplus(decay) sigmoid(r)).
+
+    x and the gates r and i (before their sigmoid) [N, C, L]; decay [C] in f32;
+    ``state`` and the returned state f32 [sequences, C].  ``save`` returns what
+    ``gated_recurrence_backward`` takes as ``saved``.  ``chunk`` forces how many
+    steps run in one piece."""
+    y = torch.empty_like(x) if want_y else None
+    last = x.new_empty((_seqs(x, offsets), x.shape[1]), dtype=torch.float32) if return_state else None
+    saved = _new_gated_saved(x, offsets) if save else None
+    _call(A.LM_GATED, [(_X, x), (_A, r), (_B, i), (_D, decay), (_S0, state), (_OFF, offsets)], [(_Y, y), (_S1, last), (_SAVED, saved)],
+          0, max_len, chunk, sharpness)
+    return ScanOut(y, last, saved)
+
+
+def _new_gated_saved(x, offsets) -> torch.Tensor:
+    """Room for the states in front of every 64th step."""
+    count = x.shape[0] * -(-x.shape[2] // 64) if offsets is None else x.shape[2] // 64 + offsets.shape[0]
+    return torch.empty(count * x.shape[1], dtype=torch.float32, device=x.device)
+
+
+def gated_recurrence_backward(gy, x, r, i, decay, *, sharpness: float = 8.0, state=None, offsets=None, max_len=None, gstate=None,
+                              saved=None, chunk=None) -> GatedGrads:
+    """Gradients of ``gated_recurrence`` for gy, the gradient of y, and
+    ``gstate``, that of the returned state.  ``saved`` comes from the forward
+    call (``save=True``) on the same tensors; without it the states are computed
+    again.  dstate comes with a state."""
+    if saved is None:
+        saved = gated_recurrence(x, r, i, decay, sharpness=sharpness, state=state, offsets=offsets, max_len=max_len, save=True,
+                                 want_y=False, chunk=chunk).saved
+    dx, dr, di, dd = (torch.empty_like(v) for v in (x, r, i, decay))
+    ds = torch.empty_like(state) if state is not None else None
+    _call(A.LM_GATED_BWD, [(_GY, gy), (_X, x), (_A, r), (_B, i), (_D, decay), (_OFF, offsets), (_GS, gstate), (_SAVED, saved)],
+          [(_DX, dx), (_DA, dr), (_DB, di), (_DD, dd), (_DS, ds)], 0, max_len, chunk, sharpness)
+    return GatedGrads(dx, dr, di, dd, ds)
+
+
+class PreparedGatedRecurrenceStep(_Step):
+    """The step of ``gated_recurrence`` for fixed descriptors."""
+
+    def __init__(self, x, r, i, decay, state, *, sharpness: float = 8.0, rows=None):
+        super().__init__(A.LM_GATED_STEP, {_X: x, _A: r, _B: i, _D: decay, _S1: state, _ROWS: rows}, tuple(x.shape), x, value=sharpness)
+
+    def run(self, x, r, i, decay, state, rows=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
+        q = _Ptrs()
+        q[_X], q[_A], q[_B], q[_D], q[_S1] = x.data_ptr(), r.data_ptr(), i.data_ptr(), decay.data_ptr(), state.data_ptr()
+        if rows is not None:
+            q[_ROWS] = rows.data_ptr()
+        return self._launch(q, y, stream)
+
+
+def gated_recurrence_step(x, r, i, decay, state, *, sharpness: float = 8.0, rows=None) -> torch.Tensor:
+    """One token: x, r, i [N, C], state f32 [N, C] updated in place; ``rows``
+    as in ``causal_conv_step``."""
+    y = _new(x)
+    _call(A.LM_GATED_STEP, [(_X, x), (_A, r), (_B, i), (_D, decay), (_S1, state), (_ROWS, rows)], [(_Y, y)], value=sharpness)
+    return y
+
+
+# --------------------------------------------------------------- RMS norm --
+
+def _norm_outputs(x, residual, out_dtype, group, save):
+    """(y, new residual, scales, rstd) of a call, None where it has none.
+    Outputs of [N, C, L] are stored as rows of channels."""
+    like = lambda c, dtype: (  # noqa: E731
+        torch.empty((x.shape[0], c), dtype=dtype, device=x.device) if x.dim() == 2 else
+        torch.empty_strided((x.shape[0], c, x.shape[2]), (x.shape[2] * c, 1, c), dtype=dtype, device=x.device))
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x has {x.dim()} dims: [N, C] or [N, C, L]")
+    if out_dtype not in (None, x.dtype, torch.float8_e4m3fn):
+        raise ValueError(f"out_dtype {out_dtype}: x's or torch.float8_e4m3fn")
+    f8, c = out_dtype is torch.float8_e4m3fn, x.shape[1]
+    if group is not None and (not f8 or group < 1 or c % group):
+        raise ValueError(f"groups of {group} of {c} channels: they come with an 8-bit output and divide the channels")
+    y = like(c, out_dtype or x.dtype)
+    return (y, like(c, x.dtype) if residual is not None else None,
+            like(1 if group is None else c // group, torch.float32) if f8 else None,
+            x.new_empty((x.shape[0],) + tuple(x.shape[2:]), dtype=torch.float32) if save else None)
+
+
+def rms_norm(x, w, *, residual=None, eps: float = 1e-6, out_dtype=None, group=None, save: bool = False) -> NormOut:
+    """y = v w / sqrt(mean of v^2 over the channels + eps),  v = x + residual.
+
+    x and ``residual`` [N, C, L] or [N, C], w [C]; up to 65536 channels.  With a
+    residual the result holds the new one, v in x's type (y comes from the
+    unrounded sum).  ``out_dtype`` torch.float8_e4m3fn stores y in 8 bits with
+    ``scales`` f32 [N, G, L] or [N, G]: y is their product.  G is 1, or C //
+    ``group`` for groups of 32, 64 or 128 channels.  ``save`` returns ``rstd``
+    for ``rms_norm_backward``."""
+    out = _norm_outputs(x, residual, out_dtype, group, save)
+    _call(A.LM_NORM, [(_X, x), (_W, w), (_S0, residual)], list(zip((_Y, _S1, _SCALES, _SAVED), out)), value=eps)
+    return NormOut(*out)
+
+
+class PreparedRmsNorm(_Step):
+    """``rms_norm`` for fixed descriptors."""
+
+    def __init__(self, x, w, residual=None, *, eps: float = 1e-6, out_dtype=None, group=None, save: bool = False):
+        self.outputs = [(slot, tuple(t.shape), t.stride(), t.dtype) if t is not None else None for slot, t in
+                        zip((_Y, _S1, _SCALES, _SAVED), _norm_outputs(x, residual, out_dtype, group, save))]
+        self.device = x.device
+        tensors = {_X: x, _W: w, _S0: residual, **{o[0]: self._empty(o) for o in self.outputs[1:] if o}}
+        super().__init__(A.LM_NORM, tensors, self.outputs[0][1], x, value=eps, dtype=self.outputs[0][3])
+
+    def _empty(self, o) -> torch.Tensor:
+        return torch.empty_strided(o[1], o[2], dtype=o[3], device=self.device)
+
+    def empty_output(self) -> torch.Tensor:
+        return self._empty(self.outputs[0])
+
+    def run(self, x, w, residual=None, stream: Optional[int] = None) -> NormOut:
+        q = _Ptrs()
+        q[_X], q[_W] = x.data_ptr(), w.data_ptr()
+        if residual is not None:
+            q[_S0] = residual.data_ptr()
+        return self._launch(q, None, stream)
+
+    def _launch(self, q, y, stream) -> NormOut:
+        if stream is not None and stream != torch._C._cuda_getCurrentRawStream(self.device.index):
+            return super()._launch(q, y, stream)
+        out = [None if o is None else self._empty(o) for o in self.outputs]
+        for o, t in zip(self.outputs, out):
+            if o is not None:
+                q[o[0]] = t.data_ptr()
+        _run(self.plan, q, self.device.index)
+        return NormOut(*out)
+
+
+def rms_norm_backward(gy, x, w, rstd, *, gresidual=None, need_dx: bool = True, need_dw: bool = True) -> NormGrads:
+    """Gradients of ``rms_norm`` for gy, the gradient of a y that is not in 8
+    bits, and ``gresidual``, that of the new residual.  ``x`` is what was
+    normalised: the call's x, or with a residual the new one it returned; dx is
+    the gradient of both.  ``rstd`` comes from the call (``save=True``)."""
+    dx = torch.empty_like(x) if need_dx else None
+    dw = _new(w) if need_dw else None
+    _call(A.LM_NORM_BWD, [(_GY, gy), (_X, x), (_W, w), (_SAVED, rstd), (_GS, gresidual)], [(_DX, dx), (_DW, dw)])
+    return NormGrads(dx, dw)
+
+
 # ---------------------------------------------------------- 4-bit products --
 
 class PreparedMatvec4(_Step):
@@ -404,3 +569,51 @@ def quantize4(w: torch.Tensor, group: int = 128, symmetric: bool = True, dtype: 
         z = zeros.float()[..., None]
     q = torch.clamp(torch.round(g / scales.float()[..., None]) + z, 0, 15).to(torch.uint8).view(n, k)
     return (q[:, 0::2] | (q[:, 1::2] << 4)).contiguous(), scales, zeros
+
+
+# --------------------------------------------------------------- adapters --
+
+def _adapters_output(x, a, b) -> torch.Tensor:
+    """Room for y, stored as rows of outputs."""
+    n = b.shape[1]
+    if x.dim() != 3:
+        return torch.empty((x.shape[0], n), dtype=a.dtype, device=x.device)
+    return torch.empty_strided((x.shape[0], n, x.shape[2]), (x.shape[2] * n, 1, n), dtype=a.dtype, device=x.device)
+
+
+class PreparedAdapters(_Step):
+    """``adapters`` for fixed descriptors; ``y`` may be the base itself."""
+
+    def __init__(self, x, a, b, index, *, base=None, scaling=None, x_scales=None):
+        y = _adapters_output(x, a, b)
+        self.strides = y.stride()
+        super().__init__(A.LM_ADAPTERS, {_X: x, _A: a, _B: b, _ROWS: index, _Z: base, _D: scaling, _SCALES: x_scales}, tuple(y.shape), a)
+
+    def empty_output(self) -> torch.Tensor:
+        return torch.empty_strided(self.shape, self.strides, dtype=self.dtype, device=self.device)
+
+    def run(self, x, a, b, index, *, base=None, scaling=None, x_scales=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
+        q = _Ptrs()
+        q[_X], q[_A], q[_B], q[_ROWS] = x.data_ptr(), a.data_ptr(), b.data_ptr(), index.data_ptr()
+        if base is not None:
+            q[_Z] = base.data_ptr()
+        if scaling is not None:
+            q[_D] = scaling.data_ptr()
+        if x_scales is not None:
+            q[_SCALES] = x_scales.data_ptr()
+        return self._launch(q, y, stream)
+
+
+def adapters(x, a, b, index, *, base=None, scaling=None, x_scales=None, out=None) -> torch.Tensor:
+    """y[m] = base[m] + scaling[e] b[e] (a[e] x[m]),  e = index[m]: each row's own
+    low-rank adapter beside what a shared projection gave it.
+
+    x [M, K] or [N, K, L], a [E, R, K], b [E, N', R] with R up to 256, index
+    int32 [M] or [N, L]: rows with an index outside 0 .. E-1 have no adapter.
+    base (zero without it) and the result [M, N'] or [N, N', L]; scaling f32
+    [E].  x may be torch.float8_e4m3fn with ``x_scales`` f32 [M, 1] or [N, 1, L],
+    as ``rms_norm`` leaves it without groups.  ``out`` may be the base itself.
+    Rows with the same adapter share its pass when they are neighbours."""
+    y = _adapters_output(x, a, b) if out is None else out
+    _call(A.LM_ADAPTERS, [(_X, x), (_A, a), (_B, b), (_ROWS, index), (_Z, base), (_D, scaling), (_SCALES, x_scales)], [(_Y, y)])
+    return y
