@@ -3,15 +3,17 @@
 //
 // Bound by memory: x, base and y once, and the adapters that the rows name.
 // Two kernels, both on the matrix cores.  adapters_in leaves A[e] x[m] in f32:
-// workgroups take a tile of rows and a part of the columns, their waves share
-// the part's columns and join in LDS.  adapters_out adds the parts up and
-// multiplies by B[e], a tile of rows and 256 outputs per workgroup.
+// workgroups take some rows and a part of the columns, their waves share the
+// part's columns and join in LDS.  adapters_out adds the parts up, keeps them
+// in LDS and multiplies by B[e], 64 outputs per wave at a time.
 //
-// A tile of 16 or 64 rows may name several adapters: each is taken for the
-// whole tile in turn -- or by workgroups of its own, `slots` at a time, so that
-// the tokens of many requests do not wait for each other -- and only its rows
-// are kept.  Lanes of other rows load the row of a neighbour that has it: the
-// rows of a matrix product do not touch each other.
+// The rows of a workgroup share an adapter.  Of a call of few rows, tokens of
+// many requests in any order, the workgroup of every 16th row that names an
+// adapter gathers those rows by a look at all of index; for more rows
+// adapters_sort, one workgroup, puts them in the adapters' order first and
+// lists tiles of 64 of them.  (Tiles of neighbours, which may name several
+// adapters, took each of them in turn: four changes in 8192 rows made the call
+// 1.3 times as long, tokens among prompts many times.)
 //
 // The inner sums stay f32 into the second product: they are cut into three
 // bf16 terms, which hold all 24 bits, against exact weights (f16 weights are
@@ -27,9 +29,11 @@ namespace miconv {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kTile = LM_ADAPTER_TILE;   // rows of a sorted tile
 constexpr int kUnit = 64;            // columns that a wave takes at a time: whole lines of 16-bit rows
 constexpr int kRanks = 64;           // of an inner product's workgroup, and of a staged piece
-constexpr int kOut = LM_ADAPTER_N;   // outputs of a workgroup
+constexpr int kOutRows = 2;          // sixteens of rows of adapters_out's tile
+constexpr int kOut = LM_ADAPTER_N;   // outputs of a workgroup at a time
 constexpr int kStride = kRanks + 8;  // of a staged row: 16-byte reads of 8 rows on different banks
 
 struct AdapterP {
@@ -38,13 +42,13 @@ struct AdapterP {
     const int32_t *index;
     void *y;
     float *t;   // [parts][rows][width]
+    int *order, *tile_count;
+    int4 *tiles;
     S3 xs, as, bs, bases, ys, scs;   // as, bs: (adapter, row, column)
     int64_t scaling_e, L;
-    int rows, K, N, R, E, parts, slots, width, tiles, blocks, groups;
+    int rows, K, N, R, E, parts, width, groups, spans, reps;   // outputs of a workgroup: reps of 512, spans of them
     bool in_place;
 };
-
-struct f8_t { uint8_t u; };
 
 // Eight values along a product's inner axis, as the matrix instruction takes
 // them; Oct<X, T>: eight of memory type X for a product in type T.
@@ -61,6 +65,7 @@ template <typename T> __device__ __forceinline__ Frag<T> frag_of(const Raw<T, 8>
     return f;
 }
 // e4m3 fits bf16 and f16.
+struct f8_t { uint8_t u; };
 struct Oct8 { uint32_t w[2]; };
 template <typename T> __device__ __forceinline__ Frag<T> frag_of(const Oct8 &o)
 {
@@ -78,23 +83,28 @@ template <typename T> __device__ __forceinline__ Frag<T> frag_of(const Oct8 &o)
     return f;
 }
 template <typename T> __device__ __forceinline__ Raw<T, 8> load_oct(const T *p) { return load_raw<T, 8>(p); }
-__device__ __forceinline__ Oct8 load_oct(const f8_t *p)
+// Sixteen neighbours, the first and the second eight.
+template <typename T> __device__ __forceinline__ void load_both(const T *p, Raw<T, 8> &a, Raw<T, 8> &b)
 {
-    struct __attribute__((packed, aligned(1))) Bytes { uint32_t w[2]; };
-    const Bytes b = *reinterpret_cast<const Bytes *>(p);
-    return {b.w[0], b.w[1]};
+    a = load_oct(p), b = load_oct(p + 8);
 }
-// The first n of eight values, any distance apart; the rest zero.
-template <typename T> __device__ __forceinline__ Raw<T, 8> load_some(const T *p, int64_t step, int n)
+__device__ __forceinline__ void load_both(const f8_t *p, Oct8 &a, Oct8 &b)
 {
-    Raw<T, 8> r;
+    struct __attribute__((packed, aligned(1))) Bytes { uint32_t w[4]; };
+    const Bytes v = *reinterpret_cast<const Bytes *>(p);
+    a = {{v.w[0], v.w[1]}}, b = {{v.w[2], v.w[3]}};
+}
+// The first n of V values, any distance apart; the rest zero.
+template <int V, typename T> __device__ __forceinline__ Raw<T, V> load_some(const T *p, int64_t step, int n)
+{
+    Raw<T, V> r;
     r.zero();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < V; ++i)
         if (i < n) r.set(i, p[i * step]);
     return r;
 }
-__device__ __forceinline__ Oct8 load_some(const f8_t *p, int64_t step, int n)
+template <int V> __device__ __forceinline__ Oct8 load_some(const f8_t *p, int64_t step, int n)
 {
     Oct8 r = {};
 #pragma unroll
@@ -102,34 +112,70 @@ __device__ __forceinline__ Oct8 load_some(const f8_t *p, int64_t step, int n)
         if (i < n) r.w[i / 4] |= (uint32_t)p[i * step].u << (i % 4 * 8);
     return r;
 }
+// Four values past the L2's lines in use: the kernel does not read them again.
+template <typename T> __device__ __forceinline__ void store_piece(T *p, const float (&v)[4])
+{
+    if constexpr (sizeof(T) == 4) store_f32<T, 4, true>(p, v);
+    else {
+        typedef uint32_t any2 __attribute__((ext_vector_type(2), aligned(2)));
+        __builtin_nontemporal_store(any2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])}, reinterpret_cast<any2 *>(p));
+    }
+}
 template <typename T> __device__ __forceinline__ void mma(const Frag<T> &a, const Frag<T> &b, f32x4 &c)
 {
     if constexpr (sizeof(T) == 4) mma_16x16x32_f32(a.v, b.v, c);
     else mma_16x16x32(a.v, b.v, c, T());
 }
 
-// The adapters of a tile's rows, lane r holding row r's.  take() gives those of
-// one slot in turn: the adapter and the set of its rows.
-struct Named {
-    uint64_t left;
-    int mine, turn;
-    __device__ __forceinline__ Named(const AdapterP &p, int row0, int rows)
+// A workgroup's rows, at most MR of them (`set`, `list`), and their adapter e, one
+// outside 0 .. E - 1 for rows without any.  Made by all waves; ends in a barrier.
+template <bool GATHER, int MR> struct Group;
+template <int MR> struct Group<false, MR> {
+    uint64_t set;
+    int e;
+    const int *list;
+    __device__ __forceinline__ Group(const AdapterP &p, int at, int *rows) : list(rows)
     {
+        constexpr int PER = kTile / MR;   // of a listed tile
         const int lane = threadIdx.x & 63;
-        mine = lane < rows && row0 + lane < p.rows ? p.index[row0 + lane] : -1;
-        if (mine < 0 || mine >= p.E) mine = -1;
-        left = __ballot(mine >= 0), turn = 0;
+        set = 0;
+        if (at / PER >= *p.tile_count) return;
+        const int4 tile = p.tiles[at / PER];   // adapter, first place in the order, rows
+        const int first = at % PER * MR, n = tile.z - first < MR ? tile.z - first : MR;
+        if (n <= 0) return;
+        e = tile.x;
+        set = n >= 64 ? ~0ull : (1ull << n) - 1;
+        if (threadIdx.x < MR && lane < n) rows[lane] = p.order[tile.y + first + lane];
+        lds_sync();
     }
-    __device__ __forceinline__ bool take(int slot, int slots, int &e, uint64_t &set)
+    __device__ __forceinline__ int row(int r) const { return list[r]; }
+};
+template <int MR> struct Group<true, MR> {
+    uint64_t set;
+    int e;
+    const int *list;
+    __device__ __forceinline__ Group(const AdapterP &p, int m, int *rows) : list(rows)
     {
-        while (left) {
-            e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-            set = __ballot(mine == e);
-            left &= ~set;
-            if (turn++ % slots == slot) return true;
+        constexpr int LOOKS = LM_ADAPTER_FEW / 64;
+        const int lane = threadIdx.x & 63;
+        int v[LOOKS];
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) v[j] = p.index[j * 64 + lane < p.rows ? j * 64 + lane : p.rows - 1];
+        e = __builtin_amdgcn_readfirstlane(p.index[m]);
+        int count = 0, first = 0;   // rows of the adapter so far, those in front of m
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+            const uint64_t same = __ballot(j * 64 + lane < p.rows && v[j] == e);
+            if (m >> 6 == j) first = count + __builtin_popcountll(same & ((1ull << (m & 63)) - 1));
+            const int place = count + __builtin_popcountll(same & ((1ull << lane) - 1)) - first;
+            if (m >> 6 <= j && threadIdx.x < 64 && same >> lane & 1 && place >= 0 && place < 16) rows[place] = j * 64 + lane;
+            count += __builtin_popcountll(same);
         }
-        return false;
+        const int n = count - first;
+        set = first % 16 ? 0 : n >= 16 ? 0xffff : (1ull << n) - 1;
+        lds_sync();
     }
+    __device__ __forceinline__ int row(int r) const { return list[r]; }
 };
 // Element offset of row m of a [N, columns, L] tensor.
 __device__ __forceinline__ int64_t row_at(const AdapterP &p, const S3 &s, int m)
@@ -139,32 +185,141 @@ __device__ __forceinline__ int64_t row_at(const AdapterP &p, const S3 &s, int m)
     return n * s.n + l * s.l;
 }
 
+// --------------------------------------------------------- rows by adapter --
+
+// The rows in the order of their adapters (in their own order within one, so
+// results repeat), and tiles of them; rows without an adapter are in tiles of
+// their own.  Each wave counts and then places a stretch of rows; kSorted
+// adapters at a time, and those without in the first turn's last bucket.
+constexpr int kSorted = 896;
+__global__ __launch_bounds__(1024) void adapters_sort(const AdapterP p)
+{
+    __shared__ int counts[16][kSorted + 1];
+    __shared__ int2 sums[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t each = ((int64_t)p.rows + 1023) / 1024 * 64, from = wave * each, to = from + each < p.rows ? from + each : p.rows;
+    int rows = 0, tiles = 0;   // placed so far
+    for (int64_t e0 = 0; e0 == 0 || e0 < p.E; e0 += kSorted) {
+        // Eight steps' loads at a time.
+        int idx[8];
+        const auto load = [&](int64_t i) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) idx[s] = p.index[i + s * 64 + lane < to ? i + s * 64 + lane : to - 1];
+        };
+        const auto bucket = [&](int64_t i, int e) {
+            if (i >= to) return -1;
+            if (e < 0 || e >= p.E) return e0 == 0 ? kSorted : -1;
+            return e >= e0 && e < e0 + kSorted ? (int)(e - e0) : -1;
+        };
+        for (int i = tid; i < 16 * (kSorted + 1); i += 1024) (&counts[0][0])[i] = 0;
+        __syncthreads();
+        for (int64_t i = from; i < to; i += 512) {
+            load(i);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int b = bucket(i + s * 64 + lane, idx[s]);
+                uint64_t left = __ballot(b >= 0);
+                while (left) {
+                    const int now = __builtin_amdgcn_readlane(b, __builtin_ctzll(left));
+                    const uint64_t same = __ballot(b == now);
+                    if (lane == 0) counts[wave][now] += __builtin_popcountll(same);
+                    left &= ~same;
+                }
+            }
+        }
+        __syncthreads();
+        // Bucket tid: its rows, its tiles, and the sums of both in front of it.
+        int n = 0;
+        if (tid <= kSorted) {
+#pragma unroll
+            for (int w = 0; w < 16; ++w) n += counts[w][tid];
+        }
+        const int t = (n + kTile - 1) / kTile;
+        int2 upto{n, t};
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int a = __shfl_up(upto.x, d), b = __shfl_up(upto.y, d);
+            if (lane >= d) upto.x += a, upto.y += b;
+        }
+        if (lane == 63) sums[wave] = upto;
+        __syncthreads();
+        int2 all{0, 0}, front{0, 0};
+        for (int w = 0; w < 16; ++w) {
+            if (w == wave) front = all;
+            all.x += sums[w].x, all.y += sums[w].y;
+        }
+        int at = rows + front.x + upto.x - n;
+        const int tile = tiles + front.y + upto.y - t;
+        for (uint64_t with = __ballot(t > 0); with; with &= with - 1) {   // a bucket's tiles by the whole wave
+            const int who = __builtin_ctzll(with), bucket_n = __builtin_amdgcn_readlane(n, who);
+            const int bucket_at = __builtin_amdgcn_readlane(at, who), bucket_tile = __builtin_amdgcn_readlane(tile, who);
+            const int e = wave * 64 + who < kSorted ? (int)e0 + wave * 64 + who : -1;
+            for (int i = lane; i * kTile < bucket_n; i += 64)
+                p.tiles[bucket_tile + i] = int4{e, bucket_at + i * kTile, bucket_n - i * kTile < kTile ? bucket_n - i * kTile : kTile, 0};
+        }
+        if (tid <= kSorted) {
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                const int c = counts[w][tid];
+                counts[w][tid] = at, at += c;
+            }
+        }
+        __syncthreads();
+        for (int64_t i = from; i < to; i += 512) {
+            if (to - from > 512) load(i);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int64_t at = i + s * 64 + lane;
+                const int b = bucket(at, idx[s]);
+                uint64_t left = __ballot(b >= 0);
+                while (left) {
+                    const int now = __builtin_amdgcn_readlane(b, __builtin_ctzll(left));
+                    const uint64_t same = __ballot(b == now);
+                    const int first = counts[wave][now];
+                    if (b == now) p.order[first + __builtin_popcountll(same & ((1ull << lane) - 1))] = (int)at;
+                    if (lane == 0) counts[wave][now] = first + __builtin_popcountll(same);
+                    left &= ~same;
+                }
+            }
+        }
+        __syncthreads();
+        rows += all.x, tiles += all.y;
+    }
+    if (tid == 0) *p.tile_count = tiles;
+}
+
 // --------------------------------------------------------- x times A[e]^T --
 
-// MF, RF: sixteens of rows and ranks.
+// MF, RF: sixteens of rows (gathered: one) and ranks.
 template <typename T, typename X, int MF, int RF, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void adapters_in(const AdapterP p)
 {
+    constexpr bool GATHER = MF == 1;
     __shared__ f32x4 join[kWaves][MF * RF][64];
-    typedef decltype(load_oct(static_cast<const X *>(nullptr))) XOct;
+    __shared__ int list[16 * MF];
+    typedef typename std::conditional<sizeof(X) == 1, Oct8, Raw<T, 8>>::type XOct;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     int at = blockIdx.x;
     const int part = at % p.parts;
     at /= p.parts;
-    const int rank0 = at % p.groups * (16 * RF), row0 = at / p.groups * (16 * MF);
+    const int rank0 = at % p.groups * (16 * RF), tile = GATHER ? blockIdx.y : at / p.groups;
     const int units = (p.K + kUnit - 1) / kUnit;
-    const int u1 = (int)((int64_t)units * (part + 1) / p.parts), whole = DENSE ? p.K / kUnit : 0;
-    const int u0 = (int)((int64_t)units * part / p.parts) + wave;
-    Named named(p, row0, 16 * MF);
-    int e;
-    uint64_t set;
-    while (named.take(blockIdx.y, p.slots, e, set)) {
+    const int whole = DENSE ? p.K / kUnit : 0;
+    const int piece = part * kWaves + wave;
+    const int u0 = (int)((int64_t)units * piece / (p.parts * kWaves)), u1 = (int)((int64_t)units * (piece + 1) / (p.parts * kWaves));
+    Group<GATHER, 16 * MF> group(p, tile, list);
+    const uint64_t set = group.set;
+    const int64_t e = group.e;
+    if (!set || e < 0 || e >= p.E) return;
+    {
         const X *x[MF];
         const T *a[RF];
-        const int k = (lane >> 4) * 8;
+        // A lane's part of a unit: sixteen neighbours, eight for each of two
+        // products (which columns meet there is the same for both sides).
+        const int k = (lane >> 4) * 16;
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
             const int r = m * 16 + (lane & 15);
-            x[m] = static_cast<const X *>(p.x) + row_at(p, p.xs, row0 + (set >> r & 1 ? r : __builtin_ctzll(set))) + k * p.xs.c;
+            x[m] = static_cast<const X *>(p.x) + row_at(p, p.xs, group.row(set >> r & 1 ? r : 0)) + k * p.xs.c;
         }
 #pragma unroll
         for (int j = 0; j < RF; ++j) {
@@ -185,44 +340,41 @@ template <typename T, typename X, int MF, int RF, bool DENSE> __global__ __launc
         };
         const int end = u1 < whole ? u1 : whole;
         if (u0 < end) {
-            XOct xo[2][MF];
-            Raw<T, 8> ao[2][RF];
-            const auto fetch = [&](int u) {
+            // Two units' registers in turn: handed on from one to the other
+            // they would be waited for at once.
+            XOct xo[2][2][MF];
+            Raw<T, 8> ao[2][2][RF];
+            const int count = end - u0, turn = GATHER ? 0 : tile % count;   // from another one on for each tile, as in adapters_out
+            const auto fetch = [&](int i, XOct (&xs)[2][MF], Raw<T, 8> (&as)[2][RF]) {
+                i = (i < count ? i : 0) + turn;
+                const int64_t c = (int64_t)(u0 + (i < count ? i : i - count)) * kUnit;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int m = 0; m < MF; ++m) load_both(x[m] + c, xs[0][m], xs[1][m]);
 #pragma unroll
-                    for (int m = 0; m < MF; ++m) xo[h][m] = load_oct(x[m] + (int64_t)u * kUnit + h * 32);
-#pragma unroll
-                    for (int j = 0; j < RF; ++j) ao[h][j] = load_oct(a[j] + (int64_t)u * kUnit + h * 32);
-                }
+                for (int j = 0; j < RF; ++j) load_both(a[j] + c, as[0][j], as[1][j]);
             };
-            fetch(u0);
-            for (int u = u0; u < end; u += kWaves) {
-                XOct xn[2][MF];
-                Raw<T, 8> an[2][RF];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) xn[h][m] = xo[h][m];
-#pragma unroll
-                    for (int j = 0; j < RF; ++j) an[h][j] = ao[h][j];
-                }
-                fetch(u + kWaves < end ? u + kWaves : u);
-                product(xn[0], an[0]), product(xn[1], an[1]);
+            fetch(0, xo[0], ao[0]);
+            for (int i = 0; i < count; i += 2) {
+                fetch(i + 1, xo[1], ao[1]);
+                __builtin_amdgcn_sched_barrier(0);
+                product(xo[0][0], ao[0][0]), product(xo[0][1], ao[0][1]);
+                if (i + 1 >= count) break;
+                fetch(i + 2, xo[0], ao[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                product(xo[1][0], ao[1][0]), product(xo[1][1], ao[1][1]);
             }
         }
         // Units cut short, or all of them where columns lie apart.
-        for (int u = u0; u < u1; u += kWaves) {
-            if (u < whole) continue;
+        for (int u = u0 > whole ? u0 : whole; u < u1; ++u) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                const int c = u * kUnit + h * 32, n = p.K - c - k;
+                const int c = u * kUnit + h * 8, n = p.K - c - k;
                 XOct xo[MF];
                 Raw<T, 8> ao[RF];
 #pragma unroll
-                for (int m = 0; m < MF; ++m) xo[m] = load_some(x[m] + c * p.xs.c, p.xs.c, n);
+                for (int m = 0; m < MF; ++m) xo[m] = load_some<8>(x[m] + c * p.xs.c, p.xs.c, n);
 #pragma unroll
-                for (int j = 0; j < RF; ++j) ao[j] = load_some(a[j] + c * p.as.l, p.as.l, n);
+                for (int j = 0; j < RF; ++j) ao[j] = load_some<8>(a[j] + c * p.as.l, p.as.l, n);
                 product(xo, ao);
             }
         }
@@ -237,9 +389,8 @@ template <typename T, typename X, int MF, int RF, bool DENSE> __global__ __launc
             for (int w = 1; w < kWaves; ++w) sum += join[w][f][lane];
             const int r = f / RF * 16 + (lane & 15), rank = rank0 + f % RF * 16 + (lane >> 4) * 4;
             if (rank < p.width && (set >> r & 1))
-                *reinterpret_cast<f32x4 *>(p.t + ((int64_t)part * p.rows + row0 + r) * p.width + rank) = sum;
+                *reinterpret_cast<f32x4 *>(p.t + ((int64_t)part * p.rows + group.row(r)) * p.width + rank) = sum;
         }
-        __syncthreads();
     }
 }
 
@@ -260,136 +411,227 @@ __device__ __forceinline__ void split(float v, uint16_t (&o)[3])
     o[2] = (uint16_t)(__float_as_uint(rest - __uint_as_float(w)) >> 16);
 }
 
-template <typename T, int MF, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void adapters_out(const AdapterP p)
+// Eight weights against the terms of a row.
+template <typename T> struct Weights { Frag<T> f; };
+template <> struct Weights<f16_t> { Frag<bf16_t> hi, lo; };   // 8 and 3 bits
+template <typename T> __device__ __forceinline__ Weights<T> weights_of(const Raw<T, 8> &o)
+{
+    Weights<T> w;
+    if constexpr (std::is_same<T, f16_t>::value) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v0 = o.f(2 * i), v1 = o.f(2 * i + 1);
+            const uint32_t u0 = __float_as_uint(v0) & 0xffff0000u, u1 = __float_as_uint(v1) & 0xffff0000u;
+            const float r0 = __builtin_isinf(v0) ? 0.f : v0 - __uint_as_float(u0);
+            const float r1 = __builtin_isinf(v1) ? 0.f : v1 - __uint_as_float(u1);
+            h[i] = u0 >> 16 | u1, l[i] = __float_as_uint(r0) >> 16 | (__float_as_uint(r1) & 0xffff0000u);
+        }
+        w.hi.v = uint4{h[0], h[1], h[2], h[3]}, w.lo.v = uint4{l[0], l[1], l[2], l[3]};
+    } else w.f = frag_of<T>(o);
+    return w;
+}
+template <typename T, typename U> __device__ __forceinline__ void mma_terms(const Weights<T> &w, const Frag<U> (&t)[TermOf<T>::n], f32x4 &c)
+{
+    if constexpr (std::is_same<T, f16_t>::value) {
+        mma<bf16_t>(t[1], w.lo, c), mma<bf16_t>(t[2], w.hi, c);
+        mma<bf16_t>(t[0], w.lo, c), mma<bf16_t>(t[1], w.hi, c), mma<bf16_t>(t[0], w.hi, c);
+    } else {
+#pragma unroll
+        for (int s = TermOf<T>::n - 1; s >= 0; --s) mma<T>(t[s], w.f, c);
+    }
+}
+
+// A wave takes 64 outputs at a time: a lane's four neighbours of four rows per
+// sixteen, so that sixteen lanes read and write a line of a 16-bit row.
+// KS: 32s of ranks staged for good; 0: more than 64 of them, staged in turn.
+template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void adapters_out(const AdapterP p)
 {
     typedef typename TermOf<T>::type U;
-    constexpr int NT = TermOf<T>::n, MR = 16 * MF;
+    constexpr bool GATHER = MF == 1;
+    constexpr int NT = TermOf<T>::n, MR = 16 * MF, NQ = 4;
     __shared__ __attribute__((aligned(16))) U terms[NT][MR * kStride];
+    __shared__ int list[MR];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int row0 = blockIdx.x / p.blocks * MR, n0 = blockIdx.x % p.blocks * kOut + wave * 64;
     const int quad = lane >> 4, col = lane & 15;
-    Named named(p, row0, MR);
-
-    f32x4 acc[MF][4];
-    // acc onto the rows of `set`: a lane's outputs are eight neighbours of a row, twice.
-    const auto leave = [&](uint64_t set) {
-#pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int r = m * 16 + col;
-            if (!(set >> r & 1)) continue;
-            T *y = static_cast<T *>(p.y) + row_at(p, p.ys, row0 + r);
-            const T *base = p.base ? static_cast<const T *>(p.base) + row_at(p, p.bases, row0 + r) : nullptr;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = n0 + h * 32 + quad * 8;
-                if (n >= p.N) continue;
-                float v[8];
-                if (DENSE && n + 8 <= p.N) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                    if (base) load_f32<T, 8>(base + n, v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += acc[m][2 * h + i / 4][i % 4];
-                    store_f32<T, 8>(y + n, v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (n + i < p.N)
-                            y[(n + i) * p.ys.c] = from_f32<T>((base ? to_f32(base[(n + i) * p.bases.c]) : 0.f) + acc[m][2 * h + i / 4][i % 4]);
-                }
-            }
-        }
+    const int tile = GATHER ? blockIdx.y : blockIdx.x / p.spans, span = GATHER ? blockIdx.x : blockIdx.x % p.spans;
+    // The workgroup's 256s of outputs, from another one on for each tile: rows
+    // are powers of two apart often enough that tiles at one column would keep
+    // to a few of the memory's channels.
+    const int block0 = span * p.reps, left = (p.N + kOut - 1) / kOut - block0, blocks = left < p.reps ? left : p.reps;
+    const int turn = GATHER ? 0 : tile % blocks;
+    const auto place = [&](int i) {
+        i = i < blocks ? i : 0;
+        i += turn;
+        return (block0 + (i < blocks ? i : i - blocks)) * kOut + wave * 64;
     };
-    const auto clear = [&]() {
+    const Group<GATHER, MR> group(p, tile, list);
+    const uint64_t set = group.set;
+    const int e = group.e;
+    if (!set) return;
+
+    // Offsets of a lane's rows, m * 16 + quad * 4 + i of the tile.
+    int64_t yo[MF][4], bo[MF][4];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = m * 16 + quad * 4 + i, row = group.row(set >> r & 1 ? r : 0);
+            yo[m][i] = row_at(p, p.ys, row);
+            bo[m][i] = p.base ? row_at(p, p.bases, row) : 0;
+        }
+    const T *base = static_cast<const T *>(p.base ? p.base : p.b);
+    T *y = static_cast<T *>(p.y);
+    // Past the last output, or without a base, loads repeat what is there.
+    const auto get_base = [&](int n0, Raw<T, 4> (&o)[MF][4]) {
+        const int n = n0 + col * 4;
 #pragma unroll
         for (int m = 0; m < MF; ++m)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[m][q] = f32x4{};
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DENSE) o[m][i] = load_raw<T, 4>(base + bo[m][i] + (!p.base ? 0 : n <= p.N - 4 ? n : p.N - 4));
+                else if (p.base) o[m][i] = load_some<4>(base + bo[m][i] + n * p.bases.c, p.bases.c, p.N - n);
+            }
     };
-    if (blockIdx.y == 0 && !p.in_place) {   // rows without an adapter
-        const uint64_t none = __ballot(lane < MR && row0 + lane < p.rows && named.mine < 0);
-        if (none) clear(), leave(none);
-    }
-    int e;
-    uint64_t set;
-    while (named.take(blockIdx.y, p.slots, e, set)) {
-        clear();
-        const float gain = p.scaling ? p.scaling[e * p.scaling_e] : 1.f;
-        for (int rank0 = 0; rank0 < p.R; rank0 += kRanks) {
-            const int ranks = p.width - rank0 < kRanks ? p.width - rank0 : kRanks;   // 32 or 64
-            // The parts' sums of the adapter's rows, four ranks a thread.
-            for (int i = threadIdx.x; i < MR * (kRanks / 4); i += 64 * kWaves) {
-                const int r = i / (kRanks / 4), c = i % (kRanks / 4) * 4;
-                f32x4 v = {};
-                if (set >> r & 1 && c < ranks) {
-                    const float *t = p.t + ((int64_t)row0 + r) * p.width + rank0 + c;
-                    for (int s = 0; s < p.parts; ++s) v += *reinterpret_cast<const f32x4 *>(t + (int64_t)s * p.rows * p.width);
-                    const float f = p.scales ? gain * p.scales[row_at(p, p.scs, row0 + r)] : gain;
+    const auto leave = [&](int n0, const Raw<T, 4> (&o)[MF][4], const f32x4 (&acc)[MF][NQ]) {
+        const int n = n0 + col * 4;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = rank0 + c + j < p.R ? v[j] * f : 0.f;
-                }
-                if constexpr (NT == 1) *reinterpret_cast<f32x4 *>(&terms[0][r * kStride + c]) = v;
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!(set >> (m * 16 + quad * 4 + i) & 1)) continue;
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = (p.base ? o[m][i].f(j) : 0.f) + acc[m][j][i];
+                if (DENSE && n + 4 <= p.N) store_piece(y + yo[m][i] + n, v);
                 else {
-                    uint16_t o[4][3];
+                    // The last piece of a row was loaded from its end.
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) split(v[j], o[j]);
-#pragma unroll
-                    for (int s = 0; s < 3; ++s)
-                        *reinterpret_cast<uint2 *>(&terms[s][r * kStride + c]) =
-                            uint2{o[0][s] | (uint32_t)o[1][s] << 16, o[2][s] | (uint32_t)o[3][s] << 16};
+                    for (int j = 0; j < 4; ++j)
+                        if (n + j < p.N) {
+                            if (DENSE) v[j] = (p.base ? to_f32(base[bo[m][i] + n + j]) : 0.f) + acc[m][j][i];
+                            y[yo[m][i] + (n + j) * p.ys.c] = from_f32<T>(v[j]);
+                        }
                 }
             }
-            __syncthreads();
-            if (n0 < p.N)
-                for (int k0 = 0; k0 < ranks; k0 += 32) {
-                    const int k = k0 + quad * 8, rank = rank0 + k;
-                    Raw<T, 8> bo[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {   // which output is row `col` of the product's tile q
-                        int n = n0 + (q >> 1) * 32 + (col >> 2) * 8 + (q & 1) * 4 + (col & 3);
-                        n = n < p.N ? n : p.N - 1;
-                        const T *b = static_cast<const T *>(p.b) + e * p.bs.n + n * p.bs.c;
-                        if constexpr (DENSE) {   // R is a multiple of 8
-                            bo[q] = load_oct(b + (rank < p.R ? rank : 0));
-                            if (rank >= p.R) bo[q].zero();
-                        } else bo[q] = load_some(b + rank * p.bs.l, p.bs.l, p.R - rank);
-                    }
-#pragma unroll
-                    for (int m = 0; m < MF; ++m) {
-                        Frag<U> tf[NT];
-#pragma unroll
-                        for (int s = 0; s < NT; ++s) {
-                            const U *t = &terms[s][(m * 16 + col) * kStride + k];
-                            __builtin_memcpy(&tf[s], __builtin_assume_aligned(t, 16), sizeof(tf[s]));
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if constexpr (std::is_same<T, f16_t>::value) {
-                                Frag<bf16_t> hi, lo;   // 8 and 3 bits
-                                uint32_t h[4], l[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float v0 = bo[q].f(2 * i), v1 = bo[q].f(2 * i + 1);
-                                    const uint32_t u0 = __float_as_uint(v0) & 0xffff0000u, u1 = __float_as_uint(v1) & 0xffff0000u;
-                                    const float r0 = __builtin_isinf(v0) ? 0.f : v0 - __uint_as_float(u0);
-                                    const float r1 = __builtin_isinf(v1) ? 0.f : v1 - __uint_as_float(u1);
-                                    h[i] = u0 >> 16 | u1, l[i] = __float_as_uint(r0) >> 16 | (__float_as_uint(r1) & 0xffff0000u);
-                                }
-                                hi.v = uint4{h[0], h[1], h[2], h[3]}, lo.v = uint4{l[0], l[1], l[2], l[3]};
-                                mma<bf16_t>(lo, tf[1], acc[m][q]), mma<bf16_t>(hi, tf[2], acc[m][q]);
-                                mma<bf16_t>(lo, tf[0], acc[m][q]), mma<bf16_t>(hi, tf[1], acc[m][q]);
-                                mma<bf16_t>(hi, tf[0], acc[m][q]);
-                            } else {
-                                const Frag<T> bf = frag_of<T>(bo[q]);
-#pragma unroll
-                                for (int s = NT - 1; s >= 0; --s) mma<T>(bf, tf[s], acc[m][q]);
-                            }
-                        }
-                    }
-                }
-            __syncthreads();
+    };
+    if (e < 0 || e >= p.E) {   // rows without an adapter
+        if (p.in_place) return;
+        const f32x4 zero[MF][NQ] = {};
+        Raw<T, 4> o[2][MF][4];
+        get_base(place(0), o[0]);
+        for (int i = 0; i < blocks; i += 2) {
+            get_base(place(i + 1), o[1]);
+            __builtin_amdgcn_sched_barrier(0);
+            leave(place(i), o[0], zero);
+            if (i + 1 >= blocks) break;
+            get_base(place(i + 2), o[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            leave(place(i + 1), o[1], zero);
         }
-        leave(set);
+        return;
+    }
+    const T *b = static_cast<const T *>(p.b) + e * p.bs.n;
+    const float gain = p.scaling ? p.scaling[e * p.scaling_e] : 1.f;
+    // Weights for the outputs n0 .. n0 + 63 from `rank` on; tile q
+    // of a product has every fourth output from n0 + q on.
+    const auto get_weights = [&](int n0, int rank, Raw<T, 8> (&o)[NQ]) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            int n = n0 + col * 4 + q;
+            n = n < p.N ? n : p.N - 1;
+            if constexpr (DENSE) o[q] = load_oct(b + n * p.bs.c + (rank < p.R ? rank : 0));   // R is a multiple of 8
+            else o[q] = load_some<8>(b + n * p.bs.c + rank * p.bs.l, p.bs.l, p.R - rank);
+        }
+    };
+    // The parts' sums of the rows from rank0 on, scaled and cut into terms.
+    const auto stage = [&](int rank0) {
+        for (int i = threadIdx.x; i < MR * (kRanks / 4); i += 64 * kWaves) {
+            const int r = i / (kRanks / 4), c = i % (kRanks / 4) * 4;
+            f32x4 v = {};
+            if (set >> r & 1 && rank0 + c < p.R) {
+                const int row = group.row(r);
+                const float *t = p.t + (int64_t)row * p.width + rank0 + c;
+                const float f = p.scales ? gain * p.scales[row_at(p, p.scs, row)] : gain;
+#pragma unroll 4
+                for (int s = 0; s < p.parts; ++s) v += *reinterpret_cast<const f32x4 *>(t + (int64_t)s * p.rows * p.width);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = rank0 + c + j < p.R ? v[j] * f : 0.f;
+            }
+            if constexpr (NT == 1) *reinterpret_cast<f32x4 *>(&terms[0][r * kStride + c]) = v;
+            else {
+                uint16_t o[4][3];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split(v[j], o[j]);
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                    *reinterpret_cast<uint2 *>(&terms[s][r * kStride + c]) =
+                        uint2{o[0][s] | (uint32_t)o[1][s] << 16, o[2][s] | (uint32_t)o[3][s] << 16};
+            }
+        }
+    };
+    // acc += the staged terms from k on times the weights o.  Ranks past the
+    // last are zeros in the terms; weights there are an earlier rank's.
+    const auto multiply = [&](const Raw<T, 8> (&o)[NQ], int k, int rank, f32x4 (&acc)[MF][NQ]) {
+        Frag<U> t[MF][NT];
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+            for (int s = 0; s < NT; ++s)
+                __builtin_memcpy(&t[m][s], __builtin_assume_aligned(&terms[s][(m * 16 + col) * kStride + k + quad * 8], 16), sizeof(t[m][s]));
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            Raw<T, 8> w = o[q];
+            if (rank + quad * 8 >= p.R) w.zero();
+            const Weights<T> wf = weights_of<T>(w);
+#pragma unroll
+            for (int m = 0; m < MF; ++m) mma_terms<T, U>(wf, t[m], acc[m][q]);
+        }
+    };
+    if constexpr (KS > 0) {   // staged once; the next outputs' base in flight
+        Raw<T, 8> w[KS][NQ];
+        Raw<T, 4> o[2][MF][4];
+        const auto get_all = [&](int n0) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) get_weights(n0, k * 32 + quad * 8, w[k]);
+        };
+        const auto finish = [&](int i, const Raw<T, 4> (&os)[MF][4]) {
+            f32x4 acc[MF][NQ] = {};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) multiply(w[k], k * 32, k * 32, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            get_all(place(i + 1));
+            leave(place(i), os, acc);
+        };
+        get_all(place(0)), get_base(place(0), o[0]);
+        stage(0);
+        __syncthreads();
+        for (int i = 0; i < blocks; i += 2) {
+            get_base(place(i + 1), o[1]);
+            __builtin_amdgcn_sched_barrier(0);
+            finish(i, o[0]);
+            if (i + 1 >= blocks) break;
+            get_base(place(i + 2), o[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            finish(i + 1, o[1]);
+        }
+    } else {
+        // The waves stay together: all of them stage for each 64 outputs.
+        for (int i = 0; i < blocks; ++i) {
+            const int n0 = place(i);
+            f32x4 acc[MF][NQ] = {};
+            for (int rank0 = 0; rank0 < p.R; rank0 += kRanks) {
+                __syncthreads();
+                stage(rank0);
+                __syncthreads();
+                for (int k = 0; k < kRanks && rank0 + k < p.R; k += 32) {
+                    Raw<T, 8> w[NQ];
+                    get_weights(n0, rank0 + k + quad * 8, w), multiply(w, k, rank0 + k, acc);
+                }
+            }
+            Raw<T, 4> o[MF][4];
+            get_base(n0, o), leave(n0, o, acc);
+        }
     }
 }
 
@@ -411,13 +653,21 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     a.xs = s3(p.t[LM_X]), a.as = s3(p.t[LM_A]), a.bs = s3(p.t[LM_B]), a.bases = s3(p.t[LM_Z]), a.ys = s3(p.t[LM_Y]), a.scs = s3(p.t[LM_SCALES]);
     a.scaling_e = p.t[LM_D].strides[0], a.L = p.L;
     a.rows = (int)p.seqs, a.K = (int)p.K, a.N = (int)p.C, a.R = (int)p.S, a.E = (int)p.G;
-    a.parts = shape.parts, a.slots = shape.slots, a.width = shape.width;
-    a.tiles = (int)lm_cdiv(p.seqs, shape.rows), a.blocks = (int)lm_cdiv(p.C, kOut), a.groups = (int)lm_cdiv(p.S, kRanks);
+    a.parts = shape.parts, a.width = shape.width, a.reps = shape.reps;
+    const bool few = shape.rows == 1;   // a workgroup for each row, which gathers its like
+    a.spans = (int)lm_cdiv(p.C, (int64_t)kOut * shape.reps), a.groups = (int)lm_cdiv(p.S, kRanks);
+    const unsigned tiles = (unsigned)shape.tiles, tiles_out = tiles * (few ? 1 : kTile / (16 * kOutRows));
+    if (!few) {
+        a.tiles = reinterpret_cast<int4 *>(static_cast<char *>(ws) + adapter_sums_bytes(p));
+        a.order = reinterpret_cast<int *>(a.tiles + shape.tiles);
+        a.tile_count = a.order + p.seqs;
+        adapters_sort<<<1, 1024, 0, s>>>(a);
+    }
     a.in_place = a.base == a.y;
     const bool f8 = p.t[LM_X].dtype == LM_F8;
     const bool dense_in = (a.xs.c == 1 && a.as.l == 1) || p.K == 1;
-    const bool dense_out = a.bs.l == 1 && a.R % 8 == 0 && a.ys.c == 1 && (!a.base || a.bases.c == 1);
-    const dim3 in((unsigned)(a.tiles * a.groups * a.parts), (unsigned)a.slots), out((unsigned)(a.tiles * a.blocks), (unsigned)a.slots);
+    const bool dense_out = a.bs.l == 1 && a.R % 8 == 0 && a.N >= 4 && a.ys.c == 1 && (!a.base || a.bases.c == 1);
+    const dim3 in((few ? 1 : tiles) * a.groups * a.parts, few ? tiles : 1), out((few ? 1 : tiles_out) * a.spans, few ? tiles_out : 1);
     const auto run = [&](auto t, auto x) {
         typedef decltype(t) T;
         typedef decltype(x) X;
@@ -434,11 +684,17 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
                 if (dense_in) ranks(mf, std::true_type());
                 else ranks(mf, std::false_type());
             }
-            if (dense_out) adapters_out<T, MF, true><<<out, 64 * kWaves, 0, s>>>(a);
-            else adapters_out<T, MF, false><<<out, 64 * kWaves, 0, s>>>(a);
+            const auto ranks_out = [&](auto ks) {
+                constexpr int MO = MF == 1 ? 1 : kOutRows, KS = decltype(ks)::value;
+                if (dense_out) adapters_out<T, MO, KS, true><<<out, 64 * kWaves, 0, s>>>(a);
+                else adapters_out<T, MO, 0, false><<<out, 64 * kWaves, 0, s>>>(a);
+            };
+            if (a.R <= 32) ranks_out(std::integral_constant<int, 1>());
+            else if (a.R <= 64) ranks_out(std::integral_constant<int, 2>());
+            else ranks_out(std::integral_constant<int, 0>());
         };
-        if (shape.rows == 64) rows(std::integral_constant<int, 4>());
-        else rows(std::integral_constant<int, 1>());
+        if (few) rows(std::integral_constant<int, 1>());
+        else rows(std::integral_constant<int, 4>());
     };
     const auto types = [&](auto t) {
         if (f8) run(t, f8_t());

@@ -285,6 +285,7 @@ template <typename T> __global__ __launch_bounds__(1024) void norm_dw(const floa
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float v = 0.f;
     if (c < C)
+#pragma unroll 16
         for (int64_t i = wave; i < parts; i += 16) v += part[i * C + c];
     sums[wave][lane] = v;
     __syncthreads();

@@ -109,20 +109,32 @@ inline int64_t norm_bwd_groups(const lm_plan_t &p)
     return std::max<int64_t>(1, std::min<int64_t>(lm_cdiv(rows, per), t == 1024 ? 256 : 1024));
 }
 
-// Adapters: rows of a tile, parts of the columns of x, adapters of a tile that
-// are worked on at a time, width of a row of inner sums.
-constexpr int LM_MAX_RANK = 256, LM_ADAPTER_N = 256;
-struct AdapterShape { int rows, parts, slots, width; };
+// Adapters: rows of a workgroup (1: those of its row's adapter, gathered),
+// tiles of that many (sorted by adapter, so each may leave one short), parts of
+// the columns of x, 256s of outputs of a workgroup, width of a row of inner sums.
+// About one workgroup for each compute unit: with two of them adapters_out took
+// 55 us for 50 of 8192 rows and outputs, adapters_in 26 for 21 at rank 64.
+constexpr int LM_MAX_RANK = 256, LM_ADAPTER_N = 256, LM_ADAPTER_FEW = 512, LM_ADAPTER_TILE = 64;
+struct AdapterShape { int rows, parts, reps, width; int64_t tiles; };
 inline AdapterShape adapter_shape(const lm_plan_t &p)
 {
     AdapterShape s;
-    s.rows = p.seqs >= 512 ? 64 : 16;
-    const int64_t tiles = lm_cdiv(p.seqs, s.rows);
-    s.slots = (int)std::min<int64_t>(s.rows == 64 ? 2 : 16, std::max<int64_t>(1, std::min(p.seqs, p.G)));
-    const int64_t want = lm_cdiv(512, std::max<int64_t>(1, tiles * (s.rows == 64 ? 1 : s.slots)));
-    s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({want, lm_cdiv(p.K, 256), 16}));
+    const bool few = p.seqs <= LM_ADAPTER_FEW;
+    s.rows = few ? 1 : LM_ADAPTER_TILE;
+    s.tiles = few ? p.seqs : p.seqs / s.rows + std::min(p.seqs, p.G + 1);
+    // Workgroups with work: gathered, one for each adapter and each 16 rows.
+    const int64_t groups = std::max<int64_t>(1, few ? std::min(p.seqs, p.G + p.seqs / 16) : lm_cdiv(p.seqs, s.rows));
+    s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({lm_cdiv(256, groups), lm_cdiv(p.K, 256), 16}));
+    const int64_t blocks = std::max<int64_t>(1, lm_cdiv(p.C, LM_ADAPTER_N)), halves = 2 * groups;
+    const int64_t spans = std::max<int64_t>(1, std::min<int64_t>(blocks, (256 + halves / 2) / halves));
+    s.reps = few ? 1 : (int)lm_cdiv(blocks, spans);
     s.width = (int)lm_cdiv(p.S, 32) * 32;
     return s;
+}
+inline int64_t adapter_sums_bytes(const lm_plan_t &p)
+{
+    const AdapterShape s = adapter_shape(p);
+    return lm_cdiv(4 * p.seqs * s.parts * s.width, 256) * 256;
 }
 
 typedef void *const *lm_ptrs;

@@ -137,7 +137,7 @@ def test_refusals(i):
     (A.LM_GATED_STEP, lambda v: {**{k: v(1 << 20, 16384) for k in (lm._X, lm._A, lm._B, lm._Y)}, lm._D: v(16384, d=F), lm._S1: v(1 << 20, 16384, d=F)}),
     (A.LM_NORM, lambda v: {lm._X: v(1 << 23, 64), lm._W: v(64), lm._Y: v(1 << 23, 64)}),
     (A.LM_ADAPTERS, lambda v: {lm._X: v(1 << 31, 64), lm._A: v(2, 8, 64), lm._B: v(2, 8, 8), lm._ROWS: v(1 << 31, d=I32), lm._Y: v(1 << 31, 8)}),
-    (A.LM_ADAPTERS, lambda v: {lm._X: v(1 << 24, 64), lm._A: v(2, 8, 64), lm._B: v(2, 65536, 8), lm._ROWS: v(1 << 24, d=I32), lm._Y: v(1 << 24, 65536)}),
+    (A.LM_ADAPTERS, lambda v: {lm._X: v(1 << 30, 64), lm._A: v(2, 8, 64), lm._B: v(2, 16, 8), lm._ROWS: v(1 << 30, d=I32), lm._Y: v(1 << 30, 16)}),
 ])
 def test_refuses_what_one_launch_cannot_hold(op, make):
     t = make(lambda *s, d=BF: torch.empty(s, dtype=d, device="meta"))
