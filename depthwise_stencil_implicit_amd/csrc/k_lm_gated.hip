@@ -13,8 +13,14 @@
 // the next tile are in flight meanwhile.  Lanes lie along the channels, so a
 // wave reads whole lines of rows of channels.
 //
-// Few sequences are split along the axis (gated_chunks): a first pass leaves
-// each chunk's (P, s), and a workgroup folds those in front of its own.
+// Few sequences leave units idle.  Forward, each tile is then a workgroup of its
+// own (gated_tile): it holds its rows' factors in registers, puts its (P, s)
+// where the tiles behind it look, finds what enters it from the sixteen tiles in
+// front -- the nearest one whose end is known, and the maps of those since --
+// and goes through its rows.  So the tensors are still read once (a first pass
+// for the maps took 1 x 65536 x 2560 498 us).  Backward, a first pass over two of
+// the seven tensors leaves the (P, s) of chunks, and a workgroup folds those
+// behind its own.
 //
 // 1 - a^2 comes from a where a is clear of 1, and from three terms of the
 // exponential's series where 2 k sigmoid(r) < 1/16: there a has lost what the
@@ -39,6 +45,7 @@ struct GatedP {
     void *y, *dx, *dr, *di;
     float *s1, *ds, *saved, *dd;
     float *sums, *part;   // (P, s) of each chunk and channel; terms of ddecay
+    uint64_t *ahead;      // tickets, then the (P, s) and the end of each tile
     const int32_t *off, *rows;
     S3 xs, rs, is, ys, gys, dxs, drs, dis;
     int64_t s0_n, s0_c, s1_n, s1_c, gs_n, gs_c, ds_n, ds_c, decay_c, dd_c;
@@ -156,8 +163,8 @@ template <int V> __device__ __forceinline__ void fold(const GatedP &p, int64_t f
 
 // ---------------------------------------------------------------- forward --
 
-// SUMS: the first pass, which leaves (P, s) of every chunk that another follows.
-template <typename T, int V, bool DENSE, bool SUMS> __global__ __launch_bounds__(64 * kWaves) void gated_fwd(const GatedP p)
+// Whole sequences.
+template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void gated_fwd(const GatedP p)
 {
     __shared__ __attribute__((aligned(16))) float2 sums[2][kWaves][64 * V];
     __shared__ float carry[2][64 * V];
@@ -165,7 +172,6 @@ template <typename T, int V, bool DENSE, bool SUMS> __global__ __launch_bounds__
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lv = (threadIdx.x & 63) * V;
     const GatedAt at = gated_at(p, blockIdx.x);
     const uint32_t block = blockIdx.x - (uint32_t)at.part * p.blocks;
-    if (at.ch < 0 || (SUMS && at.ch == at.nch - 1)) return;
     const LaneAt<V> lane(p, block);
     const int64_t c = lane.c;
     const RowsAt<T, V, DENSE> px(p.x, p.xs, at.sp, c, block), pr(p.r, p.rs, at.sp, c, block), pi(p.i, p.is, at.sp, c, block);
@@ -173,17 +179,16 @@ template <typename T, int V, bool DENSE, bool SUMS> __global__ __launch_bounds__
     Raw<T, V> nx[R], nr[R], ni[R];
     const int64_t w0 = at.t0 + wave * R;
     if (at.t0 < at.t1) get_rows(px, w0, at.t1 - 1, nx), get_rows(pr, w0, at.t1 - 1, nr), get_rows(pi, w0, at.t1 - 1, ni);
-    float k2[V], h[V], all[V];
+    float k2[V], h[V];
     get_rate<V>(p, c, k2);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.f, all[v] = 1.f;
-    if (!SUMS && wave == kWaves - 1) {   // this wave carries the state from tile to tile
+    for (int v = 0; v < V; ++v) h[v] = 0.f;
+    if (wave == kWaves - 1) {   // this wave carries the state from tile to tile
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
             if (p.s0) h[v] = p.s0[at.seq * p.s0_n + (c + v) * p.s0_c];
-        fold<V>(p, at.part - at.ch, 1, at.ch, c, h);
-#pragma unroll
-        for (int v = 0; v < V; ++v) carry[0][lv + v] = h[v];
+            carry[0][lv + v] = h[v];
+        }
     }
     int buf = 0;
     for (int64_t t = at.t0; t < at.t1; t += LM_GATED_TILE, buf ^= 1) {
@@ -209,16 +214,6 @@ template <typename T, int V, bool DENSE, bool SUMS> __global__ __launch_bounds__
 #pragma unroll
         for (int v = 0; v < V; ++v) sums[buf][wave][lv + v] = make_float2(P[v], s[v]);
         lds_sync();
-        if constexpr (SUMS) {
-            if (wave != kWaves - 1) continue;
-            for (int w = 0; w < kWaves; ++w)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float2 q = sums[buf][w][lv + v];
-                    h[v] = __builtin_fmaf(q.x, h[v], q.y), all[v] *= q.x;
-                }
-            continue;
-        }
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = carry[buf][lv + v];
         for (int w = 0; w < wave; ++w)
@@ -243,14 +238,175 @@ template <typename T, int V, bool DENSE, bool SUMS> __global__ __launch_bounds__
             for (int v = 0; v < V; ++v) carry[buf ^ 1][lv + v] = h[v];
         }
     }
-    if (wave != kWaves - 1 || !lane.own) return;
-    if constexpr (SUMS) {
+    if (wave != kWaves - 1 || !lane.own || !p.s1) return;
 #pragma unroll
-        for (int v = 0; v < V; ++v) reinterpret_cast<float2 *>(p.sums)[at.part * p.C + c + v] = make_float2(all[v], h[v]);
-    } else if (p.s1 && at.ch == at.nch - 1) {
+    for (int v = 0; v < V; ++v) p.s1[at.seq * p.s1_n + (c + v) * p.s1_c] = h[v];
+}
+
+// Words that tiles leave for those behind them: never all ones, which says that
+// nothing has been left yet.  They carry their own validity, so atomics without
+// an order do.
+constexpr uint64_t kNothing = ~0ull;
+constexpr int kTicket = 16;   // words between tickets: lines of their own
+__device__ __forceinline__ uint64_t word_of(float a, float b)
+{
+    const uint32_t u = a != a ? 0x7fc00000u : __float_as_uint(a);
+    return u | (uint64_t)__float_as_uint(b) << 32;
+}
+__device__ __forceinline__ void leave_word(uint64_t *p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint64_t look(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// A wait is given up after about a second of looks, with NaN for a state, rather
+// than hang.
+constexpr int kPatience = 1 << 20;
+
+__global__ __launch_bounds__(256) void gated_clear(const GatedP p, int64_t words)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, tickets = (int64_t)p.blocks * kTicket;
+    if (i < tickets + words) p.ahead[i] = i < tickets ? 0 : kNothing;
+}
+
+// One tile of a sequence.  Tiles of the same channels are taken by a ticket, so
+// those that a tile waits for have been started before it, and each leaves its
+// (P, s) before it waits itself: all waits end.
+template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWaves, 8) void gated_tile(const GatedP p)
+{
+    __shared__ __attribute__((aligned(16))) float2 sums[kWaves][64 * V];
+    __shared__ __attribute__((aligned(16))) float2 front[kWaves][64 * V];
+    __shared__ int reach, missing;
+    __shared__ uint32_t ticket;
+    constexpr int R = kFwd;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lv = (threadIdx.x & 63) * V;
+    const uint32_t block = blockIdx.x % p.blocks;
+    if (threadIdx.x == 0) ticket = atomicAdd(reinterpret_cast<uint32_t *>(p.ahead + (int64_t)block * kTicket), 1u);
+    __syncthreads();
+    const GatedAt at = gated_at(p, (uint32_t)__builtin_amdgcn_readfirstlane(ticket) * p.blocks);
+    const LaneAt<V> lane(p, block);
+    const int64_t c = lane.c, tw = at.t0 + wave * R;
+    if (at.ch < 0) return;
+    uint64_t *map_of = p.ahead + (int64_t)p.blocks * kTicket + at.part * p.C + c, *end_of = map_of + p.parts * p.C;
+    float a[R][V], b[R][V], P[V], s[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) P[v] = 1.f, s[v] = 0.f;
+    if (at.t0 < at.t1) {
+        const RowsAt<T, V, DENSE> px(p.x, p.xs, at.sp, c, block), pr(p.r, p.rs, at.sp, c, block), pi(p.i, p.is, at.sp, c, block);
+        Raw<T, V> nx[R], nr[R], ni[R];
+        get_rows(pr, tw, at.t1 - 1, nr), get_rows(pi, tw, at.t1 - 1, ni), get_rows(px, tw, at.t1 - 1, nx);
+        float k2[V];
+        get_rate<V>(p, c, k2);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = tw + r < at.t1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float t2 = k2[v] * sigmoid(nr[r].f(v)), f = hw_exp2(t2);
+                const float g = complement(t2, f) * sigmoid(ni[r].f(v)) * nx[r].f(v);
+                a[r][v] = in ? f : 1.f, b[r][v] = in ? g : 0.f;
+                P[v] *= a[r][v], s[v] = __builtin_fmaf(a[r][v], s[v], b[r][v]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[r][v] = 1.f, b[r][v] = 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[wave][lv + v] = make_float2(P[v], s[v]);
+    lds_sync();
+    if (wave == kWaves - 1 && at.ch + 1 < at.nch) {   // the tile's map, for those behind it
+#pragma unroll
+        for (int v = 0; v < V; ++v) P[v] = 1.f, s[v] = 0.f;
+        for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float2 q = sums[w][lv + v];
+                s[v] = __builtin_fmaf(q.x, s[v], q.y), P[v] *= q.x;
+            }
+#pragma unroll
+        for (int v = 0; v < V; ++v) leave_word(map_of + v, word_of(P[v], s[v]));
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = at.ch == 0 && p.s0 ? p.s0[at.seq * p.s0_n + (c + v) * p.s0_c] : 0.f;
+    if (at.ch > 0) {
+        const int near = at.ch < kWaves ? (int)at.ch : kWaves;
+        for (int looks = 0;;) {   // the first wave's count
+            // One channel's words tell how far to reach: to the nearest tile
+            // whose end is there, over tiles whose maps are.
+            if (wave == 0) {
+                const int w = threadIdx.x & 15, back = w < near ? w : near - 1;
+                const uint64_t *of = threadIdx.x & 16 ? map_of : end_of;
+                int to = -1;
+                while (looks++ < kPatience) {
+                    const uint64_t there = __ballot(look(of - (back + 1) * p.C) != kNothing);
+                    const int ends = (int)there & 0xffff & ((1 << near) - 1), maps = (int)(there >> 16) & 0xffff;
+                    to = ends ? __builtin_ctz(ends) : -1;
+                    if (to >= 0 && (maps & ((1 << to) - 1)) == (1 << to) - 1) break;
+                    to = -1;
+                }
+                reach = to, missing = 0;
+            }
+            lds_sync();
+            const int to = __builtin_amdgcn_readfirstlane(reach);
+            if (to < 0) break;
+            if (wave <= to) {
+                const uint64_t *of = (wave < to ? map_of : end_of) - (wave + 1) * p.C;
+                bool here = true;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const uint64_t m = look(of + v);
+                    here = here && m != kNothing;
+                    front[wave][lv + v] = make_float2(__uint_as_float((uint32_t)m), __uint_as_float((uint32_t)(m >> 32)));
+                }
+                if (__ballot(!here) != 0) missing = 1;
+            }
+            lds_sync();
+            const bool again = __builtin_amdgcn_readfirstlane(missing) != 0;
+            if (!again) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = front[to][lv + v].x;
+                for (int w = to - 1; w >= 0; --w)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float2 q = front[w][lv + v];
+                        h[v] = __builtin_fmaf(q.x, h[v], q.y);
+                    }
+                break;
+            }
+            lds_sync();
+        }
+        if (__builtin_amdgcn_readfirstlane(reach) < 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = __builtin_nanf("");
+    }
+    // The end by the map, not by the rows: what a tile behind finds then does
+    // not depend on how far it has had to reach.
+    if (wave == kWaves - 1 && at.ch + 1 < at.nch) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) leave_word(end_of + v, word_of(__builtin_fmaf(P[v], h[v], s[v]), 0.f));
+    }
+    for (int w = 0; w < wave; ++w)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 q = sums[w][lv + v];
+            h[v] = __builtin_fmaf(q.x, h[v], q.y);
+        }
+    if (p.saved && lane.own && (wave * R) % LM_GATED_SAVE == 0 && tw < at.t1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.saved[(at.first + tw / LM_GATED_SAVE) * p.C + c + v] = h[v];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = b[r][v] = __builtin_fmaf(a[r][v], h[v], b[r][v]);
+    if (wave == kWaves - 1 && at.ch == at.nch - 1 && p.s1 && lane.own) {
 #pragma unroll
         for (int v = 0; v < V; ++v) p.s1[at.seq * p.s1_n + (c + v) * p.s1_c] = h[v];
     }
+    if (!p.y || !lane.own) return;
+    const RowsAt<T, V, DENSE> py(p.y, p.ys, at.sp, c, block);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (tw + r < at.t1) put<T, V>(py.row(tw + r), b[r]);
 }
 
 // --------------------------------------------------------------- backward --
@@ -529,7 +685,7 @@ GatedP base(const lm_plan_t &p, lm_ptrs q, void *ws)
     a.blocks = (uint32_t)lm_cdiv(p.C, 64 * gated_width(p));
     a.state_rows = p.t[LM_STATE_OUT].sizes[0];
     a.value = p.args.value;
-    a.sums = static_cast<float *>(ws);
+    a.ahead = static_cast<uint64_t *>(ws), a.sums = static_cast<float *>(ws);
     a.part = a.sums + (p.chunks > 1 ? 2 * a.parts * p.C : 0);
     return a;
 }
@@ -564,8 +720,11 @@ int launch_lm_gated(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
         typedef decltype(t) T;
         constexpr int V = decltype(v)::value;
         constexpr bool D = decltype(dense)::value;
-        if (a.chunks > 1) gated_fwd<T, V, D, true><<<groups, 64 * kWaves, 0, s>>>(a);
-        gated_fwd<T, V, D, false><<<groups, 64 * kWaves, 0, s>>>(a);
+        if (a.chunks > 1) {
+            const int64_t words = 2 * a.parts * a.C;
+            gated_clear<<<(unsigned)lm_cdiv(words + (int64_t)a.blocks * kTicket, 256), 256, 0, s>>>(a, words);
+            gated_tile<T, V, D><<<groups, 64 * kWaves, 0, s>>>(a);
+        } else gated_fwd<T, V, D><<<groups, 64 * kWaves, 0, s>>>(a);
     });
     return lm_launch_status();
 }

@@ -87,6 +87,7 @@ inline int mv4_parts(const lm_plan_t &p)
 // channels of a thread (two of 16 bits make a word; other memory orders take
 // one, as do single channels).
 constexpr int LM_GATED_TILE = 128, LM_GATED_SAVE = 64;
+inline bool gated_look(const lm_plan_t &p) { return p.op == LM_GATED && p.chunks > 1; }   // tile by tile over the axis
 inline int gated_width(const lm_plan_t &p)
 {
     if (p.dtype == CONV_F32 || p.C < 2) return 1;
@@ -112,8 +113,9 @@ inline int64_t norm_bwd_groups(const lm_plan_t &p)
 // Adapters: rows of a workgroup (1: those of its row's adapter, gathered),
 // tiles of that many (sorted by adapter, so each may leave one short), parts of
 // the columns of x, 256s of outputs of a workgroup, width of a row of inner sums.
-// About one workgroup for each compute unit: with two of them adapters_out took
-// 55 us for 50 of 8192 rows and outputs, adapters_in 26 for 21 at rank 64.
+// About one workgroup of adapters_in for each compute unit (with two it took 26
+// us for 21 of 4096 rows and rank 64) and three of adapters_out (8192 rows and
+// outputs, rank 32: 70 us; with one 79, two 73, four 70).
 constexpr int LM_MAX_RANK = 256, LM_ADAPTER_N = 256, LM_ADAPTER_FEW = 512, LM_ADAPTER_TILE = 64;
 struct AdapterShape { int rows, parts, reps, width; int64_t tiles; };
 inline AdapterShape adapter_shape(const lm_plan_t &p)
@@ -126,7 +128,7 @@ inline AdapterShape adapter_shape(const lm_plan_t &p)
     const int64_t groups = std::max<int64_t>(1, few ? std::min(p.seqs, p.G + p.seqs / 16) : lm_cdiv(p.seqs, s.rows));
     s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({lm_cdiv(256, groups), lm_cdiv(p.K, 256), 16}));
     const int64_t blocks = std::max<int64_t>(1, lm_cdiv(p.C, LM_ADAPTER_N)), halves = 2 * groups;
-    const int64_t spans = std::max<int64_t>(1, std::min<int64_t>(blocks, (256 + halves / 2) / halves));
+    const int64_t spans = std::max<int64_t>(1, std::min<int64_t>(blocks, (768 + halves / 2) / halves));
     s.reps = few ? 1 : (int)lm_cdiv(blocks, spans);
     s.width = (int)lm_cdiv(p.S, 32) * 32;
     return s;

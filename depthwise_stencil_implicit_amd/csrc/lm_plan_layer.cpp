@@ -10,26 +10,35 @@ namespace {
 // The grids' threads, in double: sizes may be any.
 bool fits(double groups, double size) { return std::ceil(groups) * size < 4294967296.0; }
 
-// Rows per chunk and chunks per sequence of the recurrence.  One workgroup
-// walks 64 V channels of a chunk and keeps a compute unit's memory path and
-// vector unit about two thirds busy, so 256 of them fill the chip.  Fewer are
-// split along the axis, at the price of a first pass over the chunks for what
-// leaves them, which reads what the main pass reads but writes nothing
-// (three quarters of its time).  A workgroup's start costs about a tile.
+// Rows per chunk and chunks per sequence of the recurrence.  A workgroup walks
+// 64 V channels of a sequence, about 4 us a tile while fewer than 256 of them
+// share the memory, and 0.03 us for each that runs when all do.
+//
+// Forward: where whole sequences leave units idle, every tile is a workgroup of
+// its own (a chunk of a tile's rows), for the same 0.03 us and 8 to begin with.
+// Backward: chunks by the least estimated time; what enters them takes a pass
+// over two of seven tensors and a workgroup's start about a tile.
 void gated_chunks(lm_plan_t &p, int64_t max_len)
 {
-    const int64_t blocks = lm_cdiv(p.C, 64 * gated_width(p)), tile = LM_GATED_TILE;
+    const int64_t blocks = lm_cdiv(p.C, 64 * gated_width(p)), tile = LM_GATED_TILE, len = std::max<int64_t>(max_len, 1);
     const bool packed = p.t[LM_OFFSETS].rank > 0;
     int64_t rows = forced_rows(p, max_len);
-    if (rows <= 0) {
-        const int64_t len = std::max<int64_t>(max_len, 1);
+    if (rows > 0) {
+        if (p.op == LM_GATED && rows < len) rows = tile;
+    } else if (p.op == LM_GATED) {
+        const double groups = (double)p.seqs * blocks;
+        const double tiles = (packed ? (double)p.L / tile + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(len, tile)) * blocks;
+        // Packed sequences are of unlike lengths: the longest one counts, and all of them together.
+        const double walk = std::max((double)lm_cdiv(len, tile) * 4, 0.03 * tiles * (packed ? 1 : std::ceil(groups / 256) / (groups / 256)));
+        rows = len > tile && walk > 0.03 * tiles + 8 ? tile : len;
+    } else {
         double best = 0;
         for (int64_t n = 1; n <= 256; ++n) {
             const int64_t chunk = lm_cdiv(lm_cdiv(len, n), tile) * tile;
             if (n > 1 && chunk < 2 * tile) break;
             const double groups = (packed && n > 1 ? (double)p.L / chunk + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(len, chunk)) * blocks;
             const double per_cu = packed ? std::max(1.0, groups / 256) : std::ceil(groups / 256);
-            const double cost = per_cu * (chunk + tile) * (n > 1 ? 1.75 : 1.0) + (n > 1 ? tile : 0);
+            const double cost = per_cu * (chunk + tile) * (n > 1 ? 1.3 : 1.0) + (n > 1 ? tile : 0);
             if (n == 1 || cost < best) best = cost, rows = chunk;
         }
     }
@@ -84,10 +93,10 @@ int plan_gated(int op, Checker &k, const lm_args &args, lm_plan_t &p)
         if (k.status == CONV_OK && k.has(LM_SAVED) && k.t[LM_SAVED].strides[0] != 1 && p.saved_floats > 1) k.fail(CONV_EINVAL, "saved has to be contiguous");
         if (k.status != CONV_OK) return k.status;
         const int64_t parts = lm_parts(p);
-        p.workspace_bytes = 4 * p.C * ((p.chunks > 1 ? 2 * parts : 0) + (bwd ? parts : 0));
+        p.workspace_bytes = gated_look(p) ? 16 * parts * p.C + 128 * lm_cdiv(p.C, 64 * gated_width(p)) : 4 * p.C * ((p.chunks > 1 ? 2 * parts : 0) + (bwd ? parts : 0));
     }
     const double groups = (double)lm_parts(p) * std::ceil((double)p.C / (64 * gated_width(p)));
-    if (!(step ? fits((double)N * p.C / gated_width(p) / 256, 256) : fits(groups, 1024)) || !fits((double)p.C / 64, 1024) ||
+    if (!(step ? fits((double)N * p.C / gated_width(p) / 256, 256) : fits(groups, 1024) && (!gated_look(p) || fits(2 * (double)(lm_parts(p) + 16) * p.C, 1))) || !fits((double)p.C / 64, 1024) ||
         lm_parts(p) >= 0x7fffffff)
         return k.fail(CONV_EUNSUPPORTED, "too many rows for one launch"), k.status;
     const int64_t states = (step ? 2 : k.has(LM_STATE_IN) + k.has(LM_STATE_OUT)) + k.has(LM_GSTATE) + k.has(LM_DSTATE);

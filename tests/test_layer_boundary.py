@@ -159,7 +159,7 @@ def test_packed_workspace_follows_the_rows(seqs, t, c, max_len):
     x = m(1, c, t)
     ins = {lm._X: x, lm._A: x, lm._B: x, lm._D: m(c, d=F), lm._OFF: m(seqs + 1, d=I32)}
     p = lm._make_plan(A.LM_GATED, {**ins, lm._Y: x}, max_len=max_len, value=8.0)
-    assert p.workspace_bytes <= (t // p.chunk + seqs) * 8 * c
+    assert p.workspace_bytes <= (t // p.chunk + seqs) * 16 * c + 2 * c
     p = lm._make_plan(A.LM_GATED_BWD, {**ins, lm._GY: x, lm._DX: x, lm._DA: x, lm._DB: x, lm._DD: m(c, d=F),
                                        lm._SAVED: m((t // 64 + seqs + 1) * c, d=F)}, max_len=max_len, value=8.0)
     assert p.workspace_bytes <= (t // p.chunk + seqs) * 12 * c
