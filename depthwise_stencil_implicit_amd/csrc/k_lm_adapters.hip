@@ -31,10 +31,9 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = LM_ADAPTER_TILE;   // rows of a sorted tile
 constexpr int kUnit = 64;            // columns that a wave takes at a time: whole lines of 16-bit rows
-constexpr int kRanks = 64;           // of an inner product's workgroup, and of a staged piece
+constexpr int kRanks = 64;           // of an inner product's workgroup
 constexpr int kOutRows = 2;          // sixteens of rows of adapters_out's tile
 constexpr int kOut = LM_ADAPTER_N;   // outputs of a workgroup at a time
-constexpr int kStride = kRanks + 8;  // of a staged row: 16-byte reads of 8 rows on different banks
 
 struct AdapterP {
     const void *x, *a, *b, *base;
@@ -94,22 +93,28 @@ __device__ __forceinline__ void load_both(const f8_t *p, Oct8 &a, Oct8 &b)
     const Bytes v = *reinterpret_cast<const Bytes *>(p);
     a = {{v.w[0], v.w[1]}}, b = {{v.w[2], v.w[3]}};
 }
-// The first n of V values, any distance apart; the rest zero.
+// The first n of V values, any distance apart; the rest, all of them for an n
+// below one, zero.  There is an (n - 1)th value at p in any case, which loads
+// past the end repeat: behind branches they would be waited for one by one.
 template <int V, typename T> __device__ __forceinline__ Raw<T, V> load_some(const T *p, int64_t step, int n)
 {
+    T v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[(i < n ? i : n - 1) * step];
     Raw<T, V> r;
     r.zero();
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i < n) r.set(i, p[i * step]);
+    for (int i = 0; i < V; ++i) r.set(i, i < n ? v[i] : T{});
     return r;
 }
 template <int V> __device__ __forceinline__ Oct8 load_some(const f8_t *p, int64_t step, int n)
 {
+    uint8_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[(i < n ? i : n - 1) * step].u;
     Oct8 r = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) r.w[i / 4] |= (uint32_t)p[i * step].u << (i % 4 * 8);
+    for (int i = 0; i < 8; ++i) r.w[i / 4] |= (uint32_t)(i < n ? v[i] : 0) << (i % 4 * 8);
     return r;
 }
 // Four values past the L2's lines in use: the kernel does not read them again.
@@ -444,13 +449,14 @@ template <typename T, typename U> __device__ __forceinline__ void mma_terms(cons
 
 // A wave takes 64 outputs at a time: a lane's four neighbours of four rows per
 // sixteen, so that sixteen lanes read and write a line of a 16-bit row.
-// KS: 32s of ranks staged for good; 0: more than 64 of them, staged in turn.
+// KS: 32s of ranks; 0: any number of them, their weights loaded in turn.
 template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void adapters_out(const AdapterP p)
 {
     typedef typename TermOf<T>::type U;
     constexpr bool GATHER = MF == 1;
     constexpr int NT = TermOf<T>::n, MR = 16 * MF, NQ = 4;
-    __shared__ __attribute__((aligned(16))) U terms[NT][MR * kStride];
+    constexpr int RANKS = KS ? kRanks : LM_MAX_RANK, STRIDE = RANKS + 8;   // 16-byte reads of 8 rows on different banks
+    __shared__ __attribute__((aligned(16))) U terms[NT][MR * STRIDE];
     __shared__ int list[MR];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int quad = lane >> 4, col = lane & 15;
@@ -505,13 +511,17 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
                 for (int j = 0; j < 4; ++j) v[j] = (p.base ? o[m][i].f(j) : 0.f) + acc[m][j][i];
                 if (DENSE && n + 4 <= p.N) store_piece(y + yo[m][i] + n, v);
                 else {
-                    // The last piece of a row was loaded from its end.
+                    if (DENSE && p.base && n < p.N) {   // the last piece of a row was loaded from its end
+                        const int by = n - (p.N - 4);
+#pragma unroll
+                        for (int j = 0; j < 3; ++j) {
+                            const float f = by == 1 ? o[m][i].f(j + 1) : by == 2 ? o[m][i].f(j + 2 < 4 ? j + 2 : 3) : o[m][i].f(3);
+                            v[j] = f + acc[m][j][i];
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (n + j < p.N) {
-                            if (DENSE) v[j] = (p.base ? to_f32(base[bo[m][i] + n + j]) : 0.f) + acc[m][j][i];
-                            y[yo[m][i] + (n + j) * p.ys.c] = from_f32<T>(v[j]);
-                        }
+                        if (n + j < p.N) y[yo[m][i] + (n + j) * p.ys.c] = from_f32<T>(v[j]);
                 }
             }
     };
@@ -544,45 +554,53 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
             else o[q] = load_some<8>(b + n * p.bs.c + rank * p.bs.l, p.bs.l, p.R - rank);
         }
     };
-    // The parts' sums of the rows from rank0 on, scaled and cut into terms.
-    const auto stage = [&](int rank0) {
-        for (int i = threadIdx.x; i < MR * (kRanks / 4); i += 64 * kWaves) {
-            const int r = i / (kRanks / 4), c = i % (kRanks / 4) * 4;
+    // The parts' sums of the rows, scaled and cut into terms.
+    const auto stage = [&]() {
+        const int quads = p.width / 4;
+        for (int i = threadIdx.x; i < MR * quads; i += 64 * kWaves) {
+            const int r = i / quads, c = i % quads * 4;
             f32x4 v = {};
-            if (set >> r & 1 && rank0 + c < p.R) {
+            if (set >> r & 1 && c < p.R) {
                 const int row = group.row(r);
-                const float *t = p.t + (int64_t)row * p.width + rank0 + c;
+                const float *t = p.t + (int64_t)row * p.width + c;
                 const float f = p.scales ? gain * p.scales[row_at(p, p.scs, row)] : gain;
-#pragma unroll 4
-                for (int s = 0; s < p.parts; ++s) v += *reinterpret_cast<const f32x4 *>(t + (int64_t)s * p.rows * p.width);
+                constexpr int AT_ONCE = GATHER ? 16 : 4;   // all of a short call's, which waits for them
+                for (int s0 = 0; s0 < p.parts; s0 += AT_ONCE) {
+                    f32x4 u[AT_ONCE];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = rank0 + c + j < p.R ? v[j] * f : 0.f;
+                    for (int s = 0; s < AT_ONCE; ++s)
+                        u[s] = *reinterpret_cast<const f32x4 *>(t + (int64_t)(s0 + s < p.parts ? s0 + s : 0) * p.rows * p.width);
+#pragma unroll
+                    for (int s = 0; s < AT_ONCE; ++s) v += s0 + s < p.parts ? u[s] : f32x4{};
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = c + j < p.R ? v[j] * f : 0.f;
             }
-            if constexpr (NT == 1) *reinterpret_cast<f32x4 *>(&terms[0][r * kStride + c]) = v;
+            if constexpr (NT == 1) *reinterpret_cast<f32x4 *>(&terms[0][r * STRIDE + c]) = v;
             else {
                 uint16_t o[4][3];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) split(v[j], o[j]);
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
-                    *reinterpret_cast<uint2 *>(&terms[s][r * kStride + c]) =
+                    *reinterpret_cast<uint2 *>(&terms[s][r * STRIDE + c]) =
                         uint2{o[0][s] | (uint32_t)o[1][s] << 16, o[2][s] | (uint32_t)o[3][s] << 16};
             }
         }
     };
     // acc += the staged terms from k on times the weights o.  Ranks past the
     // last are zeros in the terms; weights there are an earlier rank's.
-    const auto multiply = [&](const Raw<T, 8> (&o)[NQ], int k, int rank, f32x4 (&acc)[MF][NQ]) {
+    const auto multiply = [&](const Raw<T, 8> (&o)[NQ], int k, f32x4 (&acc)[MF][NQ]) {
         Frag<U> t[MF][NT];
 #pragma unroll
         for (int m = 0; m < MF; ++m)
 #pragma unroll
             for (int s = 0; s < NT; ++s)
-                __builtin_memcpy(&t[m][s], __builtin_assume_aligned(&terms[s][(m * 16 + col) * kStride + k + quad * 8], 16), sizeof(t[m][s]));
+                __builtin_memcpy(&t[m][s], __builtin_assume_aligned(&terms[s][(m * 16 + col) * STRIDE + k + quad * 8], 16), sizeof(t[m][s]));
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             Raw<T, 8> w = o[q];
-            if (rank + quad * 8 >= p.R) w.zero();
+            if (k + quad * 8 >= p.R) w.zero();
             const Weights<T> wf = weights_of<T>(w);
 #pragma unroll
             for (int m = 0; m < MF; ++m) mma_terms<T, U>(wf, t[m], acc[m][q]);
@@ -598,13 +616,13 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
         const auto finish = [&](int i, const Raw<T, 4> (&os)[MF][4]) {
             f32x4 acc[MF][NQ] = {};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) multiply(w[k], k * 32, k * 32, acc);
+            for (int k = 0; k < KS; ++k) multiply(w[k], k * 32, acc);
             __builtin_amdgcn_sched_barrier(0);
             get_all(place(i + 1));
             leave(place(i), os, acc);
         };
         get_all(place(0)), get_base(place(0), o[0]);
-        stage(0);
+        stage();
         __syncthreads();
         for (int i = 0; i < blocks; i += 2) {
             get_base(place(i + 1), o[1]);
@@ -616,21 +634,24 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
             finish(i + 1, o[1]);
         }
     } else {
-        // The waves stay together: all of them stage for each 64 outputs.
+        stage();
+        __syncthreads();
         for (int i = 0; i < blocks; ++i) {
             const int n0 = place(i);
-            f32x4 acc[MF][NQ] = {};
-            for (int rank0 = 0; rank0 < p.R; rank0 += kRanks) {
-                __syncthreads();
-                stage(rank0);
-                __syncthreads();
-                for (int k = 0; k < kRanks && rank0 + k < p.R; k += 32) {
-                    Raw<T, 8> w[NQ];
-                    get_weights(n0, rank0 + k + quad * 8, w), multiply(w, k, rank0 + k, acc);
-                }
-            }
             Raw<T, 4> o[MF][4];
-            get_base(n0, o), leave(n0, o, acc);
+            if constexpr (DENSE) get_base(n0, o);
+            f32x4 acc[MF][NQ] = {};
+            Raw<T, 8> w[2][NQ];
+            get_weights(n0, quad * 8, w[0]);
+            for (int k = 0; k < p.R; k += 64) {
+                if (k + 32 < p.R) get_weights(n0, k + 32 + quad * 8, w[1]);
+                multiply(w[0], k, acc);
+                if (k + 32 >= p.R) break;
+                if (k + 64 < p.R) get_weights(n0, k + 64 + quad * 8, w[0]);
+                multiply(w[1], k + 32, acc);
+            }
+            if constexpr (!DENSE) get_base(n0, o);
+            leave(n0, o, acc);
         }
     }
 }

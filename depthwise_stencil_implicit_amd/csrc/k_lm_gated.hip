@@ -121,12 +121,18 @@ template <typename T, int V, bool DENSE> struct RowsAt {
 template <typename T, int V> __device__ __forceinline__ void put(T *p, const float (&v)[V]) { store_f32<T, V>(p, v); }
 
 // Rows t .. t + R - 1, those past the last one repeated: a load behind a branch
-// would be waited for where the paths meet.
+// would be waited for where the paths meet.  One address after the other: a
+// product for each row kept the scalar unit busy for half of a tile's time.
 template <typename T, int V, bool DENSE, int R>
 __device__ __forceinline__ void get_rows(const RowsAt<T, V, DENSE> &p, int64_t t, int64_t last, Raw<T, V> (&o)[R])
 {
+    const int left = last - t < R ? (int)(last - t) : R;
+    const T *row = p.base + (left < 0 ? last : t) * p.step;
 #pragma unroll
-    for (int r = 0; r < R; ++r) o[r] = load_raw<T, V>(p.row(t + r < last ? t + r : last));
+    for (int r = 0; r < R; ++r) {
+        o[r] = load_raw<T, V>(reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + p.at));
+        row += r < left ? p.step : 0;
+    }
 }
 
 // -k log2(e) of a lane's channels.
@@ -135,12 +141,13 @@ template <int V> __device__ __forceinline__ void get_rate(const GatedP &p, int64
 #pragma unroll
     for (int v = 0; v < V; ++v) k2[v] = -kLog2e * p.value * softplus(p.decay[(c + v) * p.decay_c]);
 }
-// sqrt(1 - a^2) for t2 = log2(a) <= 0.
+// sqrt(1 - a^2) for t2 = log2(a) <= 0: with u = -2 ln2 t2, u - u^2/2 + u^3/6 -
+// u^4/24 where u < 1/16.
 __device__ __forceinline__ float complement(float t2, float a)
 {
-    const float u = -2.f * kLn2 * t2;
-    const float series = u * __builtin_fmaf(-u, __builtin_fmaf(-u, __builtin_fmaf(u, -1.f / 24, 1.f / 6), 0.5f), 1.f);
-    return __builtin_amdgcn_sqrtf(u < 0.0625f ? series : __builtin_fmaf(-a, a, 1.f));
+    constexpr float c = 2.f * kLn2;
+    const float series = t2 * __builtin_fmaf(t2, __builtin_fmaf(t2, __builtin_fmaf(t2, -c * c * c * c / 24, -c * c * c / 6), -c * c / 2), -c);
+    return __builtin_amdgcn_sqrtf(t2 > -0.0625f / c ? series : __builtin_fmaf(-a, a, 1.f));
 }
 
 // v through the maps (P, s) of `count` chunks from `first` on, eight loads at a
@@ -159,6 +166,30 @@ template <int V> __device__ __forceinline__ void fold(const GatedP &p, int64_t f
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] = j + i < count ? __builtin_fmaf(m[i][v].x, o[v], m[i][v].y) : o[v];
     }
+}
+
+// a and sqrt(1 - a^2) sigmoid(i) x of rows from t on, and their map: P and s go
+// on from what they are.  Rows past the end leave everything as it is; a walk
+// meets them in its last tile only.
+template <int R, bool WALK, typename T, int V>
+__device__ __forceinline__ void factors(const Raw<T, V> (&x)[R], const Raw<T, V> (&r)[R], const Raw<T, V> (&i)[R], const float (&k2)[V],
+                                        int64_t t, int64_t end, float (&a)[R][V], float (&b)[R][V], float (&P)[V], float (&s)[V])
+{
+    const auto work = [&](auto cut) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const bool in = !decltype(cut)::value || t + j < end;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float t2 = k2[v] * sigmoid(r[j].f(v)), f = hw_exp2(t2);
+                const float g = complement(t2, f) * sigmoid(i[j].f(v)) * x[j].f(v);
+                a[j][v] = in ? f : 1.f, b[j][v] = in ? g : 0.f;
+                P[v] *= a[j][v], s[v] = __builtin_fmaf(a[j][v], s[v], b[j][v]);
+            }
+        }
+    };
+    if (WALK && t + R <= end) work(std::false_type());
+    else work(std::true_type());
 }
 
 // ---------------------------------------------------------------- forward --
@@ -196,17 +227,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
         float a[R][V], b[R][V], P[V], s[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) P[v] = 1.f, s[v] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = tw + r < at.t1;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float t2 = k2[v] * sigmoid(nr[r].f(v)), f = hw_exp2(t2);
-                const float g = complement(t2, f) * sigmoid(ni[r].f(v)) * nx[r].f(v);
-                a[r][v] = in ? f : 1.f, b[r][v] = in ? g : 0.f;
-                P[v] *= a[r][v], s[v] = __builtin_fmaf(a[r][v], s[v], b[r][v]);
-            }
-        }
+        factors<R, true>(nx, nr, ni, k2, tw, at.t1, a, b, P, s);
         if (t + LM_GATED_TILE < at.t1) {
             const int64_t n = tw + LM_GATED_TILE;
             get_rows(px, n, at.t1 - 1, nx), get_rows(pr, n, at.t1 - 1, nr), get_rows(pi, n, at.t1 - 1, ni);
@@ -293,17 +314,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
         get_rows(pr, tw, at.t1 - 1, nr), get_rows(pi, tw, at.t1 - 1, ni), get_rows(px, tw, at.t1 - 1, nx);
         float k2[V];
         get_rate<V>(p, c, k2);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = tw + r < at.t1;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float t2 = k2[v] * sigmoid(nr[r].f(v)), f = hw_exp2(t2);
-                const float g = complement(t2, f) * sigmoid(ni[r].f(v)) * nx[r].f(v);
-                a[r][v] = in ? f : 1.f, b[r][v] = in ? g : 0.f;
-                P[v] *= a[r][v], s[v] = __builtin_fmaf(a[r][v], s[v], b[r][v]);
-            }
-        }
+        factors<R, false>(nx, nr, ni, k2, tw, at.t1, a, b, P, s);
     } else {
 #pragma unroll
         for (int r = 0; r < R; ++r)

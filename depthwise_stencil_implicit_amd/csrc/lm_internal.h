@@ -127,9 +127,10 @@ inline AdapterShape adapter_shape(const lm_plan_t &p)
     // Workgroups with work: gathered, one for each adapter and each 16 rows.
     const int64_t groups = std::max<int64_t>(1, few ? std::min(p.seqs, p.G + p.seqs / 16) : lm_cdiv(p.seqs, s.rows));
     s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({lm_cdiv(256, groups), lm_cdiv(p.K, 256), 16}));
-    const int64_t blocks = std::max<int64_t>(1, lm_cdiv(p.C, LM_ADAPTER_N)), halves = 2 * groups;
-    const int64_t spans = std::max<int64_t>(1, std::min<int64_t>(blocks, (768 + halves / 2) / halves));
-    s.reps = few ? 1 : (int)lm_cdiv(blocks, spans);
+    const int64_t most = p.S <= 32 ? 768 : 384;   // the more ranks, the longer what each of them does first
+    const int64_t blocks = std::max<int64_t>(1, lm_cdiv(p.C, LM_ADAPTER_N)), with_work = few ? groups : 2 * groups;
+    const int64_t spans = std::max<int64_t>(1, std::min<int64_t>(blocks, (most + with_work / 2) / with_work));
+    s.reps = (int)lm_cdiv(blocks, spans);
     s.width = (int)lm_cdiv(p.S, 32) * 32;
     return s;
 }

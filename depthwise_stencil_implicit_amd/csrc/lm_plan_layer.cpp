@@ -10,14 +10,16 @@ namespace {
 // The grids' threads, in double: sizes may be any.
 bool fits(double groups, double size) { return std::ceil(groups) * size < 4294967296.0; }
 
-// Rows per chunk and chunks per sequence of the recurrence.  A workgroup walks
-// 64 V channels of a sequence, about 4 us a tile while fewer than 256 of them
-// share the memory, and 0.03 us for each that runs when all do.
+// Rows per chunk and chunks per sequence of the recurrence.
 //
-// Forward: where whole sequences leave units idle, every tile is a workgroup of
-// its own (a chunk of a tile's rows), for the same 0.03 us and 8 to begin with.
+// Forward: a workgroup that walks down whole sequences takes 6 us a tile, or its
+// share of the memory where more than 210 of them run (0.0285 us for each).
+// Every tile a workgroup of its own takes 0.036 us for each tile and 12 to begin
+// with: 8 x 2048 x 2048 in 85 us for 101, 12 x 2048 x 2048 in 187 for 109.
 // Backward: chunks by the least estimated time; what enters them takes a pass
-// over two of seven tensors and a workgroup's start about a tile.
+// over two of seven tensors, and a workgroup's start about a tile (8 x 2048 x
+// 2048: whole 186 us, chunks of 1024 and 512 rows 136; 1 x 1024 x 4096: whole
+// 330, 256 rows 41, 128 rows 29).
 void gated_chunks(lm_plan_t &p, int64_t max_len)
 {
     const int64_t blocks = lm_cdiv(p.C, 64 * gated_width(p)), tile = LM_GATED_TILE, len = std::max<int64_t>(max_len, 1);
@@ -29,17 +31,17 @@ void gated_chunks(lm_plan_t &p, int64_t max_len)
         const double groups = (double)p.seqs * blocks;
         const double tiles = (packed ? (double)p.L / tile + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(len, tile)) * blocks;
         // Packed sequences are of unlike lengths: the longest one counts, and all of them together.
-        const double walk = std::max((double)lm_cdiv(len, tile) * 4, 0.03 * tiles * (packed ? 1 : std::ceil(groups / 256) / (groups / 256)));
-        rows = len > tile && walk > 0.03 * tiles + 8 ? tile : len;
+        const double walk = std::max(lm_cdiv(len, tile) * std::max(6.0, packed ? 0 : 0.0285 * groups), 0.0285 * tiles);
+        rows = len > tile && walk > 0.036 * tiles + 12 ? tile : len;
     } else {
         double best = 0;
         for (int64_t n = 1; n <= 256; ++n) {
             const int64_t chunk = lm_cdiv(lm_cdiv(len, n), tile) * tile;
-            if (n > 1 && chunk < 2 * tile) break;
             const double groups = (packed && n > 1 ? (double)p.L / chunk + 0.5 * p.seqs : (double)p.seqs * lm_cdiv(len, chunk)) * blocks;
             const double per_cu = packed ? std::max(1.0, groups / 256) : std::ceil(groups / 256);
             const double cost = per_cu * (chunk + tile) * (n > 1 ? 1.3 : 1.0) + (n > 1 ? tile : 0);
             if (n == 1 || cost < best) best = cost, rows = chunk;
+            if (chunk == tile) break;
         }
     }
     p.chunk = lm_cdiv(rows, tile) * tile;
