@@ -449,8 +449,12 @@ template <typename T, typename U> __device__ __forceinline__ void mma_terms(cons
 
 // A wave takes 64 outputs at a time: a lane's four neighbours of four rows per
 // sixteen, so that sixteen lanes read and write a line of a 16-bit row.
-// KS: 32s of ranks; 0: any number of them, their weights loaded in turn.
-template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void adapters_out(const AdapterP p)
+// KS: 32s of ranks; 0: any number of them, their weights loaded in turn.  DENSE:
+// outputs are contiguous, and each one's weights.  OCTS: ranks are a multiple of
+// eight; if not, eight weights from one on may belong to the outputs behind, are
+// loaded all the same, and masked when they are used (one by one they made rank
+// 4 of 4096 x 4096 take 64 us for 20 at rank 8).
+template <typename T, int MF, int KS, bool DENSE, bool OCTS> __global__ __launch_bounds__(64 * kWaves) void adapters_out(const AdapterP p)
 {
     typedef typename TermOf<T>::type U;
     constexpr bool GATHER = MF == 1;
@@ -542,6 +546,8 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
         return;
     }
     const T *b = static_cast<const T *>(p.b) + e * p.bs.n;
+    // Where the last eight weights of all adapters start, from this one's first.
+    const int64_t last = (p.E - 1 - e) * p.bs.n + (p.N - 1) * p.bs.c + p.R - 8;
     const float gain = p.scaling ? p.scaling[e * p.scaling_e] : 1.f;
     // Weights for the outputs n0 .. n0 + 63 from `rank` on; tile q
     // of a product has every fourth output from n0 + q on.
@@ -550,8 +556,11 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
         for (int q = 0; q < NQ; ++q) {
             int n = n0 + col * 4 + q;
             n = n < p.N ? n : p.N - 1;
-            if constexpr (DENSE) o[q] = load_oct(b + n * p.bs.c + (rank < p.R ? rank : 0));   // R is a multiple of 8
-            else o[q] = load_some<8>(b + n * p.bs.c + rank * p.bs.l, p.bs.l, p.R - rank);
+            if constexpr (OCTS) o[q] = load_oct(b + n * p.bs.c + (rank < p.R ? rank : 0));
+            else if constexpr (DENSE) {
+                const int64_t at = n * p.bs.c + (rank < p.R ? rank : 0);
+                o[q] = load_oct(b + (at < last ? at : last));
+            } else o[q] = load_some<8>(b + n * p.bs.c + rank * p.bs.l, p.bs.l, p.R - rank);
         }
     };
     // The parts' sums of the rows, scaled and cut into terms.
@@ -590,7 +599,7 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
     };
     // acc += the staged terms from k on times the weights o.  Ranks past the
     // last are zeros in the terms; weights there are an earlier rank's.
-    const auto multiply = [&](const Raw<T, 8> (&o)[NQ], int k, f32x4 (&acc)[MF][NQ]) {
+    const auto multiply = [&](const Raw<T, 8> (&o)[NQ], int n0, int k, f32x4 (&acc)[MF][NQ]) {
         Frag<U> t[MF][NT];
 #pragma unroll
         for (int m = 0; m < MF; ++m)
@@ -600,7 +609,19 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             Raw<T, 8> w = o[q];
-            if (k + quad * 8 >= p.R) w.zero();
+            const int rank = k + quad * 8;
+            if constexpr (!OCTS && DENSE) {
+                int n = n0 + col * 4 + q;
+                n = n < p.N ? n : p.N - 1;
+                const int64_t over = n * p.bs.c + (rank < p.R ? rank : 0) - last;   // of the last adapter's last outputs
+                if (__ballot(over > 0)) shift_row<T, 8>(w, over > 0 ? (int)over : 0);
+#pragma unroll
+                for (int i = 0; i < w.n; ++i) {
+                    constexpr int per = 4 / sizeof(T);
+                    const int has = p.R - rank - i * per;   // of the word's elements
+                    w.w[i] = has >= per ? w.w[i] : has > 0 ? w.w[i] & 0xffffu : 0u;
+                }
+            } else if (rank >= p.R) w.zero();
             const Weights<T> wf = weights_of<T>(w);
 #pragma unroll
             for (int m = 0; m < MF; ++m) mma_terms<T, U>(wf, t[m], acc[m][q]);
@@ -616,7 +637,7 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
         const auto finish = [&](int i, const Raw<T, 4> (&os)[MF][4]) {
             f32x4 acc[MF][NQ] = {};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) multiply(w[k], k * 32, acc);
+            for (int k = 0; k < KS; ++k) multiply(w[k], place(i), k * 32, acc);
             __builtin_amdgcn_sched_barrier(0);
             get_all(place(i + 1));
             leave(place(i), os, acc);
@@ -645,10 +666,10 @@ template <typename T, int MF, int KS, bool DENSE> __global__ __launch_bounds__(6
             get_weights(n0, quad * 8, w[0]);
             for (int k = 0; k < p.R; k += 64) {
                 if (k + 32 < p.R) get_weights(n0, k + 32 + quad * 8, w[1]);
-                multiply(w[0], k, acc);
+                multiply(w[0], n0, k, acc);
                 if (k + 32 >= p.R) break;
                 if (k + 64 < p.R) get_weights(n0, k + 64 + quad * 8, w[0]);
-                multiply(w[1], k + 32, acc);
+                multiply(w[1], n0, k + 32, acc);
             }
             if constexpr (!DENSE) get_base(n0, o);
             leave(n0, o, acc);
@@ -687,7 +708,10 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     a.in_place = a.base == a.y;
     const bool f8 = p.t[LM_X].dtype == LM_F8;
     const bool dense_in = (a.xs.c == 1 && a.as.l == 1) || p.K == 1;
-    const bool dense_out = a.bs.l == 1 && a.R % 8 == 0 && a.N >= 4 && a.ys.c == 1 && (!a.base || a.bases.c == 1);
+    const bool octs = a.R % 8 == 0;
+    // With strides of their own, ranks that are not eights would need a far last place.
+    const bool runs = a.bs.l == 1 && (octs || (a.bs.c >= a.R && a.bs.n >= (a.N - 1) * a.bs.c + a.R && (a.N - 1) * a.bs.c + a.R >= 8));
+    const bool dense_out = runs && a.N >= 4 && a.ys.c == 1 && (!a.base || a.bases.c == 1);
     const dim3 in((few ? 1 : tiles) * a.groups * a.parts, few ? tiles : 1), out((few ? 1 : tiles_out) * a.spans, few ? tiles_out : 1);
     const auto run = [&](auto t, auto x) {
         typedef decltype(t) T;
@@ -705,14 +729,13 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
                 if (dense_in) ranks(mf, std::true_type());
                 else ranks(mf, std::false_type());
             }
-            const auto ranks_out = [&](auto ks) {
-                constexpr int MO = MF == 1 ? 1 : kOutRows, KS = decltype(ks)::value;
-                if (dense_out) adapters_out<T, MO, KS, true><<<out, 64 * kWaves, 0, s>>>(a);
-                else adapters_out<T, MO, 0, false><<<out, 64 * kWaves, 0, s>>>(a);
-            };
-            if (a.R <= 32) ranks_out(std::integral_constant<int, 1>());
-            else if (a.R <= 64) ranks_out(std::integral_constant<int, 2>());
-            else ranks_out(std::integral_constant<int, 0>());
+            constexpr int MO = MF == 1 ? 1 : kOutRows, size = 64 * kWaves;
+            if (!dense_out) adapters_out<T, MO, 0, false, false><<<out, size, 0, s>>>(a);
+            else if (octs && a.R <= 32) adapters_out<T, MO, 1, true, true><<<out, size, 0, s>>>(a);
+            else if (octs && a.R <= 64) adapters_out<T, MO, 2, true, true><<<out, size, 0, s>>>(a);
+            else if (octs) adapters_out<T, MO, 0, true, true><<<out, size, 0, s>>>(a);
+            else if (a.R <= 32) adapters_out<T, MO, 1, true, false><<<out, size, 0, s>>>(a);
+            else adapters_out<T, MO, 0, true, false><<<out, size, 0, s>>>(a);
         };
         if (few) rows(std::integral_constant<int, 1>());
         else rows(std::integral_constant<int, 4>());

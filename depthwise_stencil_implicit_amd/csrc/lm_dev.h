@@ -134,6 +134,21 @@ template <typename T, int V> __device__ __forceinline__ void load_f32(const T *p
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = r.f(i);
 }
+// The elements from `by` on in front, zeros behind them.
+template <typename T, int V> __device__ __forceinline__ void shift_row(Raw<T, V> &r, int by)
+{
+    constexpr int n = Raw<T, V>::n, per = 4 / sizeof(T);   // words, elements of a word
+    if (per == 2 && (by & 1)) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) r.w[i] = r.w[i] >> 16 | (i + 1 < n ? r.w[i + 1] << 16 : 0);
+    }
+#pragma unroll
+    for (int s = 1; s < n; s *= 2)
+        if (by & s * per) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) r.w[i] = i + s < n ? r.w[i + s] : 0;
+        }
+}
 // ONCE: 16 bytes that the kernel does not read again, past the L2's lines in use.
 template <typename T, int V, bool ONCE = false> __device__ __forceinline__ void store_f32(T *p, const float (&v)[V])
 {

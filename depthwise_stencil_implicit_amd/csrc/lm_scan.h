@@ -72,20 +72,6 @@ __device__ __forceinline__ Raw<T, V> get_row(const T *row, int64_t cs, int64_t c
         return r;
     }
 }
-template <typename T, int V> __device__ __forceinline__ void shift_row(Raw<T, V> &r, int by)
-{
-    constexpr int n = Raw<T, V>::n, per = 4 / sizeof(T);   // words, elements of a word
-    if (per == 2 && (by & 1)) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) r.w[i] = r.w[i] >> 16 | (i + 1 < n ? r.w[i + 1] << 16 : 0);
-    }
-#pragma unroll
-    for (int s = 1; s < n; s *= 2)
-        if (by & s * per) {
-#pragma unroll
-            for (int i = 0; i < n; ++i) r.w[i] = i + s < n ? r.w[i + s] : 0;
-        }
-}
 template <typename T, int V> __device__ __forceinline__ void put_row(T *p, int64_t cs, int n, const float (&v)[V])
 {
     if (cs == 1 && n >= V) store_f32<T, V>(p, v);
