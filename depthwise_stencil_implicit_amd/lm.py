@@ -225,17 +225,18 @@ class _Step:
     one).  A new output belongs to that stream, as if it had been made the
     current one for the call."""
 
-    def __init__(self, op, tensors, shape, ref, flags=0, value=0.0, dtype=None):
+    def __init__(self, op, tensors, shape, ref, flags=0, value=0.0, dtype=None, strides=None):
         self.device = ref.device
         if any(t is not None and not t.is_cuda for t in tensors.values()):
             raise ValueError("the sequence operators run on the GPU only; move tensors to cuda")
         if any(t is not None and t.device != ref.device for t in tensors.values()):
             raise ValueError("tensors on several devices")
         self.shape, self.dtype = shape, dtype or ref.dtype
+        self.strides = strides or torch.empty(shape, device="meta").stride()
         self.plan = _make_plan(op, {**tensors, _Y: self.empty_output()}, flags, value=value)
 
     def empty_output(self) -> torch.Tensor:
-        return torch.empty(self.shape, dtype=self.dtype, device=self.device)
+        return torch.empty_strided(self.shape, self.strides, dtype=self.dtype, device=self.device)
 
     def _launch(self, q, y, stream) -> torch.Tensor:
         dev = self.device.index
@@ -586,11 +587,8 @@ class PreparedAdapters(_Step):
 
     def __init__(self, x, a, b, index, *, base=None, scaling=None, x_scales=None):
         y = _adapters_output(x, a, b)
-        self.strides = y.stride()
-        super().__init__(A.LM_ADAPTERS, {_X: x, _A: a, _B: b, _ROWS: index, _Z: base, _D: scaling, _SCALES: x_scales}, tuple(y.shape), a)
-
-    def empty_output(self) -> torch.Tensor:
-        return torch.empty_strided(self.shape, self.strides, dtype=self.dtype, device=self.device)
+        super().__init__(A.LM_ADAPTERS, {_X: x, _A: a, _B: b, _ROWS: index, _Z: base, _D: scaling, _SCALES: x_scales}, tuple(y.shape), a,
+                         strides=y.stride())
 
     def run(self, x, a, b, index, *, base=None, scaling=None, x_scales=None, y=None, stream: Optional[int] = None) -> torch.Tensor:
         q = _Ptrs()
