@@ -711,7 +711,8 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     const bool octs = a.R % 8 == 0;
     // With strides of their own, ranks that are not eights would need a far last place.
     const bool runs = a.bs.l == 1 && (octs || (a.bs.c >= a.R && a.bs.n >= (a.N - 1) * a.bs.c + a.R && (a.N - 1) * a.bs.c + a.R >= 8));
-    const bool dense_out = runs && a.N >= 4 && a.ys.c == 1 && (!a.base || a.bases.c == 1);
+    // Without a base the loads in its place are of B, which has to have something.
+    const bool dense_out = runs && a.N >= 4 && a.ys.c == 1 && (a.base ? a.bases.c == 1 : a.E > 0);
     const dim3 in((few ? 1 : tiles) * a.groups * a.parts, few ? tiles : 1), out((few ? 1 : tiles_out) * a.spans, few ? tiles_out : 1);
     const auto run = [&](auto t, auto x) {
         typedef decltype(t) T;

@@ -276,9 +276,9 @@ __device__ __forceinline__ uint64_t word_of(float a, float b)
 }
 __device__ __forceinline__ void leave_word(uint64_t *p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ uint64_t look(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-// A wait is given up after about a second of looks, with NaN for a state, rather
-// than hang.
-constexpr int kPatience = 1 << 20;
+// A wait that cannot end (offsets that do not ascend) is given up after this many
+// looks, hundreds of times what a tile takes, with NaN for a state.
+constexpr int kPatience = 1 << 17;
 
 __global__ __launch_bounds__(256) void gated_clear(const GatedP p, int64_t words)
 {

@@ -325,7 +325,7 @@ extern "C" int lm_run(const lm_plan_t *p, void *const *q, void *workspace, size_
         if (reinterpret_cast<uintptr_t>(q[s]) % (uintptr_t)std::max<int64_t>(1, elem(t.dtype))) return CONV_EALIGN;
     }
     if (p->op == LM_MV4 && reinterpret_cast<uintptr_t>(q[LM_W]) % 16) return CONV_EALIGN;
-    if (p->op != LM_MV4 && reinterpret_cast<uintptr_t>(q[LM_SAVED]) % 16) return CONV_EALIGN;
+    if (p->op < LM_MV4 && reinterpret_cast<uintptr_t>(q[LM_SAVED]) % 16) return CONV_EALIGN;   // read as whole vectors
     if (p->workspace_bytes > 0) {
         if (!workspace || workspace_bytes < (size_t)p->workspace_bytes) return CONV_EINVAL;
         if (reinterpret_cast<uintptr_t>(workspace) % 256) return CONV_EALIGN;

@@ -149,9 +149,10 @@ int plan_norm(int op, Checker &k, const lm_args &args, lm_plan_t &p)
     if (k.status != CONV_OK) return k.status;
     if (p.C < 1) return k.fail(CONV_EINVAL, "x has no channels"), k.status;
     if (p.C > LM_NORM_MAX) return k.fail(CONV_EUNSUPPORTED, "%lld channels: 1 to %d are supported", (long long)p.C, LM_NORM_MAX), k.status;
-    const int64_t rows = N * p.L;
     p.chunk = p.chunks = 1;
-    if (!fits((double)N * (double)p.L, 1024)) return k.fail(CONV_EUNSUPPORTED, "too many rows for one launch"), k.status;
+    const double all = (double)N * (double)p.L;
+    const int64_t rows = all < 4294967296.0 ? N * p.L : 0;
+    if (!fits(all, 64) || !fits(all, (double)norm_threads(rows, p.C))) return k.fail(CONV_EUNSUPPORTED, "too many rows for one launch"), k.status;
     if (bwd && k.has(LM_DW)) p.workspace_bytes = norm_bwd_groups(p) * p.C * 4;
     const int64_t cells = rows * p.C;
     p.bytes = bwd ? cells * e * (2 + k.has(LM_GSTATE) + k.has(LM_DX)) + rows * 4 + p.C * e * (1 + k.has(LM_DW))

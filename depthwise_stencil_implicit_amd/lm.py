@@ -611,7 +611,7 @@ def adapters(x, a, b, index, *, base=None, scaling=None, x_scales=None, out=None
     base (zero without it) and the result [M, N'] or [N, N', L]; scaling f32
     [E].  x may be torch.float8_e4m3fn with ``x_scales`` f32 [M, 1] or [N, 1, L],
     as ``rms_norm`` leaves it without groups.  ``out`` may be the base itself.
-    Rows with the same adapter share its pass when they are neighbours."""
+    Rows with the same adapter share its pass, in whatever order they come."""
     y = _adapters_output(x, a, b) if out is None else out
     _call(A.LM_ADAPTERS, [(_X, x), (_A, a), (_B, b), (_ROWS, index), (_Z, base), (_D, scaling), (_SCALES, x_scales)], [(_Y, y)])
     return y

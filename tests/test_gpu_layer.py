@@ -280,6 +280,23 @@ def test_rms_norm_of_extremes():
         assert bool(((back[fine].cpu().double() - y[fine]).abs() <= lim).all())
 
 
+def test_norm_of_many_rows():
+    """More rows than a launch of 1024 threads for each would hold."""
+    rows, C = (1 << 22) + 5, 8
+    x = torch.randn(rows, C, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(BF)
+    w = torch.arange(1, 9, device="cuda").to(BF)
+    got = lm.rms_norm(x, w, save=True)
+    v = x.float()
+    want = v / (v.square().mean(1, keepdim=True) + 1e-6).sqrt() * w.float()
+    # One rounding to bf16, and f32's on both sides.
+    assert bool(((got.y.float() - want).abs() <= (2 ** -8 + 2 ** -19) * want.abs()).all())
+    back = lm.rms_norm_backward(x, x, w, got.rstd)
+    u = v.double() * got.rstd.double()[:, None]
+    dw = (v.double() * u).sum(0)
+    assert bool(((back.dw.double() - dw).abs() <= 2 ** -7 * dw).all())
+    assert torch.equal(back.dx[-3:], lm.rms_norm_backward(x[-3:], x[-3:], w, got.rstd[-3:]).dx)
+
+
 def test_norm_gradients_against_differences():
     g = gen(6)
     x, w, gy, gr = rnd(g, 3, 10), rnd(g, 10), rnd(g, 3, 10), rnd(g, 3, 10)
@@ -325,6 +342,9 @@ ADAPTERS = [
     (BF, 0, 64, 64, 8, 2, "each", True, True, False, "nlc"),
     (BF, 6, 0, 64, 8, 2, "each", True, True, False, "nlc"),
     (BF, 6, 64, 64, 8, 0, "none", True, False, False, "nlc"),
+    (BF, 6, 64, 64, 8, 0, "none", False, False, False, "nlc"),
+    (HF, 600, 64, 66, 12, 0, "none", False, True, False, "nlc"),
+    (F, 600, 64, 66, 16, 3, "none", False, True, False, "nlc"),
 ]
 
 

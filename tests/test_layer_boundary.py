@@ -135,7 +135,7 @@ def test_refusals(i):
 @pytest.mark.parametrize("op,make", [
     (A.LM_GATED, lambda v: {**gated(1, 1, 1), **{k: v(1 << 22, 8192, 1) for k in (lm._X, lm._A, lm._B, lm._Y)}, lm._D: v(8192, d=F), lm._S0: None}),
     (A.LM_GATED_STEP, lambda v: {**{k: v(1 << 20, 16384) for k in (lm._X, lm._A, lm._B, lm._Y)}, lm._D: v(16384, d=F), lm._S1: v(1 << 20, 16384, d=F)}),
-    (A.LM_NORM, lambda v: {lm._X: v(1 << 23, 64), lm._W: v(64), lm._Y: v(1 << 23, 64)}),
+    (A.LM_NORM, lambda v: {lm._X: v(1 << 26, 64), lm._W: v(64), lm._Y: v(1 << 26, 64)}),
     (A.LM_ADAPTERS, lambda v: {lm._X: v(1 << 31, 64), lm._A: v(2, 8, 64), lm._B: v(2, 8, 8), lm._ROWS: v(1 << 31, d=I32), lm._Y: v(1 << 31, 8)}),
     (A.LM_ADAPTERS, lambda v: {lm._X: v(1 << 30, 64), lm._A: v(2, 8, 64), lm._B: v(2, 16, 8), lm._ROWS: v(1 << 30, d=I32), lm._Y: v(1 << 30, 16)}),
 ])
@@ -144,6 +144,13 @@ def test_refuses_what_one_launch_cannot_hold(op, make):
     with pytest.raises(lm.ConvError, match="one launch") as r:
         lm._make_plan(op, t, value=1.0)
     assert r.value.status == A.EUNSUPPORTED
+
+
+@pytest.mark.parametrize("rows,C", [(1 << 23, 64), (1 << 25, 2048), (16 << 20, 4096)])
+def test_norms_of_many_rows(rows, C):
+    """As many as a launch of their threads holds."""
+    m = lambda *s: torch.empty(s, dtype=BF, device="meta")  # noqa: E731
+    lm._make_plan(A.LM_NORM, {lm._X: m(rows - 1, C), lm._W: m(C), lm._Y: m(rows - 1, C)}, value=1.0)
 
 
 @pytest.mark.parametrize("chunk", [101, 1 << 40, (1 << 63) - 40, (1 << 63) - 1])
