@@ -7,13 +7,14 @@
 // part's columns and join in LDS.  adapters_out adds the parts up, keeps them
 // in LDS and multiplies by B[e], 64 outputs per wave at a time.
 //
-// The rows of a workgroup share an adapter.  Of a call of few rows, tokens of
-// many requests in any order, the workgroup of every 16th row that names an
-// adapter gathers those rows by a look at all of index; for more rows
-// adapters_sort, one workgroup, puts them in the adapters' order first and
-// lists tiles of 64 of them.  (Tiles of neighbours, which may name several
-// adapters, took each of them in turn: four changes in 8192 rows made the call
-// 1.3 times as long, tokens among prompts many times.)
+// The rows of a workgroup share an adapter.  Three ways to find them, by the
+// number of rows and adapters (adapter_shape): the workgroup of every 16th row that
+// names an adapter gathers those rows by a look at all of index; tiles of 64 rows
+// in the adapters' order, which each workgroup of adapters_in finds by counting
+// all of index, and lists for the kernel behind; or such tiles that adapters_sort,
+// one workgroup, has listed before.  (Tiles of neighbours, which may name several
+// adapters, took each of them in turn: four changes in 8192 rows made the call 1.3
+// times as long, tokens among prompts many times.)
 //
 // The inner sums stay f32 into the second product: they are cut into three
 // bf16 terms, which hold all 24 bits, against exact weights (f16 weights are
@@ -182,6 +183,71 @@ template <int MR> struct Group<true, MR> {
     }
     __device__ __forceinline__ int row(int r) const { return list[r]; }
 };
+// The group of a tile that nothing has listed yet: of few adapters' rows, each
+// workgroup counts all of index and takes those whose turn it is.  at: the
+// places of one workgroup of each tile, which lists it for the kernel behind.
+struct FoundGroup {
+    uint64_t set;
+    int e;
+    const int *list;
+    __device__ __forceinline__ FoundGroup(const AdapterP &p, int at, bool lists, int *rows) : list(rows)
+    {
+        constexpr int STEPS = LM_ADAPTER_FIND / (64 * kWaves);
+        __shared__ int counts[kWaves][64];
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int per = (p.rows + 64 * kWaves - 1) / (64 * kWaves), from = wave * per * 64;   // steps of a wave; its rows
+        const auto row_of = [&](int s) { return from + s * 64 + lane; };
+        int v[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) v[s] = p.index[row_of(s) < p.rows ? row_of(s) : p.rows - 1];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) v[s] = s >= per || row_of(s) >= p.rows ? -1 : v[s] < 0 || v[s] >= p.E ? p.E : v[s];
+        int count = 0;   // rows of adapter `lane` here; p.E: of none
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            for (uint64_t left = __ballot(v[s] >= 0); left;) {
+                const int now = __builtin_amdgcn_readlane(v[s], __builtin_ctzll(left));
+                const uint64_t same = __ballot(v[s] == now);
+                count += lane == now ? __builtin_popcountll(same) : 0;
+                left &= ~same;
+            }
+        counts[wave][lane] = count;
+        lds_sync();
+        int n = 0, front = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) front += w < wave ? counts[w][lane] : 0, n += counts[w][lane];
+        const int t = (n + kTile - 1) / kTile;
+        int upto = t;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int a = __shfl_up(upto, d);
+            if (lane >= d) upto += a;
+        }
+        const uint64_t mine = __ballot(lane <= p.E && at < upto && at >= upto - t);
+        set = 0;
+        const int all = __builtin_amdgcn_readlane(upto, p.E);
+        if (lists && at == 0 && threadIdx.x == 0) *p.tile_count = all;
+        if (!mine) return;
+        e = __builtin_ctzll(mine);
+        const int first = (at - __builtin_amdgcn_readlane(upto - t, e)) * kTile, left = __builtin_amdgcn_readlane(n, e) - first;
+        const int rows_here = left < kTile ? left : kTile;
+        int place = __builtin_amdgcn_readlane(front, e) - first;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const uint64_t same = __ballot(v[s] == e);
+            const int i = place + __builtin_popcountll(same & ((1ull << lane) - 1));
+            if (v[s] == e && i >= 0 && i < kTile) rows[i] = row_of(s);
+            place += __builtin_popcountll(same);
+        }
+        set = rows_here >= 64 ? ~0ull : (1ull << rows_here) - 1;
+        lds_sync();
+        if (lists && wave == 0) {
+            if (lane == 0) p.tiles[at] = int4{e < p.E ? e : -1, at * kTile, rows_here, 0};
+            if (lane < rows_here) p.order[at * kTile + lane] = rows[lane];
+        }
+    }
+    __device__ __forceinline__ int row(int r) const { return list[r]; }
+};
 // Element offset of row m of a [N, columns, L] tensor.
 __device__ __forceinline__ int64_t row_at(const AdapterP &p, const S3 &s, int m)
 {
@@ -296,7 +362,7 @@ __global__ __launch_bounds__(1024) void adapters_sort(const AdapterP p)
 // --------------------------------------------------------- x times A[e]^T --
 
 // MF, RF: sixteens of rows (gathered: one) and ranks.
-template <typename T, typename X, int MF, int RF, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void adapters_in(const AdapterP p)
+template <typename T, typename X, int MF, int RF, bool DENSE, bool FIND> __global__ __launch_bounds__(64 * kWaves) void adapters_in(const AdapterP p)
 {
     constexpr bool GATHER = MF == 1;
     __shared__ f32x4 join[kWaves][MF * RF][64];
@@ -311,7 +377,10 @@ template <typename T, typename X, int MF, int RF, bool DENSE> __global__ __launc
     const int whole = DENSE ? p.K / kUnit : 0;
     const int piece = part * kWaves + wave;
     const int u0 = (int)((int64_t)units * piece / (p.parts * kWaves)), u1 = (int)((int64_t)units * (piece + 1) / (p.parts * kWaves));
-    Group<GATHER, 16 * MF> group(p, tile, list);
+    const auto group = [&] {
+        if constexpr (FIND) return FoundGroup(p, tile, part == 0 && rank0 == 0, list);
+        else return Group<GATHER, 16 * MF>(p, tile, list);
+    }();
     const uint64_t set = group.set;
     const int64_t e = group.e;
     if (!set || e < 0 || e >= p.E) return;
@@ -702,12 +771,12 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     if (!few) {
         a.tiles = reinterpret_cast<int4 *>(static_cast<char *>(ws) + adapter_sums_bytes(p));
         a.order = reinterpret_cast<int *>(a.tiles + shape.tiles);
-        a.tile_count = a.order + p.seqs;
-        adapters_sort<<<1, 1024, 0, s>>>(a);
+        a.tile_count = a.order + (shape.find ? shape.tiles * kTile : p.seqs);
+        if (!shape.find) adapters_sort<<<1, 1024, 0, s>>>(a);
     }
     a.in_place = a.base == a.y;
     const bool f8 = p.t[LM_X].dtype == LM_F8;
-    const bool dense_in = (a.xs.c == 1 && a.as.l == 1) || p.K == 1;
+    const bool dense_in = adapter_dense_in(p);
     const bool octs = a.R % 8 == 0;
     // With strides of their own, ranks that are not eights would need a far last place.
     const bool runs = a.bs.l == 1 && (octs || (a.bs.c >= a.R && a.bs.n >= (a.N - 1) * a.bs.c + a.R && (a.N - 1) * a.bs.c + a.R >= 8));
@@ -717,18 +786,22 @@ int launch_lm_adapters(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
     const auto run = [&](auto t, auto x) {
         typedef decltype(t) T;
         typedef decltype(x) X;
-        const auto ranks = [&](auto mf, auto dense) {
+        const auto ranks = [&](auto mf, auto dense, auto find) {
             constexpr int MF = decltype(mf)::value;
-            constexpr bool D = decltype(dense)::value;
-            if (a.R <= 16) adapters_in<T, X, MF, 1, D><<<in, 64 * kWaves, 0, s>>>(a);
-            else if (a.R <= 32) adapters_in<T, X, MF, 2, D><<<in, 64 * kWaves, 0, s>>>(a);
-            else adapters_in<T, X, MF, 4, D><<<in, 64 * kWaves, 0, s>>>(a);
+            constexpr bool D = decltype(dense)::value, FIND = decltype(find)::value;
+            if (a.R <= 16) adapters_in<T, X, MF, 1, D, FIND><<<in, 64 * kWaves, 0, s>>>(a);
+            else if (a.R <= 32) adapters_in<T, X, MF, 2, D, FIND><<<in, 64 * kWaves, 0, s>>>(a);
+            else adapters_in<T, X, MF, 4, D, FIND><<<in, 64 * kWaves, 0, s>>>(a);
         };
         const auto rows = [&](auto mf) {
             constexpr int MF = decltype(mf)::value;
             if (a.E > 0) {
-                if (dense_in) ranks(mf, std::true_type());
-                else ranks(mf, std::false_type());
+                if constexpr (MF > 1) {
+                    if (shape.find) ranks(mf, std::true_type(), std::true_type());
+                    else if (dense_in) ranks(mf, std::true_type(), std::false_type());
+                    else ranks(mf, std::false_type(), std::false_type());
+                } else if (dense_in) ranks(mf, std::true_type(), std::false_type());
+                else ranks(mf, std::false_type(), std::false_type());
             }
             constexpr int MO = MF == 1 ? 1 : kOutRows, size = 64 * kWaves;
             if (!dense_out) adapters_out<T, MO, 0, false, false><<<out, size, 0, s>>>(a);

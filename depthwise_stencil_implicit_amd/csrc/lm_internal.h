@@ -111,19 +111,31 @@ inline int64_t norm_bwd_groups(const lm_plan_t &p)
 }
 
 // Adapters: rows of a workgroup (1: those of its row's adapter, gathered),
-// tiles of that many (sorted by adapter, so each may leave one short), parts of
+// tiles of that many (rows of one adapter, so each may leave one short), parts of
 // the columns of x, 256s of outputs of a workgroup, width of a row of inner sums.
 // About one workgroup of adapters_in for each compute unit (with two it took 26
 // us for 21 of 4096 rows and rank 64) and three of adapters_out (8192 rows and
 // outputs, rank 32: 70 us; with one 79, two 73, four 70).
+//
+// Up to LM_ADAPTER_FEW rows are gathered, up to LM_ADAPTER_FIND of few adapters (a
+// lane counts each, and the rows without) found by each workgroup of adapters_in,
+// others sorted in a launch before it: 8192 rows, 4096 columns and outputs, 32
+// adapters, sorted 54 us in runs and 87 in any order, found 49 and 76.  Tiles of 64
+// beat the gathered 16 where adapters have 16 rows or more and the rows are long
+// (200 rows of 8 adapters, 4096 columns and outputs: 18 us for 21; 1024: 16 for 12;
+// of 40 adapters 4096: 30 for 18).
 constexpr int LM_MAX_RANK = 256, LM_ADAPTER_N = 256, LM_ADAPTER_FEW = 512, LM_ADAPTER_TILE = 64;
-struct AdapterShape { int rows, parts, reps, width; int64_t tiles; };
+constexpr int LM_ADAPTER_FIND = 8192, LM_ADAPTER_COUNTED = 63;
+struct AdapterShape { int rows, parts, reps, width; int64_t tiles; bool find; };
+inline bool adapter_dense_in(const lm_plan_t &p) { return (p.t[LM_X].strides[1] == 1 && p.t[LM_A].strides[2] == 1) || p.K == 1; }
 inline AdapterShape adapter_shape(const lm_plan_t &p)
 {
     AdapterShape s;
-    const bool few = p.seqs <= LM_ADAPTER_FEW;
+    const bool counted = p.G > 0 && p.G <= LM_ADAPTER_COUNTED && p.seqs <= LM_ADAPTER_FIND && adapter_dense_in(p);
+    const bool few = p.seqs <= LM_ADAPTER_FEW && !(counted && p.seqs >= 16 * p.G && p.seqs * (p.K + p.C) > 1 << 20);
     s.rows = few ? 1 : LM_ADAPTER_TILE;
     s.tiles = few ? p.seqs : p.seqs / s.rows + std::min(p.seqs, p.G + 1);
+    s.find = counted && !few;
     // Workgroups with work: gathered, one for each adapter and each 16 rows.
     const int64_t groups = std::max<int64_t>(1, few ? std::min(p.seqs, p.G + p.seqs / 16) : lm_cdiv(p.seqs, s.rows));
     s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({lm_cdiv(256, groups), lm_cdiv(p.K, 256), 16}));

@@ -204,7 +204,7 @@ int plan_adapters(Checker &k, lm_plan_t &p)
     const double tiles = s.rows == 1 ? 1 : (double)s.tiles;   // gathered rows lie along the grid's second dimension
     if (!fits(tiles * s.parts * lm_cdiv(p.S, 64), 256) || !fits(2 * tiles * lm_cdiv(p.C, (int64_t)LM_ADAPTER_N * s.reps), 256))
         return k.fail(CONV_EUNSUPPORTED, "too many rows for one launch"), k.status;
-    p.workspace_bytes = adapter_sums_bytes(p) + (s.rows == 1 ? 0 : lm_cdiv(16 * s.tiles + 4 * (p.seqs + 1), 256) * 256);
+    p.workspace_bytes = adapter_sums_bytes(p) + (s.rows == 1 ? 0 : lm_cdiv(16 * s.tiles + 4 * ((s.find ? s.tiles * s.rows : p.seqs) + 1), 256) * 256);
     p.flops = 2 * p.seqs * p.S * (p.K + p.C);
     p.bytes = p.seqs * (p.K * elem(x.dtype) + p.C * e * (1 + k.has(LM_Z)) + 4 + (f8 ? 4 : 0)) + std::min(E, p.seqs) * p.S * (p.K + p.C) * e;
     return k.status;

@@ -342,6 +342,8 @@ ADAPTERS = [
     (BF, 0, 64, 64, 8, 2, "each", True, True, False, "nlc"),
     (BF, 6, 0, 64, 8, 2, "each", True, True, False, "nlc"),
     (BF, 6, 64, 64, 8, 0, "none", True, False, False, "nlc"),
+    (BF, 300, 2100, 1500, 16, 3, "mixed", True, True, False, "nlc"),
+    (HF, (2, 250), 2304, 600, 40, 31, "mixed", True, True, True, "nlc"),
     (BF, 6, 64, 64, 8, 0, "none", False, False, False, "nlc"),
     (HF, 600, 64, 66, 12, 0, "none", False, True, False, "nlc"),
     (F, 600, 64, 66, 16, 3, "none", False, True, False, "nlc"),

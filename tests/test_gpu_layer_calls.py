@@ -186,7 +186,8 @@ def test_two_streams_at_once():
 
 # ---------------------------------------------------------- any order, many --
 
-@pytest.mark.parametrize("dt,m,e,rank", [(BF, 1500, 300, 8), (HF, 520, 3, 20), (F, 1300, 1100, 6), (BF, 4000, 5, 100)])
+@pytest.mark.parametrize("dt,m,e,rank", [(BF, 1500, 300, 8), (HF, 520, 3, 20), (F, 1300, 1100, 6), (BF, 4000, 5, 100),
+                                            (BF, 2000, 63, 8), (HF, 1000, 64, 8), (F, 8192, 10, 4), (BF, 8193, 10, 4), (HF, 600, 1, 16)])
 def test_adapters_of_many_rows_in_any_order(dt, m, e, rank):
     """More adapters than one turn of the sort holds, many rows of one adapter,
     many adapters of one row: rows in any order get what each alone would."""
