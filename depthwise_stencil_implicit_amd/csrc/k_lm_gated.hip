@@ -22,6 +22,16 @@
 // the seven tensors leaves the (P, s) of chunks, and a workgroup folds those
 // behind its own.
 //
+// Measured (bf16, rows of channels; medians of traced kernels): 8 x 2048 x 4096
+// whole sequences 118 us, 4.6 TB/s of the 5.1 that a copy reaches; 1 x 65536 x
+// 2560 in tiles 366 us, 3.7 TB/s (and 7 to clear their words), where half the
+// time of a tile is the wait for its loads and for the tiles in front; its
+// gradients, 8 x 2048 x 4096, 212 to 226 us, 4.3 TB/s.
+//
+// Everything between load and store is f32; y and the gradients are rounded once.
+// A state that has overflowed (an infinity in x) may come out as NaN further on
+// where the map's P has run down to zero, h infinite: 0 times infinity.
+//
 // 1 - a^2 comes from a where a is clear of 1, and from three terms of the
 // exponential's series where 2 k sigmoid(r) < 1/16: there a has lost what the
 // difference needs.  Both are within 2^-19 at the seam.
@@ -194,7 +204,7 @@ __device__ __forceinline__ void factors(const Raw<T, V> (&x)[R], const Raw<T, V>
 
 // ---------------------------------------------------------------- forward --
 
-// Whole sequences.
+// Whole sequences: bound by memory where 256 workgroups or more run.
 template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void gated_fwd(const GatedP p)
 {
     __shared__ __attribute__((aligned(16))) float2 sums[2][kWaves][64 * V];
@@ -286,7 +296,8 @@ __global__ __launch_bounds__(256) void gated_clear(const GatedP p, int64_t words
     if (i < tickets + words) p.ahead[i] = i < tickets ? 0 : kNothing;
 }
 
-// One tile of a sequence.  Tiles of the same channels are taken by a ticket, so
+// One tile of a sequence.  Two workgroups of 64 registers share a unit, so one's
+// loads cover the other's wait.  Tiles of the same channels are taken by a ticket, so
 // those that a tile waits for have been started before it, and each leaves its
 // (P, s) before it waits itself: all waits end.
 template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWaves, 8) void gated_tile(const GatedP p)
@@ -479,7 +490,8 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
     }
 }
 
-// Tiles from the last one up.  Each starts from the saved state in front of it;
+// Bound by memory (seven tensors) and by one workgroup a unit: 121 registers of a
+// lane, which a limit of 64 spilled.  Tiles from the last one up.  Each starts from the saved state in front of it;
 // the waves' maps of h go down through LDS, those of q up.
 template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void gated_bwd(const GatedP p)
 {
@@ -630,7 +642,8 @@ __global__ __launch_bounds__(1024) void gated_ddecay(const GatedP p)
 
 // ------------------------------------------------------------------- step --
 
-// One token for each batch row, its state moved in place.
+// One token for each batch row, its state moved in place.  Latency: 64 rows of
+// 4096 channels 4.0 us, of which an empty launch is 1.7.
 template <typename T, int V> __global__ __launch_bounds__(256) void gated_step(const GatedP p, uint32_t per)
 {
     int64_t cv;

