@@ -21,7 +21,7 @@
 // two bf16 terms, f32 ones go through the f32 instruction).  y is rounded once.
 //
 // Measured (medians of traced kernels): bf16 8192 rows, 4096 columns, 8192 outputs,
-// rank 32, 6 adapters: in 26 us, 7 of them to find the rows, out 69 (3.9 TB/s of
+// rank 32, 6 adapters: in 24 us, 5 of them to find the rows, out 69 (3.9 TB/s of
 // the 5.1 that a copy reaches).  8-bit rows, 4100 x 5120 to 5120, rank 64: 21 and
 // 33.  32 tokens of 24 adapters, 4096 x 4096, rank 16: 5.5 and 7.4, a launch and
 // three waits for memory each.  What adapters_in asks for (x, and A once for each
