@@ -71,15 +71,15 @@ def prepared(kind):
         kw0 = dict(out_dtype=F8, group=64) if kind == "norm8" else dict(save=True)
         p = lm.PreparedRmsNorm(x, w, res, **kw0)
         return lambda stream=None: p.run(x, w, res, stream=stream), lm.rms_norm(x, w, residual=res, **kw0)
-    m = 700 if kind == "adapters sorted" else 30
-    x, a, b, base = rnd(g, m, 200, dtype=BF), rnd(g, 6, 24, 200, dtype=BF), rnd(g, 6, 90, 24, dtype=BF), rnd(g, m, 90, dtype=BF)
-    index = torch.randint(-1, 6, (m,), generator=g).to(torch.int32).cuda()
+    m, e = {"adapters": (30, 6), "adapters found": (700, 6), "adapters sorted": (700, 70)}[kind]
+    x, a, b, base = rnd(g, m, 200, dtype=BF), rnd(g, e, 24, 200, dtype=BF), rnd(g, e, 90, 24, dtype=BF), rnd(g, m, 90, dtype=BF)
+    index = torch.randint(-1, e, (m,), generator=g).to(torch.int32).cuda()
     p = lm.PreparedAdapters(x, a, b, index, base=base)
     assert p.plan.workspace_bytes > 0
     return lambda **kw: (p.run(x, a, b, index, base=base, **kw),), (lm.adapters(x, a, b, index, base=base),)
 
 
-@pytest.mark.parametrize("kind", ["step", "norm", "norm8", "adapters", "adapters sorted"])
+@pytest.mark.parametrize("kind", ["step", "norm", "norm8", "adapters", "adapters found", "adapters sorted"])
 def test_prepared_run_on_a_given_stream(kind):
     """On the current stream, on another one that is busy while the current one
     allocates, and on the default stream from within another."""
@@ -119,15 +119,15 @@ def test_prepared_adapters_onto_the_base():
     assert p.run(x, a, b, index, base=base, y=base) is base and torch.equal(base, want)
 
 
-@pytest.mark.parametrize("m", [40, 600])
-def test_a_layer_in_a_graph(m):
+@pytest.mark.parametrize("m,e", [(40, 3), (600, 3), (600, 70)])
+def test_a_layer_in_a_graph(m, e):
     """Norm, adapters and recurrence of a token and of a prompt in one captured
     graph, replayed with other inputs and eager work between."""
     g = gen(43)
     c, l = 96, 300
     w, decay = rnd(g, c, dtype=BF), rnd(g, c) - 4
-    a, b = rnd(g, 3, 16, c, dtype=BF), rnd(g, 3, c, 16, dtype=BF)
-    ins = [(rnd(g, m, c, dtype=BF), rnd(g, m, c, dtype=BF), torch.randint(-1, 3, (m,), generator=g).to(torch.int32).cuda(),
+    a, b = rnd(g, e, 16, c, dtype=BF), rnd(g, e, c, 16, dtype=BF)
+    ins = [(rnd(g, m, c, dtype=BF), rnd(g, m, c, dtype=BF), torch.randint(-1, e, (m,), generator=g).to(torch.int32).cuda(),
             rnd(g, 1, l, c, dtype=BF).transpose(1, 2)) for _ in range(4)]
     start = rnd(g, m, c)
 
@@ -166,12 +166,13 @@ def test_a_layer_in_a_graph(m):
     assert torch.equal(state, eager)
 
 
-def test_two_streams_at_once():
-    """Long recurrences and sorted adapters on two streams beside each other."""
+@pytest.mark.parametrize("e", [5, 80])
+def test_two_streams_at_once(e):
+    """Long recurrences and adapters of many rows on two streams beside each other."""
     g = gen(44)
     x = rnd(g, 1, 20000, 192, dtype=BF).transpose(1, 2)
-    decay, index = rnd(g, 192) - 5, torch.randint(-1, 5, (3000,), generator=g).to(torch.int32).cuda()
-    rows, a, b = rnd(g, 3000, 256, dtype=BF), rnd(g, 5, 16, 256, dtype=BF), rnd(g, 5, 300, 16, dtype=BF)
+    decay, index = rnd(g, 192) - 5, torch.randint(-1, e, (3000,), generator=g).to(torch.int32).cuda()
+    rows, a, b = rnd(g, 3000, 256, dtype=BF), rnd(g, e, 16, 256, dtype=BF), rnd(g, e, 300, 16, dtype=BF)
     want = lm.gated_recurrence(x, x, x, decay).y, lm.adapters(rows, a, b, index)
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
