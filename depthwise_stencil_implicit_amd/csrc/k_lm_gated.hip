@@ -210,6 +210,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
     __shared__ __attribute__((aligned(16))) float2 sums[2][kWaves][64 * V];
     __shared__ float carry[2][64 * V];
     constexpr int R = kFwd;
+    const int waves = blockDim.x >> 6;   // 16 where there is more than a tile
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lv = (threadIdx.x & 63) * V;
     const GatedAt at = gated_at(p, blockIdx.x);
     const uint32_t block = blockIdx.x - (uint32_t)at.part * p.blocks;
@@ -224,7 +225,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
     get_rate<V>(p, c, k2);
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = 0.f;
-    if (wave == kWaves - 1) {   // this wave carries the state from tile to tile
+    if (wave == waves - 1) {   // this wave carries the state from tile to tile
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (p.s0) h[v] = p.s0[at.seq * p.s0_n + (c + v) * p.s0_c];
@@ -264,12 +265,12 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
             for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(a[r][v], h[v], b[r][v]);
             if (p.y && tw + r < at.t1 && lane.own) put<T, V>(py.row(tw + r), h);
         }
-        if (wave == kWaves - 1) {
+        if (wave == waves - 1) {
 #pragma unroll
             for (int v = 0; v < V; ++v) carry[buf ^ 1][lv + v] = h[v];
         }
     }
-    if (wave != kWaves - 1 || !lane.own || !p.s1) return;
+    if (wave != waves - 1 || !lane.own || !p.s1) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) p.s1[at.seq * p.s1_n + (c + v) * p.s1_c] = h[v];
 }
@@ -499,6 +500,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
     __shared__ float qs[2][kWaves][64 * V];
     __shared__ float carry[2][64 * V];
     constexpr int R = kBwd;
+    const int waves = blockDim.x >> 6;   // 16 where there is more than a tile
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lv = (threadIdx.x & 63) * V;
     const GatedAt at = gated_at(p, blockIdx.x);
     const uint32_t block = blockIdx.x - (uint32_t)at.part * p.blocks;
@@ -570,7 +572,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
             }
 #pragma unroll
         for (int v = 0; v < V; ++v) q[v] = carry[buf][lv + v];
-        for (int w = kWaves - 1; w > wave; --w)
+        for (int w = waves - 1; w > wave; --w)
 #pragma unroll
             for (int v = 0; v < V; ++v) q[v] = __builtin_fmaf(hs[buf][w][lv + v].x, q[v], qs[buf][w][lv + v]);
         float before[R][V];   // h in front of each row
@@ -617,7 +619,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float sum = 0.f;
-            for (int w = 0; w < kWaves; ++w) sum += qs[0][w][lv + v];
+            for (int w = 0; w < waves; ++w) sum += qs[0][w][lv + v];
             p.part[at.part * p.C + c + v] = sum;
         }
     }
@@ -714,6 +716,13 @@ GatedP base(const lm_plan_t &p, lm_ptrs q, void *ws)
     return a;
 }
 
+// Threads of a workgroup whose waves take `rows` each: no waves without rows where
+// no sequence has a tile's (24 x 4 x 3800 f32, output and gradients: 29 us for 65).
+unsigned group_size(const GatedP &a, int rows)
+{
+    return 64 * (unsigned)(a.chunks > 1 ? kWaves : std::max<int64_t>(1, std::min<int64_t>(kWaves, lm_cdiv(a.L, rows))));
+}
+
 // f(type, channels of a thread, whether channels are contiguous).
 template <typename F> void with_type(const lm_plan_t &p, F f)
 {
@@ -748,7 +757,7 @@ int launch_lm_gated(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
             const int64_t words = 2 * a.parts * a.C;
             gated_clear<<<(unsigned)lm_cdiv(words + (int64_t)a.blocks * kTicket, 256), 256, 0, s>>>(a, words);
             gated_tile<T, V, D><<<groups, 64 * kWaves, 0, s>>>(a);
-        } else gated_fwd<T, V, D><<<groups, 64 * kWaves, 0, s>>>(a);
+        } else gated_fwd<T, V, D><<<groups, group_size(a, kFwd), 0, s>>>(a);
     });
     return lm_launch_status();
 }
@@ -763,7 +772,7 @@ int launch_lm_gated_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
             constexpr int V = decltype(v)::value;
             constexpr bool D = decltype(dense)::value;
             if (a.chunks > 1) gated_bwd_sums<T, V, D><<<groups, 64 * kWaves, 0, s>>>(a);
-            gated_bwd<T, V, D><<<groups, 64 * kWaves, 0, s>>>(a);
+            gated_bwd<T, V, D><<<groups, group_size(a, kBwd), 0, s>>>(a);
         });
     gated_ddecay<<<(unsigned)lm_cdiv(p.C, 64), 1024, 0, s>>>(a);
     return lm_launch_status();

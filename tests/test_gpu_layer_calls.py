@@ -56,6 +56,29 @@ def test_long_recurrences(dt, c, lens):
         R.assert_close(getattr(back, k), o[k], b[k], 8 * t + 384 + (t if k == "ddecay" else 0), k)
 
 
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("l", [1, 2, 4, 5, 8, 9, 33, 60, 64, 65, 120, 121, 128])
+def test_short_recurrences(dt, l):
+    """Workgroups of fewer waves, the last of them with a row or all of its rows;
+    the same tokens packed into unlike sequences."""
+    g = gen(l)
+    n, c = 3, 70
+    decay, st, gs = rnd(g, c) - 4, rnd(g, n, c), rnd(g, n, c)
+    x, r, i, gy = (rnd(g, n, l, c, dtype=dt).transpose(1, 2) for _ in range(4))
+    packed = [rnd(g, 1, l, c, dtype=dt).transpose(1, 2) for _ in range(4)]
+    off = torch.tensor([0, l // 3, l // 3, l], dtype=torch.int32, device="cuda")
+    for (x, r, i, gy), off in (((x, r, i, gy), None), (packed, off)):
+        o, b = (Y.gated(x, r, i, decay, state=st, offsets=off, bound=k) for k in (False, True))
+        go, gb = (Y.gated(x, r, i, decay, state=st, offsets=off, gy=gy, gstate=gs, bound=k) for k in (False, True))
+        steps = 24 * l + 192
+        got = lm.gated_recurrence(x, r, i, decay, state=st, offsets=off, return_state=True, save=True)
+        R.assert_close(got.y, o["y"], b["y"], steps, "y")
+        R.assert_close(got.state, o["state"], b["state"], steps, "state")
+        back = lm.gated_recurrence_backward(gy, x, r, i, decay, state=st, offsets=off, gstate=gs, saved=got.saved)
+        for k in ("dx", "dr", "di", "ddecay", "dstate"):
+            R.assert_close(getattr(back, k), go[k], gb[k], 2 * steps + (n * l if k == "ddecay" else 0), k)
+
+
 # -------------------------------------------------- prepared calls, streams --
 
 def prepared(kind):
