@@ -7,9 +7,10 @@
 // stays in registers between its sums and its results: 64, 256 or 1024 threads
 // share a row (norm_threads), each with up to 8 pieces of 8 channels, 16 bytes
 // of a 16-bit type.  y comes from the unrounded sum v, one rounding from the
-// result; the gradients start from v as it was stored, which is what a program
-// has kept (dw's error is then 0.0024 of its norm in bf16 for 0.0018 from an
-// unrounded v, which would be a third tensor to read).
+// result.  The gradients start from x and residual, whose sum they form again, or
+// from v as it was stored, which is one tensor less to read and rounds each term
+// of dw once more (16384 x 4096 bf16: dw is off by 0.0024 of its norm for 0.0017,
+// which its own rounding makes, and the call takes 107 us for 134).
 //
 // Measured (bf16, medians of traced kernels): 8192 x 5120 with residual, scales of
 // 128 channels and 8-bit output 64 us, 4.6 TB/s of the 5.1 that a copy reaches;
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_fwd(const NormP p)
 // A workgroup goes through rows and keeps its threads' part of dw in registers:
 // 1024 workgroups at most, whose parts of dw are 17 MB for 4096 channels, 3% of what
 // 16384 rows move.
-template <typename T, int TPR, int P, bool DENSE> __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_bwd(const NormP p)
+template <typename T, int TPR, int P, bool DENSE, bool RES> __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_bwd(const NormP p)
 {
     __shared__ float sh[2][16];
     __shared__ float join[TPR == 64 ? 3 * 64 * P * kPiece : 1];
@@ -237,6 +238,12 @@ template <typename T, int TPR, int P, bool DENSE> __global__ __launch_bounds__(T
         for (int i = 0; i < P; ++i) {
             const Piece<DENSE> q(p, i * TPR + tid);
             q.get(x, p.xs.c, u[i]), q.get(gy, p.gys.c, g[i]);
+            if constexpr (RES) {
+                float r[kPiece];
+                q.get(at(p.res, p.ress), p.ress.c, r);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) u[i][j] += r[j];
+            }
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -393,7 +400,10 @@ int launch_lm_norm_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
         typedef decltype(t) T;
         with_shape(p, a, [&](auto threads, auto pieces, auto dense) {
             constexpr int TPR = decltype(threads)::value, P = decltype(pieces)::value;
-            norm_bwd<T, TPR, P, decltype(dense)::value><<<(unsigned)groups, TPR == 64 ? 256 : TPR, 0, s>>>(a);
+            constexpr bool D = decltype(dense)::value;
+            const unsigned size = TPR == 64 ? 256 : TPR;
+            if (a.res) norm_bwd<T, TPR, P, D, true><<<(unsigned)groups, size, 0, s>>>(a);
+            else norm_bwd<T, TPR, P, D, false><<<(unsigned)groups, size, 0, s>>>(a);
         });
         if (q[LM_DW])
             norm_dw<T><<<(unsigned)lm_cdiv(p.C, 64), 1024, 0, s>>>(a.part, groups, p.C, static_cast<T *>(q[LM_DW]), p.t[LM_DW].strides[0]);

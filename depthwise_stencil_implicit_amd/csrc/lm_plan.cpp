@@ -36,7 +36,7 @@ uint64_t allowed(int op)
         return m({LM_X, LM_A, LM_B, LM_D, LM_OFFSETS, LM_SAVED, LM_GY, LM_GSTATE, LM_DX, LM_DA, LM_DB, LM_DD, LM_DSTATE});
     case LM_GATED_STEP: return m({LM_X, LM_A, LM_B, LM_D, LM_Y, LM_STATE_OUT, LM_ROWS});
     case LM_NORM: return m({LM_X, LM_W, LM_Y, LM_STATE_IN, LM_STATE_OUT, LM_SCALES, LM_SAVED});
-    case LM_NORM_BWD: return m({LM_X, LM_W, LM_GY, LM_GSTATE, LM_SAVED, LM_DX, LM_DW});
+    case LM_NORM_BWD: return m({LM_X, LM_W, LM_STATE_IN, LM_GY, LM_GSTATE, LM_SAVED, LM_DX, LM_DW});
     case LM_ADAPTERS: return m({LM_X, LM_A, LM_B, LM_ROWS, LM_Z, LM_D, LM_SCALES, LM_Y});
     default: return 0;
     }

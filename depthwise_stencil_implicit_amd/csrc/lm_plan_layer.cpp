@@ -125,7 +125,7 @@ int plan_norm(int op, Checker &k, const lm_args &args, lm_plan_t &p)
     if (x.rank == 3) k.want(LM_SAVED, CONV_F32, {N, p.L}, !bwd);
     else k.want(LM_SAVED, CONV_F32, {N}, !bwd);
     if (bwd) {
-        shaped(LM_GY, dt, p.C, false), shaped(LM_GSTATE, dt, p.C, true), shaped(LM_DX, dt, p.C, true);
+        shaped(LM_STATE_IN, dt, p.C, true), shaped(LM_GY, dt, p.C, false), shaped(LM_GSTATE, dt, p.C, true), shaped(LM_DX, dt, p.C, true);
         k.want(LM_DW, dt, {p.C}, true);
         if (k.status == CONV_OK && !k.has(LM_DX) && !k.has(LM_DW)) k.fail(CONV_EINVAL, "no gradient wanted");
         if (k.status == CONV_OK && k.has(LM_GSTATE) && !k.has(LM_DX)) k.fail(CONV_EINVAL, "gstate without dx");
@@ -155,7 +155,7 @@ int plan_norm(int op, Checker &k, const lm_args &args, lm_plan_t &p)
     if (!fits(all, 64) || !fits(all, (double)norm_threads(rows, p.C))) return k.fail(CONV_EUNSUPPORTED, "too many rows for one launch"), k.status;
     if (bwd && k.has(LM_DW)) p.workspace_bytes = norm_bwd_groups(p) * p.C * 4;
     const int64_t cells = rows * p.C;
-    p.bytes = bwd ? cells * e * (2 + k.has(LM_GSTATE) + k.has(LM_DX)) + rows * 4 + p.C * e * (1 + k.has(LM_DW))
+    p.bytes = bwd ? cells * e * (2 + k.has(LM_STATE_IN) + k.has(LM_GSTATE) + k.has(LM_DX)) + rows * 4 + p.C * e * (1 + k.has(LM_DW))
                   : cells * e * (k.has(LM_STATE_IN) ? 3 : 1) + cells * elem(k.t[LM_Y].dtype) + p.C * e + rows * 4 * (p.G + k.has(LM_SAVED));
     p.flops = cells * (bwd ? 10 : 6);
     return k.status;

@@ -506,14 +506,16 @@ class PreparedRmsNorm(_Step):
         return NormOut(*out)
 
 
-def rms_norm_backward(gy, x, w, rstd, *, gresidual=None, need_dx: bool = True, need_dw: bool = True) -> NormGrads:
+def rms_norm_backward(gy, x, w, rstd, *, residual=None, gresidual=None, need_dx: bool = True, need_dw: bool = True) -> NormGrads:
     """Gradients of ``rms_norm`` for gy, the gradient of a y that is not in 8
-    bits, and ``gresidual``, that of the new residual.  ``x`` is what was
-    normalised: the call's x, or with a residual the new one it returned; dx is
-    the gradient of both.  ``rstd`` comes from the call (``save=True``)."""
+    bits, and ``gresidual``, that of the new residual.  ``x`` and ``residual`` are
+    the call's own.  Where they have not been kept, ``x`` alone may be the new
+    residual that the call returned: one tensor less to read, and each term of dw
+    carries that tensor's rounding.  dx is the gradient of x and of the residual.
+    ``rstd`` comes from the call (``save=True``)."""
     dx = torch.empty_like(x) if need_dx else None
     dw = _new(w) if need_dw else None
-    _call(A.LM_NORM_BWD, [(_GY, gy), (_X, x), (_W, w), (_SAVED, rstd), (_GS, gresidual)], [(_DX, dx), (_DW, dw)])
+    _call(A.LM_NORM_BWD, [(_GY, gy), (_X, x), (_W, w), (_S0, residual), (_SAVED, rstd), (_GS, gresidual)], [(_DX, dx), (_DW, dw)])
     return NormGrads(dx, dw)
 
 

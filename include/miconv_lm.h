@@ -76,7 +76,8 @@
  *   largest |y| of the group, and what is stored is y 448 / top rounded to
  *   nearest even.  top counts as 2^-112 at least; a group of zeros has scale 1,
  *   one with a NaN has scale NaN.
- *   LM_NORM_BWD: x is v as LM_NORM rounded it.  With u = v rstd:
+ *   LM_NORM_BWD: x is v as LM_NORM rounded it or, with LM_STATE_IN, both are what
+ *   LM_NORM had and v is their sum in f32.  With u = v rstd:
  *   dx = gstate + rstd (w gy - u mean(w gy u)),  dw = sum over rows of gy u;
  *   gstate (optional) is the gradient of LM_STATE_OUT.  dx is the gradient of x
  *   and of the residual.

@@ -255,3 +255,14 @@ def test_every_call_refuses_host_memory():
                  lambda: lm.adapters(*ad), lambda: lm.PreparedAdapters(*ad)):
         with pytest.raises(ValueError, match="GPU only"):
             call()
+
+
+def test_norm_gradients_take_the_calls_residual(calls):  # noqa: F811
+    t = norm_bwd()
+    assert status(A.LM_NORM_BWD, {**t, lm._S0: e(3, 64)}, value=1e-6) == A.OK
+    for bad in (e(3, 64, d=F), e(3, 63), e(2, 64), e(3, 64, 1)):
+        assert status(A.LM_NORM_BWD, {**t, lm._S0: bad}, value=1e-6) == A.EINVAL
+    x, w, rstd = e(3, 64), e(64), e(3, d=F)
+    lm.rms_norm_backward(x, x, w, rstd, residual=e(3, 128)[:, ::2])
+    lm.rms_norm_backward(x, x, w, rstd)
+    assert [c[0].t[lm._S0].rank for c in calls] == [2, 0] and calls[0][0].t[lm._S0].strides[1] == 2
