@@ -305,7 +305,7 @@ def run(s):
     from depthwise_stencil_implicit_amd import lm
     if op == "norm_train":
         f = lm.rms_norm(s["x"], s["w"], residual=s["residual"], eps=EPS, save=True)
-        g = lm.rms_norm_backward(s["gy"], f.residual, s["w"], f.rstd, gresidual=s["gresidual"])
+        g = lm.rms_norm_backward(s["gy"], s["x"], s["w"], f.rstd, residual=s["residual"], gresidual=s["gresidual"])
         return {"y": f.y, "residual": f.residual, "dx": g.dx, "dw": g.dw}
     args = (s["x"], s["r"], s["i"], s["decay"])
     if op == "gated":
