@@ -781,7 +781,7 @@ int launch_lm_gated_bwd(const lm_plan_t &p, lm_ptrs q, void *ws, hipStream_t s)
 int launch_lm_gated_step(const lm_plan_t &p, lm_ptrs q, hipStream_t s)
 {
     const GatedP a = base(p, q, nullptr);
-    const bool two = p.C % 2 == 0;
+    const bool two = gated_step_width(p) == 2;
     const uint32_t per = (uint32_t)(two ? p.C / 2 : p.C);
     const unsigned groups = (unsigned)lm_cdiv(p.seqs * per, 256);
     if (!groups) return CONV_OK;

@@ -95,6 +95,9 @@ inline int gated_width(const lm_plan_t &p)
         if (p.t[s].rank && p.t[s].strides[1] != 1) return 1;
     return 2;
 }
+// Of a step's thread: two of any type, but one of an odd number (the state moves
+// in place, so no two threads may share a channel).
+inline int gated_step_width(const lm_plan_t &p) { return p.C % 2 ? 1 : 2; }
 
 // The norm: channels that a workgroup's registers hold, workgroups of the
 // gradients, each of which leaves one row of dw's sums.

@@ -98,7 +98,7 @@ int plan_gated(int op, Checker &k, const lm_args &args, lm_plan_t &p)
         p.workspace_bytes = gated_look(p) ? 16 * parts * p.C + 128 * lm_cdiv(p.C, 64 * gated_width(p)) : 4 * p.C * ((p.chunks > 1 ? 2 * parts : 0) + (bwd ? parts : 0));
     }
     const double groups = (double)lm_parts(p) * std::ceil((double)p.C / (64 * gated_width(p)));
-    if (!(step ? fits((double)N * p.C / gated_width(p) / 256, 256) : fits(groups, 1024) && (!gated_look(p) || fits(2 * (double)(lm_parts(p) + 16) * p.C, 1))) || !fits((double)p.C / 64, 1024) ||
+    if (!(step ? fits((double)N * p.C / gated_step_width(p) / 256, 256) : fits(groups, 1024) && (!gated_look(p) || fits(2 * (double)(lm_parts(p) + 16) * p.C, 1))) || !fits((double)p.C / 64, 1024) ||
         lm_parts(p) >= 0x7fffffff)
         return k.fail(CONV_EUNSUPPORTED, "too many rows for one launch"), k.status;
     const int64_t states = (step ? 2 : k.has(LM_STATE_IN) + k.has(LM_STATE_OUT)) + k.has(LM_GSTATE) + k.has(LM_DSTATE);

@@ -266,3 +266,20 @@ def test_norm_gradients_take_the_calls_residual(calls):  # noqa: F811
     lm.rms_norm_backward(x, x, w, rstd, residual=e(3, 128)[:, ::2])
     lm.rms_norm_backward(x, x, w, rstd)
     assert [c[0].t[lm._S0].rank for c in calls] == [2, 0] and calls[0][0].t[lm._S0].strides[1] == 2
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F])
+@pytest.mark.parametrize("n,c,fits", [(1 << 20, 8191, False), (1 << 20, 8193, False), ((1 << 20) + 1, 8192, False), ((1 << 20) - 1, 8192, True),
+                                      (1 << 19, 8191, True), (1 << 30, 3, True), (1 << 30, 5, False)])
+def test_steps_that_one_launch_holds(dtype, n, c, fits):
+    """An even number of channels takes two a thread, an odd number one, of any
+    type and memory order: fewer than 2^32 threads either way."""
+    v = lambda *s, d=dtype: torch.empty(s, dtype=d, device="meta")  # noqa: E731
+    for x in (v(n, c), v(c, n).t()):
+        t = {**{k: x for k in (lm._X, lm._A, lm._B, lm._Y)}, lm._D: v(c, d=F), lm._S1: v(n, c, d=F)}
+        if fits:
+            lm._make_plan(A.LM_GATED_STEP, t, value=1.0)
+        else:
+            with pytest.raises(lm.ConvError, match="one launch") as r:
+                lm._make_plan(A.LM_GATED_STEP, t, value=1.0)
+            assert r.value.status == A.EUNSUPPORTED
