@@ -139,8 +139,13 @@ inline AdapterShape adapter_shape(const lm_plan_t &p)
     s.rows = few ? 1 : LM_ADAPTER_TILE;
     s.tiles = few ? p.seqs : p.seqs / s.rows + std::min(p.seqs, p.G + 1);
     s.find = counted && !few;
-    // Workgroups with work: gathered, one for each adapter and each 16 rows.
-    const int64_t groups = std::max<int64_t>(1, few ? std::min(p.seqs, p.G + p.seqs / 16) : lm_cdiv(p.seqs, s.rows));
+    // Workgroups with work: gathered, one for each adapter and each 16 rows; of
+    // tiles, one for each 64 rows, or for an eighth of the adapters where those are
+    // more (4096 columns and outputs, rank 16, 1000 adapters: 513 rows 83 us for 185,
+    // 1024 rows 115 for 284).  How many of them the rows name is not known here
+    // (with 6 of the 1000 named 513 rows take 34 us for 31, 1024 rows 35 for 47).
+    const int64_t groups =
+        std::max<int64_t>(1, few ? std::min(p.seqs, p.G + p.seqs / 16) : std::max(lm_cdiv(p.seqs, s.rows), std::min(p.seqs, p.G / 8)));
     s.parts = (int)std::max<int64_t>(1, std::min<int64_t>({lm_cdiv(256, groups), lm_cdiv(p.K, 256), 16}));
     const int64_t most = p.S <= 32 ? 768 : 384;   // the more ranks, the longer what each of them does first
     const int64_t blocks = std::max<int64_t>(1, lm_cdiv(p.C, LM_ADAPTER_N)), with_work = few ? groups : 2 * groups;

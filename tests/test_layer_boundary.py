@@ -283,3 +283,14 @@ def test_steps_that_one_launch_holds(dtype, n, c, fits):
             with pytest.raises(lm.ConvError, match="one launch") as r:
                 lm._make_plan(A.LM_GATED_STEP, t, value=1.0)
             assert r.value.status == A.EUNSUPPORTED
+
+
+@pytest.mark.parametrize("m,e,parts", [(513, 1000, 4), (1024, 1000, 4), (2048, 2000, 2), (513, 6, 16), (8192, 6, 2), (8192, 1000, 2), (512, 1000, 1)])
+def test_many_adapters_count_as_workgroups(m, e, parts):
+    """Tiles of a row or two each are many workgroups: their columns are not
+    split further, as those of few tiles are, and the sums in the workspace stay few."""
+    v = lambda *s, d=BF: torch.empty(s, dtype=d, device="meta")  # noqa: E731
+    p = lm._make_plan(A.LM_ADAPTERS, {lm._X: v(m, 4096), lm._A: v(e, 16, 4096), lm._B: v(e, 4096, 16), lm._ROWS: v(m, d=I32), lm._Y: v(m, 4096)})
+    assert p.chunks <= parts and p.chunks >= parts // 2
+    tiles = m // 64 + min(m, e + 1)   # listed with a place, an adapter and 64 rows each
+    assert p.workspace_bytes <= 4 * m * parts * 32 + tiles * (16 + 64 * 4) + 1024
