@@ -24,15 +24,18 @@
 //
 // Measured (bf16, rows of channels; medians of traced kernels): 8 x 2048 x 4096
 // whole sequences 118 us, 4.6 TB/s of the 5.1 that a copy reaches; 1 x 65536 x
-// 2560 in tiles 366 us, 3.7 TB/s (and 7 to clear their words), where half the
-// time of a tile is the wait for its loads and for the tiles in front; its
-// gradients, 8 x 2048 x 4096, 212 to 226 us, 4.3 TB/s.
+// 2560 in tiles 370 us, 3.6 TB/s (and 7 to clear their words); gradients, 8 x 2048
+// x 4096, 206 to 228 us, 4.1 to 4.6 TB/s.  What the tiles of 16-bit types lose,
+// beside the wait for their loads and for the tiles in front: at 64 registers six
+// are spilled, 16 bytes of a lane written and read again (330 MB on 1311), and
+// each tile pays for the masks of the last one, 51 vector instructions an element
+// for 32 of gated_fwd.  f32 spills none and takes 565 us, 1.08 of its bytes' time.
 //
 // Everything between load and store is f32; y and the gradients are rounded once.
 // A state that has overflowed (an infinity in x) may come out as NaN further on
 // where the map's P has run down to zero, h infinite: 0 times infinity.
 //
-// 1 - a^2 comes from a where a is clear of 1, and from three terms of the
+// 1 - a^2 comes from a where a is clear of 1, and from four terms of the
 // exponential's series where 2 k sigmoid(r) < 1/16: there a has lost what the
 // difference needs.  Both are within 2^-19 at the seam.
 #include <hip/hip_runtime.h>
@@ -288,7 +291,8 @@ __device__ __forceinline__ uint64_t word_of(float a, float b)
 __device__ __forceinline__ void leave_word(uint64_t *p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ uint64_t look(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 // A wait that cannot end (offsets that do not ascend) is given up after this many
-// looks, hundreds of times what a tile takes, with NaN for a state.
+// looks, with NaN for a state: each is a load's wait, several hundred ns, so tens
+// of ms in all where a tile takes tens of us.
 constexpr int kPatience = 1 << 17;
 
 __global__ __launch_bounds__(256) void gated_clear(const GatedP p, int64_t words)
@@ -491,7 +495,7 @@ template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWave
     }
 }
 
-// Bound by memory (seven tensors) and by one workgroup a unit: 121 registers of a
+// Bound by memory (seven tensors) and by one workgroup a unit: 116 registers of a
 // lane, which a limit of 64 spilled.  Tiles from the last one up.  Each starts from the saved state in front of it;
 // the waves' maps of h go down through LDS, those of q up.
 template <typename T, int V, bool DENSE> __global__ __launch_bounds__(64 * kWaves) void gated_bwd(const GatedP p)

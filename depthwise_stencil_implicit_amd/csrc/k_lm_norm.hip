@@ -14,9 +14,12 @@
 //
 // Measured (bf16, medians of traced kernels): 8192 x 5120 with residual, scales of
 // 128 channels and 8-bit output 64 us, 4.6 TB/s of the 5.1 that a copy reaches;
-// 16384 x 4096 with residual in 16 bits 86 us (6.2 TB/s), its gradients 115 us and
-// 5.6 for dw's sum (4.8 TB/s); 32 rows of 4096 5.2 us, the time of a launch, two
-// waits for memory and two joins.
+// 16384 x 4096 with residual in 16 bits 86 us (6.2 TB/s), its gradients 143 us from
+// x and residual, 115 from the stored sum (4.7 TB/s), and 5.7 for dw's sum; 32 rows
+// of 4096 5.2 us, the time of a launch, two waits for memory and two joins.
+// Gradients of more than 8192 channels lack registers: 256 threads of 8 pieces hold
+// 410, one wave a SIMD (4096 x 12288 181 us, 1.7 TB/s), 1024 threads of 4 and 8
+// pieces spill 88 and 319 (2048 x 32768 271 us, 1.5 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -333,7 +336,8 @@ NormP base(const lm_plan_t &p, lm_ptrs q)
 
 // f(threads of a row, pieces of a thread, whether channels are contiguous): the
 // pieces that norm_threads leaves, in powers of two, or the most of them for
-// channels apart.
+// channels apart, whose gradients then spill 320 to 1100 registers (4 x 2048 x 4096
+// in the order [N, C, L]: 1.2 to 1.4 ms).
 template <typename F> void with_shape(const lm_plan_t &p, const NormP &a, F f)
 {
     bool dense = a.w_c == 1 && p.C >= kPiece;

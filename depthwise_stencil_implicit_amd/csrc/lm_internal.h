@@ -123,7 +123,11 @@ inline int64_t norm_bwd_groups(const lm_plan_t &p)
 // Up to LM_ADAPTER_FEW rows are gathered, up to LM_ADAPTER_FIND of few adapters (a
 // lane counts each, and the rows without) found by each workgroup of adapters_in,
 // others sorted in a launch before it: 8192 rows, 4096 columns and outputs, 32
-// adapters, sorted 54 us in runs and 87 in any order, found 49 and 76.  Tiles of 64
+// adapters, sorted 54 us in runs and 87 in any order, found 49 and 76.  FIND is what
+// a workgroup's registers hold of index, 32 a lane, and COUNTED what its lanes do,
+// not where the sort would win: 63 adapters in any order, found, against 64, sorted,
+// took 129 us against 152 there, but 192 against 149 with 2048 columns and outputs
+// and rank 64, where counting is more of the work.  Tiles of 64
 // beat the gathered 16 where adapters have 16 rows or more and the rows are long
 // (200 rows of 8 adapters, 4096 columns and outputs: 18 us for 21; 1024: 16 for 12;
 // of 40 adapters 4096: 30 for 18).
