@@ -336,8 +336,8 @@ NormP base(const lm_plan_t &p, lm_ptrs q)
 
 // f(threads of a row, pieces of a thread, whether channels are contiguous): the
 // pieces that norm_threads leaves, in powers of two, or the most of them for
-// channels apart, whose gradients then spill 320 to 1100 registers (4 x 2048 x 4096
-// in the order [N, C, L]: 1.2 to 1.4 ms).
+// channels apart, whose gradients then spill 320 to 1100 registers at 256 and 1024
+// threads (4 x 2048 x 4096 in the order [N, C, L]: 1.2 to 1.4 ms).
 template <typename F> void with_shape(const lm_plan_t &p, const NormP &a, F f)
 {
     bool dense = a.w_c == 1 && p.C >= kPiece;
